@@ -12,6 +12,7 @@ quantized proxy -> shared channel mask -> exact sparse SwiGLU).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -59,6 +60,24 @@ class _Taps(ctypes.Structure):
                 ("event_mode", ctypes.c_int32), ("stream_idx", ctypes.c_void_p), ("timeline", ctypes.c_void_p)]
 
 
+class _KVCache(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("head_pad", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("ctx_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p)]
+
+
+class _KVRotation(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_void_p), ("rot_rows", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("g_q", ctypes.c_void_p), ("g_k", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
 N_PHASES = 3
 PHASES = ("stage1", "stage2", "reduce_y")
 
@@ -68,7 +87,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"Prox HIP library missing: {LIB_PATH}; build it with "
                           "`python -m free_ffn_activation_prox_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "prox_abi_version": (I32, []),
         "prox_proxy_bytes": (SZ, [I32, I32, I32]),
@@ -87,6 +106,13 @@ def _load() -> ctypes.CDLL:
         "prox_build_qweights": (I32, [ctypes.POINTER(_Weights), P, SZ, ctypes.POINTER(_QWeights), P]),
         "prox_ffn_forward_q8": (I32, [P, I32, ctypes.POINTER(_QWeights), ctypes.POINTER(_Proxy), I32, I32, P, P, P,
                                       P, SZ, ctypes.POINTER(_Taps), P]),
+        "prox_kv_head_pad": (I32, [I32]),
+        "prox_kv_append": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, P, I64,
+                                 ctypes.POINTER(_KVRotation), I32, P, I64, P, I64, P]),
+        "prox_kv_workspace_bytes": (SZ, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), I32]),
+        "prox_kv_attention": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, ctypes.c_float,
+                                    I32, P, I64, P, SZ, P]),
+        "prox_kv_read": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, P, I32, P]),
         "prox_status_str": (ctypes.c_char_p, [I32]),
         "prox_last_error": (ctypes.c_char_p, []),
     }
@@ -385,5 +411,213 @@ def ffn_forward_noalloc(x, weights: Weights, proxy: Proxy, k_in: int, k_ff: int,
     return y, mask, idx[:, :k_ff]
 
 
-__all__ = ["QWeights", "build_qweights", "qweights_bytes", "quality", "timeline_forward", "read_probe", "noalloc_scratch_bytes", "ffn_forward_noalloc", "Weights", "Proxy", "ProxError", "abi_version", "library_sha256", "proxy_bytes", "workspace_bytes",
+# ---- paged 8-bit key/value cache ------------------------------------------------
+
+KV_KINDS = {"int8": 1, "fp8": 2}
+KV_PAGE = 64
+ROPE_PAIRINGS = {"interleaved": 0, "halves": 1}
+
+
+def kv_head_pad(head_dim: int) -> int:
+    """Channels a head takes in the cache (head_dim rounded up to a multiple of 64)."""
+    return _lib.prox_kv_head_pad(head_dim)
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(stream, device):
+    """(stream pointer, context) of a call on tensors of `device`: the given
+    stream, else the device's current one; the context makes the device the
+    current one where it is not."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError("stream and tensors are on different devices")
+    if device.index == torch.cuda.current_device():
+        return stream.cuda_stream, contextlib.nullcontext()
+    return stream.cuda_stream, torch.cuda.device(device)
+
+
+class KVCache:
+    """Handle of a paged 8-bit key/value cache (layout: ``include/prox.h``).
+
+    kind "int8" or "fp8" (e4m3); device tensors k, v uint8 [n_pages][n_kv]
+    [64 * kv_head_pad(head_dim)] and k_scale, v_scale fp32 [n_pages][n_kv].
+    ``KVCache.alloc`` makes an empty one."""
+
+    def __init__(self, kind: str, head_dim: int, k, v, k_scale, v_scale):
+        _need(kind in KV_KINDS, f"unknown cache kind {kind!r}")
+        hp = kv_head_pad(head_dim)
+        _need(hp > 0, "head_dim must be a multiple of 8 between 8 and 256")
+        _need(k.dim() == 3 and k.shape[2] == KV_PAGE * hp, "k must be [n_pages][n_kv][64 * kv_head_pad(head_dim)]")
+        for n, t, dt, shape in (("k", k, torch.uint8, k.shape), ("v", v, torch.uint8, k.shape),
+                                ("k_scale", k_scale, torch.float32, k.shape[:2]),
+                                ("v_scale", v_scale, torch.float32, k.shape[:2])):
+            _need(t.dtype == dt and t.is_cuda and t.is_contiguous() and t.shape == shape and t.device == k.device,
+                  f"{n}: wrong dtype, shape, layout or device")
+        self.kind, self.head_dim, self.head_pad = kind, int(head_dim), hp
+        self.n_pages, self.n_kv = int(k.shape[0]), int(k.shape[1])
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self._c = _KVCache(KV_KINDS[kind], self.n_pages, self.n_kv, self.head_dim, hp, k.data_ptr(), v.data_ptr(),
+                           k_scale.data_ptr(), v_scale.data_ptr())
+
+    @classmethod
+    def alloc(cls, kind: str, n_pages: int, n_kv: int, head_dim: int, device="cuda") -> "KVCache":
+        hp = kv_head_pad(head_dim)
+        _need(hp > 0, "head_dim must be a multiple of 8 between 8 and 256")
+        codes = [torch.zeros(n_pages, n_kv, KV_PAGE * hp, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros(n_pages, n_kv, dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(kind, head_dim, *codes, *scales)
+
+
+class KVBatch:
+    """The tokens a call works on: the last tokens of n_seq sequences.
+
+    ctx_len int32 [n_seq]: tokens of each sequence, the call's included;
+    block_table int32 [n_seq][max_pages]: pages of each sequence in order;
+    q_start int32 [n_seq + 1]: rows of the call (None: one row per sequence);
+    n_tokens: rows; max_q: the most rows of one sequence (default n_tokens).
+    The device tensors are read when the kernels run."""
+
+    def __init__(self, ctx_len, block_table, q_start=None, *, n_tokens: Optional[int] = None,
+                 max_q: Optional[int] = None):
+        n_seq = int(ctx_len.shape[0])
+        _need(block_table.dim() == 2 and block_table.shape[0] == n_seq, "block_table must be [n_seq][max_pages]")
+        _need(q_start is not None or n_tokens in (None, n_seq), "without q_start there is one token per sequence")
+        _need(q_start is None or n_tokens is not None, "n_tokens is needed with q_start")
+        for n, t, shape in (("ctx_len", ctx_len, (n_seq,)), ("block_table", block_table, tuple(block_table.shape)),
+                            ("q_start", q_start, (n_seq + 1,))):
+            if t is not None:
+                _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and tuple(t.shape) == shape
+                      and t.device == ctx_len.device, f"{n}: must be int32, contiguous, of shape {shape}, on one device")
+        self.n_seq, self.n_tokens = n_seq, n_seq if n_tokens is None else int(n_tokens)
+        self.max_q = (1 if q_start is None else self.n_tokens) if max_q is None else int(max_q)
+        self.ctx_len, self.block_table, self.q_start = ctx_len, block_table, q_start
+        self.device = ctx_len.device
+        self._c = _KVBatch(n_seq, self.n_tokens, self.max_q, int(block_table.shape[1]), ctx_len.data_ptr(),
+                           block_table.data_ptr(), 0 if q_start is None else q_start.data_ptr())
+
+
+def _kv_rows(name, t, batch, heads, hd, device):
+    """Row stride of an activation [n_tokens][heads][hd] (heads adjacent)."""
+    _need(t.dtype == torch.bfloat16 and t.is_cuda and t.device == device, f"{name} must be bf16 on the cache's device")
+    _need(t.dim() == 3 and t.shape[0] == batch.n_tokens and (heads is None or t.shape[1] == heads) and t.shape[2] == hd,
+          f"{name} must be [n_tokens][heads][head_dim]")
+    if t.shape[0] == 0:
+        return t.shape[1] * hd
+    _need(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == hd), f"{name}: the heads of a token must be adjacent")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * hd)
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k, v, *, rot=None, q=None, q_out=None, g_q=None, g_k=None,
+              eps: float = 1e-5, pairing: str = "interleaved", stream=None):
+    """Append the batch's keys and values (bf16 [n_tokens][n_kv][head_dim], rows
+    of any stride) to the cache, with the norm of each head (g_q, g_k: fp32
+    [head_dim] gains) and the rotation of q and k by position on the way.  rot:
+    cos, sin of every position and pair, complex64 [rows][rot_dim / 2] or
+    fp32 [rows][rot_dim / 2][2], rows >= 64 * max_pages.  Returns q normed and
+    rotated (bf16; q_out, which may be q, or a new tensor), None without q."""
+    dev = cache.device
+    _need(batch.device == dev, "cache and batch are on different devices")
+    _need(pairing in ROPE_PAIRINGS, f"unknown pairing {pairing!r}")
+    hd = cache.head_dim
+    ks = _kv_rows("k", k, batch, cache.n_kv, hd, dev)
+    vs = _kv_rows("v", v, batch, cache.n_kv, hd, dev)
+    r = _KVRotation(None, 0, 0, ROPE_PAIRINGS[pairing], None, None, eps)
+    if rot is not None:
+        _need(rot.is_contiguous() and rot.device == dev and (
+            rot.dtype == torch.complex64 and rot.dim() == 2
+            or rot.dtype == torch.float32 and rot.dim() == 3 and rot.shape[2] == 2),
+            "rot must be contiguous complex64 [rows][rot_dim / 2] or fp32 [rows][rot_dim / 2][2]")
+        r.rot, r.rot_rows, r.rot_dim = rot.data_ptr(), rot.shape[0], 2 * rot.shape[1]
+    for n, g in (("g_q", g_q), ("g_k", g_k)):
+        if g is not None:
+            _need(g.dtype == torch.float32 and g.device == dev and g.is_contiguous() and tuple(g.shape) == (hd,),
+                  f"{n} must be fp32 [head_dim]")
+            setattr(r, n, g.data_ptr())
+    n_heads, qp, qs, qop, qos = cache.n_kv, None, 0, None, 0
+    if q is not None:
+        n_heads = q.shape[1]
+        qs = _kv_rows("q", q, batch, None, hd, dev)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        qos = _kv_rows("q_out", q_out, batch, n_heads, hd, dev)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    else:
+        _need(q_out is None, "q_out without q")
+    sp, ctx = _on(stream, dev)
+    with ctx:
+        _check(_lib.prox_kv_append(ctypes.byref(cache._c), ctypes.byref(batch._c), k.data_ptr(), ks, v.data_ptr(), vs,
+                                   ctypes.byref(r), n_heads, qp, qs, qop, qos, sp), "prox_kv_append")
+    return q_out
+
+
+def kv_workspace_bytes(cache: KVCache, batch: KVBatch, n_heads: int) -> int:
+    return _lib.prox_kv_workspace_bytes(ctypes.byref(cache._c), ctypes.byref(batch._c), n_heads)
+
+
+def alloc_kv_workspace(cache: KVCache, batch: KVBatch, n_heads: int):
+    """Workspace of kv_attention for batches of this shape (n_seq, max_q, max_pages)."""
+    with torch.cuda.device(cache.device):
+        n = kv_workspace_bytes(cache, batch, n_heads)
+    if n == 0:
+        raise ValueError("invalid cache, batch or n_heads for a workspace")
+    raw = torch.empty(n + 256, dtype=torch.uint8, device=cache.device)
+    off = (-raw.data_ptr()) % 256
+    return raw[off: off + n]
+
+
+def kv_attention(q, cache: KVCache, batch: KVBatch, *, scale: Optional[float] = None, window: int = 0, out=None,
+                 workspace=None, stream=None):
+    """Causal attention of q (bf16 [n_tokens][n_heads][head_dim], rows of any
+    stride, as kv_append returns it) over the cache; scale defaults to
+    1 / sqrt(head_dim), window > 0 limits a row to its last `window` positions.
+    Returns out, bf16 [n_tokens][n_heads][head_dim]; rows that see nothing are
+    zeros, rows outside every sequence are left as they were."""
+    dev, hd = cache.device, cache.head_dim
+    _need(batch.device == dev, "cache and batch are on different devices")
+    qs = _kv_rows("q", q, batch, None, hd, dev)
+    n_heads = q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    os_ = _kv_rows("out", out, batch, n_heads, hd, dev)
+    if workspace is None:
+        workspace = alloc_kv_workspace(cache, batch, n_heads)
+    _need(workspace.is_cuda and workspace.device == dev and workspace.is_contiguous(),
+          "workspace must be contiguous on the cache's device")
+    sp, ctx = _on(stream, dev)
+    with ctx:
+        _check(_lib.prox_kv_attention(ctypes.byref(cache._c), ctypes.byref(batch._c), q.data_ptr(), qs, n_heads,
+                                      hd ** -0.5 if scale is None else scale, window, out.data_ptr(), os_,
+                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(), sp),
+               "prox_kv_attention")
+    return out
+
+
+def kv_read(cache: KVCache, batch: KVBatch, *, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """The batch's tokens back from the cache: (k, v), each [n_tokens][n_kv]
+    [head_dim] in bf16 or fp32, the values that the codes stand for."""
+    dev = cache.device
+    _need(batch.device == dev, "cache and batch are on different devices")
+    _need(dtype in (torch.bfloat16, torch.float32), "dtype must be bfloat16 or float32")
+    shape = (batch.n_tokens, cache.n_kv, cache.head_dim)
+    k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
+    for n, t in (("k_out", k_out), ("v_out", v_out)):
+        _need(t.dtype == dtype and t.device == dev and t.is_contiguous() and tuple(t.shape) == shape,
+              f"{n}: wrong dtype, shape, layout or device")
+    sp, ctx = _on(stream, dev)
+    with ctx:
+        _check(_lib.prox_kv_read(ctypes.byref(cache._c), ctypes.byref(batch._c), k_out.data_ptr(), v_out.data_ptr(),
+                                 1 if dtype == torch.float32 else 0, sp), "prox_kv_read")
+    return k_out, v_out
+
+
+__all__ = ["KVCache", "KVBatch", "KV_KINDS", "KV_PAGE", "kv_head_pad", "kv_append", "kv_attention", "kv_read",
+           "kv_workspace_bytes", "alloc_kv_workspace",
+           "QWeights", "build_qweights", "qweights_bytes", "quality", "timeline_forward", "read_probe", "noalloc_scratch_bytes", "ffn_forward_noalloc", "Weights", "Proxy", "ProxError", "abi_version", "library_sha256", "proxy_bytes", "workspace_bytes",
            "build_proxy", "alloc_workspace", "ffn_forward", "LIB_PATH", "KINDS", "N_PHASES", "PHASES"]

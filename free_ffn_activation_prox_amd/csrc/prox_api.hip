@@ -13,8 +13,12 @@
 using namespace prox;
 
 namespace {
-
 thread_local std::string g_err;
+}
+
+namespace prox {
+
+void clear_error() { g_err.clear(); }
 
 prox_status fail(prox_status st, const char* fmt, ...) {
     char buf[512];
@@ -29,6 +33,23 @@ prox_status fail(prox_status st, const char* fmt, ...) {
 prox_status hip_fail(hipError_t e, const char* where) {
     return fail(PROX_E_HIP, "%s: %s", where, hipGetErrorString(e));
 }
+
+// Compute units of the current device (cached per device id).
+int device_cus() {
+    static int cache[64] = {0};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    if (cache[dev] == 0) {
+        int n = 0;
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+        cache[dev] = n;
+    }
+    return cache[dev];
+}
+
+}  // namespace prox
+
+namespace {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -82,19 +103,6 @@ ProxyView view_of(const prox_proxy* p) {
     v.codes = static_cast<const uint8_t*>(p->buf);
     v.scales = reinterpret_cast<const float*>(static_cast<const uint8_t*>(p->buf) + p->scale_offset);
     return v;
-}
-
-// Compute units of the current device (cached per device id).
-int device_cus() {
-    static int cache[64] = {0};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-        cache[dev] = n;
-    }
-    return cache[dev];
 }
 
 // A tag per call for the Stage-1 arrival counters: counters left by any

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "prox.h"
+
 namespace prox {
 
 constexpr int kInt4Group = 128;
@@ -192,5 +194,23 @@ hipError_t launch_proxy_batch(const uint16_t* xm, int B, int d, const ProxyView&
 hipError_t launch_stage2_batch(const uint16_t* x, const uint16_t* wg_t, const uint16_t* wu_t,
                                const uint16_t* wd, const uint8_t* mask, uint16_t* hb, int B, int d,
                                int F, int f_pad, float* ypart, int* ks_out, hipStream_t s);
+
+// ---- errors of the calling host thread and device properties (prox_api.hip)
+void clear_error();
+prox_status fail(prox_status st, const char* fmt, ...);
+prox_status hip_fail(hipError_t e, const char* where);
+int device_cus();
+
+// ---- paged 8-bit key/value cache (prox_kv.hip, prox_kv_attn.hip)
+hipError_t launch_kv_append(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* k, int64_t k_stride,
+                            const uint16_t* v, int64_t v_stride, const prox_kv_rotation& r, int n_heads,
+                            const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t q_out_stride,
+                            hipStream_t s);
+hipError_t launch_kv_read(const prox_kv_cache& c, const prox_kv_batch& b, void* k_out, void* v_out, bool fp32,
+                          hipStream_t s);
+size_t kv_attention_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads);
+hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride,
+                               int n_heads, float scale, int window, uint16_t* out, int64_t out_stride,
+                               void* workspace, hipStream_t s);
 
 }  // namespace prox

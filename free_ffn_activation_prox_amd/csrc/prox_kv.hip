@@ -1,0 +1,396 @@
+// Paged 8-bit key/value cache: appending tokens and reading them back.
+//
+// Append, for a token at position p and a head x of k (q the same, to bf16):
+//   y = x / sqrt(mean(x^2) + eps) * g         (optional)
+//   (a, b) -> (a cos_p - b sin_p, a sin_p + b cos_p) for the pairs of channels
+//   r = fp32(y),  scale = max(old scale, fp32(max|r| / qmax)),  code = r / scale
+// The norm and the rotation run in fp64 (bf16 x fp32 products are exact there),
+// rounded once, so that a code does not depend on how a kernel orders its sums:
+// one code of an 8-bit cache is up to 2^-4 of a value, far more than the
+// rounding that would flip it.  The work is a few operations a byte moved; what
+// bounds the call is reading q, k, v once and, for one token, the latency of
+// the launch.
+#include "prox_kv.hpp"
+
+namespace prox {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct RotArgs {
+    const float2* rot;
+    int half;            // rot_dim / 2 (0: no rotation)
+    int halves;          // pairing
+    double eps;
+};
+
+// Channels c .. c + 7 of one head (TPT neighbouring lanes hold the head; lanes
+// with c >= hd take part with zeros), normed by `gain` (nullable) and rotated
+// with the table row `rot`.
+template <int TPT>
+__device__ __forceinline__ void head8(const uint16_t* __restrict__ x, int c, int hd, const float* __restrict__ gain,
+                                      const float2* __restrict__ rot, const RotArgs& a, float out[8]) {
+    const bool in = c < hd;
+    const bool turn = in && c < 2 * a.half;
+    double v[8], w[8];
+    auto load = [&](int ch, double o[8]) {
+        const uint4 u = *reinterpret_cast<const uint4*>(x + ch);
+        const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            o[2 * e] = (double)bf16_lo(d[e]);
+            o[2 * e + 1] = (double)bf16_hi(d[e]);
+        }
+    };
+    const bool lower = c < a.half;
+    const int pc = lower ? c + a.half : c - a.half;      // the other channel of each pair (halves)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.0;
+    if (in) load(c, v);
+    if (a.halves && turn) load(pc, w);
+    if (gain) {
+        double ss = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fma(v[e], v[e], ss);
+#pragma unroll
+        for (int m = 1; m < TPT; m *= 2) ss += __shfl_xor(ss, m);
+        const double inv = 1.0 / sqrt(ss / (double)hd + a.eps);
+        if (in) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * (double)gain[c + e];
+        }
+        if (a.halves && turn) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = w[e] * inv * (double)gain[pc + e];
+        }
+    }
+    if (!turn) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = (float)v[e];
+    } else if (a.halves) {
+        const float2* cs = rot + (lower ? c : pc);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float2 t = cs[e];
+            out[e] = (float)(lower ? fma(-w[e], (double)t.y, v[e] * (double)t.x)
+                                   : fma(w[e], (double)t.y, v[e] * (double)t.x));
+        }
+    } else {
+        const float2* cs = rot + c / 2;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const double p = v[2 * e], q = v[2 * e + 1];
+            if (c + 2 * e < 2 * a.half) {
+                const float2 t = cs[e];
+                out[2 * e] = (float)fma(-q, (double)t.y, p * (double)t.x);
+                out[2 * e + 1] = (float)fma(p, (double)t.y, q * (double)t.x);
+            } else {
+                out[2 * e] = (float)p;
+                out[2 * e + 1] = (float)q;
+            }
+        }
+    }
+}
+
+struct Append {
+    prox_kv_cache c;
+    prox_kv_batch b;
+    const uint16_t *k, *v, *q;
+    uint16_t* q_out;
+    int64_t ks, vs, qs, qos;
+    const float *g_q, *g_k;
+    RotArgs rot;
+    int H, pp;            // query heads; pages that one sequence's tokens can touch
+    int kv_blocks;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    b2 r;
+    r[0] = (__bf16)lo;
+    r[1] = (__bf16)hi;
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// One side (K or V) of one page and head: slots s0 .. s1 - 1 come from rows
+// row0 + (slot - s0).  Block of 256 threads; every thread passes the barriers.
+//   few new slots, scale kept: the new codes are stored where they belong;
+//   else the page is put together in LDS -- what it held (requantised where the
+//   scale grew), cleared where it begins anew -- and stored whole.
+template <int KIND, int TPT, bool VAL>
+__device__ void append_side(const Append& A, uint8_t* image, float* red, int page, int head, int s0, int s1,
+                            int row0, int pos0) {
+    constexpr int RPP = kThreads / TPT;          // slots of one pass over the threads
+    constexpr int NP = kKvPage / RPP;
+    constexpr int kDirect = 8;                   // at most so many slots are stored on their own
+    const int t = threadIdx.x, c = (t % TPT) * 8, hd = A.c.head_dim, hp = A.c.head_pad;
+    const size_t at = (size_t)page * A.c.n_kv + head;
+    uint8_t* codes = static_cast<uint8_t*>(VAL ? A.c.v : A.c.k) + at * (size_t)(kKvPage * hp);
+    float* scale = (VAL ? A.c.v_scale : A.c.k_scale) + at;
+    const bool fresh = s0 == 0;
+    const float old = fresh ? 0.f : *scale;
+
+    float r[NP][8];
+    float most = 0.f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        if ((p + 1) * RPP <= s0 || p * RPP >= s1) continue;           // uniform
+        const int slot = p * RPP + t / TPT;
+        const bool live = slot >= s0 && slot < s1;
+        const int row = row0 + (live ? slot - s0 : 0);
+        if constexpr (VAL) {
+            const uint16_t* x = A.v + (int64_t)row * A.vs + (int64_t)head * hd;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (c < hd) u = *reinterpret_cast<const uint4*>(x + c);
+            const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                r[p][2 * e] = bf16_lo(d[e]);
+                r[p][2 * e + 1] = bf16_hi(d[e]);
+            }
+        } else {
+            const uint16_t* x = A.k + (int64_t)row * A.ks + (int64_t)head * hd;
+            const int pos = pos0 + (live ? slot - s0 : 0);
+            head8<TPT>(x, c, hd, A.g_k, A.rot.rot + (int64_t)pos * A.rot.half, A.rot, r[p]);
+        }
+        if (live) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float m = fabsf(r[p][e]);
+                if (m < INFINITY) most = fmaxf(most, m);              // false for NaN too
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) most = fmaxf(most, __shfl_xor(most, m));
+    __syncthreads();                             // red and image: the previous side is done with them
+    if ((t & 63) == 0) red[t >> 6] = most;
+    __syncthreads();
+    most = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float sc = fmaxf(old, most / kv_qmax<KIND>());
+    const bool grown = sc > old && old > 0.f;
+    const bool whole = fresh || grown || s1 - s0 > kDirect;
+    if (t == 0 && sc != old) *scale = sc;
+    if (t == 0 && fresh) *scale = sc;
+    const float unit = sc > 0.f ? sc : 1.f;
+
+    if (whole) {
+        for (int i = t; i < kKvPage * hp / 16; i += kThreads) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (!fresh) u = reinterpret_cast<const uint4*>(codes)[i];
+            if (grown) {
+                uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x[4];
+                    kv_values4<KIND>(d[e], x);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) x[f] = x[f] * old / unit;
+                    d[e] = kv_codes4<KIND>(x);
+                }
+                u = make_uint4(d[0], d[1], d[2], d[3]);
+            }
+            reinterpret_cast<uint4*>(image)[i] = u;
+        }
+        __syncthreads();
+    }
+    uint8_t* to = whole ? image : codes;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        if ((p + 1) * RPP <= s0 || p * RPP >= s1) continue;
+        const int slot = p * RPP + t / TPT;
+        if (slot < s0 || slot >= s1 || c >= hd) continue;
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = sc > 0.f ? r[p][4 * h + e] / unit : 0.f;
+            w[h] = kv_codes4<KIND>(x);
+        }
+        if constexpr (VAL) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) to[kv_v_index(slot, c + e)] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+        } else {
+            *reinterpret_cast<uint2*>(to + kv_k_index(slot, c)) = make_uint2(w[0], w[1]);
+        }
+    }
+    if (whole) {
+        __syncthreads();
+        for (int i = t; i < kKvPage * hp / 16; i += kThreads)
+            reinterpret_cast<uint4*>(codes)[i] = reinterpret_cast<const uint4*>(image)[i];
+    }
+}
+
+// grid: first one block per (sequence, page that its tokens can touch, head),
+// then blocks of 256 / TPT (row, query head) pairs.
+template <int KIND, int TPT>
+__global__ void __launch_bounds__(kThreads) k_kv_append(Append A) {
+    __shared__ __align__(16) uint8_t image[kKvPage * 8 * TPT];
+    __shared__ float red[4];
+    const int t = threadIdx.x;
+    if ((int)blockIdx.x < A.kv_blocks) {
+        const int head = blockIdx.x % A.c.n_kv;
+        const int rest = blockIdx.x / A.c.n_kv;
+        const int s = rest / A.pp, j = rest % A.pp;
+        const KvRows R = kv_rows(A.b, s);
+        if (R.rows <= 0 || R.first + R.rows <= 0) return;
+        const int lo = max(R.first, 0);
+        const int hi = min((int64_t)R.first + R.rows, (int64_t)A.b.max_pages * kKvPage);   // positions lo .. hi - 1
+        const int pg = lo / kKvPage + j;
+        const int a = max(lo, pg * kKvPage), b = min(hi, (pg + 1) * kKvPage);
+        if (a >= b) return;
+        const int page = A.b.block_table[(size_t)s * A.b.max_pages + pg];
+        if (page < 0 || page >= A.c.n_pages) return;
+        const int s0 = a - pg * kKvPage, s1 = b - pg * kKvPage, row0 = R.q0 + (a - R.first);
+        append_side<KIND, TPT, false>(A, image, red, page, head, s0, s1, row0, a);
+        append_side<KIND, TPT, true>(A, image, red, page, head, s0, s1, row0, a);
+        return;
+    }
+    constexpr int RPP = kThreads / TPT;
+    const int64_t id = (int64_t)((int)blockIdx.x - A.kv_blocks) * RPP + t / TPT;
+    const int64_t row64 = id / A.H;
+    if (row64 >= A.b.n_tokens) return;                       // a head's lanes leave together
+    const int row = (int)row64, h = (int)(id % A.H), c = (t % TPT) * 8, hd = A.c.head_dim;
+    const int s = kv_seq_of(A.b, row);
+    const KvRows R = kv_rows(A.b, s);
+    const int i = row - R.q0;
+    if (i < 0 || i >= R.rows) return;
+    const int pos = R.first + i;
+    const bool seen = pos >= 0 && pos < A.b.max_pages * kKvPage;
+    float o[8];
+    head8<TPT>(A.q + (int64_t)row * A.qs + (int64_t)h * hd, c, hd, A.g_q,
+               A.rot.rot + (int64_t)(seen ? pos : 0) * A.rot.half, A.rot, o);
+    if (c >= hd) return;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (seen) u = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+    *reinterpret_cast<uint4*>(A.q_out + (int64_t)row * A.qos + (int64_t)h * hd + c) = u;
+}
+
+struct Read {
+    prox_kv_cache c;
+    prox_kv_batch b;
+    void *k, *v;
+};
+
+// One thread: eight channels of one (row, head), K and V.
+template <int KIND, bool FP32>
+__global__ void __launch_bounds__(kThreads) k_kv_read(Read A) {
+    const int hd = A.c.head_dim, hp = A.c.head_pad, n8 = hd / 8;
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t row64 = id / (A.c.n_kv * n8);
+    if (row64 >= A.b.n_tokens) return;
+    const int row = (int)row64, rest = (int)(id % (A.c.n_kv * n8)), head = rest / n8, c = rest % n8 * 8;
+    const int s = kv_seq_of(A.b, row);
+    const KvRows R = kv_rows(A.b, s);
+    const int i = row - R.q0;
+    if (i < 0 || i >= R.rows) return;
+    const int pos = R.first + i;
+    int page = -1;
+    if (pos >= 0 && pos < A.b.max_pages * kKvPage) page = A.b.block_table[(size_t)s * A.b.max_pages + pos / kKvPage];
+    float k[8] = {}, v[8] = {};
+    if (page >= 0 && page < A.c.n_pages) {
+        const size_t at = (size_t)page * A.c.n_kv + head;
+        const uint8_t* kc = static_cast<const uint8_t*>(A.c.k) + at * (size_t)(kKvPage * hp);
+        const uint8_t* vc = static_cast<const uint8_t*>(A.c.v) + at * (size_t)(kKvPage * hp);
+        const float ks = A.c.k_scale[at], vs = A.c.v_scale[at];
+        const int slot = pos % kKvPage;
+        const uint2 w = *reinterpret_cast<const uint2*>(kc + kv_k_index(slot, c));
+        uint32_t x[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e >> 2] |= (uint32_t)vc[kv_v_index(slot, c + e)] << (8 * (e & 3));
+        kv_values4<KIND>(w.x, k);
+        kv_values4<KIND>(w.y, k + 4);
+        kv_values4<KIND>(x[0], v);
+        kv_values4<KIND>(x[1], v + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            k[e] *= ks;
+            v[e] *= vs;
+        }
+    }
+    const int64_t o = ((int64_t)row * A.c.n_kv + head) * hd + c;
+    auto store = [&](void* out, const float* x) {
+        if constexpr (FP32) {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+            p[0] = make_float4(x[0], x[1], x[2], x[3]);
+            p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) =
+                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        }
+    };
+    store(A.k, k);
+    store(A.v, v);
+}
+
+template <int KIND>
+hipError_t append_kind(const Append& A, int64_t blocks, hipStream_t s) {
+    const dim3 g((uint32_t)blocks), t(kThreads);
+    if (A.c.head_pad <= 64) hipLaunchKernelGGL((k_kv_append<KIND, 8>), g, t, 0, s, A);
+    else if (A.c.head_pad <= 128) hipLaunchKernelGGL((k_kv_append<KIND, 16>), g, t, 0, s, A);
+    else hipLaunchKernelGGL((k_kv_append<KIND, 32>), g, t, 0, s, A);
+    return hipGetLastError();
+}
+
+int lanes_per_head(int hp) { return hp <= 64 ? 8 : hp <= 128 ? 16 : 32; }
+
+}  // namespace
+
+// Pages that the tokens of one sequence can touch: max_q neighbouring
+// positions, the first anywhere in a page.
+static int pages_touched(const prox_kv_batch& b) {
+    const int64_t n = ((int64_t)b.max_q + 2 * kKvPage - 2) / kKvPage;
+    return (int)(n < b.max_pages ? n : b.max_pages);
+}
+
+hipError_t launch_kv_append(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* k, int64_t k_stride,
+                            const uint16_t* v, int64_t v_stride, const prox_kv_rotation& r, int n_heads,
+                            const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t q_out_stride,
+                            hipStream_t s) {
+    Append A{};
+    A.c = c;
+    A.b = b;
+    A.k = k;
+    A.v = v;
+    A.q = q;
+    A.q_out = q_out;
+    A.ks = k_stride;
+    A.vs = v_stride;
+    A.qs = q_stride;
+    A.qos = q_out_stride;
+    A.g_q = r.g_q;
+    A.g_k = r.g_k;
+    A.rot.rot = reinterpret_cast<const float2*>(r.rot);
+    A.rot.half = r.rot ? r.rot_dim / 2 : 0;
+    A.rot.halves = r.pairing == PROX_ROPE_HALVES;
+    A.rot.eps = (double)r.eps;
+    A.H = q ? n_heads : 1;
+    A.pp = pages_touched(b);
+    const int64_t kvb = (int64_t)b.n_seq * A.pp * c.n_kv;
+    const int rpp = kThreads / lanes_per_head(c.head_pad);
+    const int64_t qb = q ? ((int64_t)b.n_tokens * n_heads + rpp - 1) / rpp : 0;
+    if (kvb + qb > 0x7fffffffll) return hipErrorInvalidConfiguration;
+    A.kv_blocks = (int)kvb;
+    return c.kind == PROX_KV_INT8 ? append_kind<PROX_KV_INT8>(A, kvb + qb, s)
+                                  : append_kind<PROX_KV_FP8>(A, kvb + qb, s);
+}
+
+hipError_t launch_kv_read(const prox_kv_cache& c, const prox_kv_batch& b, void* k_out, void* v_out, bool fp32,
+                          hipStream_t s) {
+    const Read A{c, b, k_out, v_out};
+    const int64_t blocks = ((int64_t)b.n_tokens * c.n_kv * (c.head_dim / 8) + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffll) return hipErrorInvalidConfiguration;
+    const dim3 g((uint32_t)blocks), t(kThreads);
+    if (c.kind == PROX_KV_INT8) {
+        if (fp32) hipLaunchKernelGGL((k_kv_read<PROX_KV_INT8, true>), g, t, 0, s, A);
+        else hipLaunchKernelGGL((k_kv_read<PROX_KV_INT8, false>), g, t, 0, s, A);
+    } else {
+        if (fp32) hipLaunchKernelGGL((k_kv_read<PROX_KV_FP8, true>), g, t, 0, s, A);
+        else hipLaunchKernelGGL((k_kv_read<PROX_KV_FP8, false>), g, t, 0, s, A);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace prox

@@ -286,6 +286,133 @@ prox_status prox_quality(const uint8_t* mask_a, const uint8_t* mask_b, int32_t b
                          const float* y, const float* y_ref, int32_t d_model, int32_t* overlap,
                          double* err, void* stream);
 
+/* ---- Paged 8-bit key/value cache ---------------------------------------------
+ * The attention next to the FFN in a decode step: a cache of keys and values
+ * in pages of PROX_KV_PAGE tokens, 8 bits a value, with one fp32 scale for
+ * every (page, head) of the keys and one of the values; the operator that
+ * writes it (norms and rotation on the way) and the two that read it.
+ *
+ * Kinds: PROX_KV_INT8 codes in [-127, 127], qmax = 127; PROX_KV_FP8 e4m3 codes
+ * (OCP, largest 448), qmax = 448.  scale = fp32(max|r| / qmax) over the finite
+ * values r; code = r / scale (one fp32 rounding), clamped to +-qmax, rounded
+ * half-even to a code (the proxies' rule above).  Infinities are stored as
+ * +-qmax codes, NaN as 0; a page of zeros has scale 0 and codes 0.
+ *
+ * A sequence's position p lies in page block_table[p / 64], slot p % 64.  A
+ * page's codes of one head, hp = head_pad channels (head_dim rounded up to a
+ * multiple of 64; the padding channels hold 0), are stored in the order in
+ * which the matrix cores take them:
+ *   k  [hp / 64][4][4][16][16]  indexes a b c d e: slot 16 b + d, channel 64 a + 16 c + e
+ *   v  [hp / 16][4][16][4][4]   indexes a b c d e: slot 16 d + 4 b + e, channel 16 a + c */
+#define PROX_KV_PAGE 64
+#define PROX_KV_MAX_HEAD_DIM 256
+#define PROX_KV_MAX_HEADS 1024
+
+typedef enum {
+    PROX_KV_INT8 = 1,
+    PROX_KV_FP8 = 2
+} prox_kv_kind;
+
+/* Descriptor of a cache (host struct; the caller owns the device buffers).
+ * 8 <= head_dim <= 256, head_dim % 8 == 0; 1 <= n_kv <= 1024;
+ * head_pad = prox_kv_head_pad(head_dim).  k, v 16-byte aligned. */
+typedef struct {
+    int32_t kind;
+    int32_t n_pages;
+    int32_t n_kv;
+    int32_t head_dim;
+    int32_t head_pad;
+    void* k;          /* codes [n_pages][n_kv][64 * head_pad] */
+    void* v;          /* codes [n_pages][n_kv][64 * head_pad] */
+    float* k_scale;   /* [n_pages][n_kv] */
+    float* v_scale;   /* [n_pages][n_kv] */
+} prox_kv_cache;
+
+/* The tokens one call works on: the last tokens of n_seq sequences (host
+ * struct, device arrays).  Sequence s has ctx_len[s] tokens, the call's own
+ * included; the call's rows q_start[s] .. q_start[s + 1] - 1 are its last ones,
+ * so row i of n has position ctx_len[s] - n + i.  q_start null: one token per
+ * sequence (n_tokens == n_seq).  max_q: the most rows of one sequence; rows
+ * beyond it are not worked on.  Rows outside every sequence are not touched.
+ * The device arrays are read when the kernels run, so a captured call follows
+ * them.  Nothing that they hold makes a call read or write out of bounds:
+ *   - a row whose position is negative or not below 64 * max_pages is written
+ *     as zeros, and its key and value are not stored;
+ *   - a table entry outside [0, n_pages) names no page: its keys and values
+ *     are neither stored nor seen. */
+typedef struct {
+    int32_t n_seq;
+    int32_t n_tokens;
+    int32_t max_q;
+    int32_t max_pages;             /* entries of one table row; 64 * max_pages < 2^31 */
+    const int32_t* ctx_len;        /* [n_seq] */
+    const int32_t* block_table;    /* [n_seq][max_pages] */
+    const int32_t* q_start;        /* [n_seq + 1] or null */
+} prox_kv_batch;
+
+/* Rotation of a token's q and k heads by its position, and their norms. */
+#define PROX_ROPE_INTERLEAVED 0   /* pairs (2i, 2i + 1) */
+#define PROX_ROPE_HALVES 1        /* pairs (i, i + rot_dim / 2); rot_dim % 16 == 0 */
+typedef struct {
+    const float* rot;   /* [rot_rows][rot_dim / 2][2]: cos, sin of each position's pairs; null: no rotation */
+    int32_t rot_rows;   /* >= 64 * max_pages */
+    int32_t rot_dim;    /* rotated channels, even, <= head_dim; the others pass */
+    int32_t pairing;
+    const float* g_q;   /* [head_dim] gain of the norm of q's heads; null: q is not normed */
+    const float* g_k;   /* [head_dim] gain of the norm of k's heads; null: k is not normed */
+    float eps;
+} prox_kv_rotation;
+
+/* head_dim rounded up to the stored channels; 0 if out of range. */
+int32_t prox_kv_head_pad(int32_t head_dim);
+
+/* Append the batch's keys and values to the cache.  For every token and head
+ *   norm    x_i / sqrt(mean(x^2) + eps) * g_i          (where a gain is given)
+ *   rotate  (a, b) -> (a cos - b sin, a sin + b cos)   (where a table is given)
+ * in fp64, rounded once to fp32; k and v (taken as they are) then go into the
+ * cache, q (nullable) to q_out as bf16.
+ *   q, k, v  device bf16 [n_tokens][heads][head_dim], the heads of a token
+ *            adjacent, rows *_stride elements apart (% 8 == 0, >= heads *
+ *            head_dim), 16-byte aligned
+ *   q_out    device bf16, rows q_out_stride elements apart; q itself for a
+ *            call in place (with the same stride)
+ * A page whose slot 0 the call writes begins anew: its scale comes from the
+ * call's tokens alone and its other slots are cleared.  A page that the call
+ * goes on with keeps its scale unless a new value needs a larger one; then the
+ * codes it holds are rounded once more, to the larger scale.  A page that is
+ * written belongs to one sequence of the batch (pages that are only read may be
+ * shared).  Rounding depends on which tokens share a call, never on timing. */
+prox_status prox_kv_append(const prox_kv_cache* c, const prox_kv_batch* b, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const prox_kv_rotation* r, int32_t n_heads,
+                           const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, void* stream);
+
+/* Workspace bytes prox_kv_attention needs for this cache, batch and query
+ * heads; 0 if the arguments are invalid. */
+size_t prox_kv_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, int32_t n_heads);
+
+/* Attention of the batch's tokens over the cache: for query head h of the row
+ * at position p, with the stored keys and values of head h / (n_heads / n_kv),
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * over the visible positions j: j <= p, and j > p - window where window > 0.
+ * A row that sees nothing is written as zeros.
+ *   q, out   device bf16 [n_tokens][n_heads][head_dim], rows *_stride elements
+ *            apart (% 8 == 0), 16-byte aligned; n_heads a multiple of n_kv
+ *   workspace  device, >= prox_kv_workspace_bytes(), 256-byte aligned, scratch
+ *            only: never read before the call wrote it.  Calls that share a
+ *            workspace must not overlap in time.
+ * Scores, softmax statistics and sums are fp32; a softmax weight is rounded to
+ * bf16 for the product with the values, and the sum it is divided by is that
+ * of the rounded weights. */
+prox_status prox_kv_attention(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
+                              int32_t n_heads, float scale, int32_t window, void* out, int64_t out_stride,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* The batch's tokens back from the cache: code * scale (one fp32 rounding) as
+ * fp32 (out_fp32 != 0) or bf16, k_out and v_out device [n_tokens][n_kv]
+ * [head_dim] contiguous, 16-byte aligned. */
+prox_status prox_kv_read(const prox_kv_cache* c, const prox_kv_batch* b, void* k_out, void* v_out, int32_t out_fp32,
+                         void* stream);
+
 /* ---- Measurement helper (not part of the forward) ---------------------------
  * Read-stream probe: reads the first bytes / 16 * 16 bytes of the device
  * buffer `buf` (16-byte aligned) with `blocks` blocks of 512 threads, each
