@@ -47,6 +47,13 @@ int device_cus() {
     return cache[dev];
 }
 
+// A tag per call for arrival counters: counters left by any earlier call (this
+// process or another, or never cleared) carry another tag.
+uint32_t next_call_tag() {
+    static std::atomic<uint32_t> tag{(uint32_t)std::chrono::steady_clock::now().time_since_epoch().count() | 1u};
+    return tag.fetch_add(1u, std::memory_order_relaxed);
+}
+
 }  // namespace prox
 
 namespace {
@@ -103,13 +110,6 @@ ProxyView view_of(const prox_proxy* p) {
     v.codes = static_cast<const uint8_t*>(p->buf);
     v.scales = reinterpret_cast<const float*>(static_cast<const uint8_t*>(p->buf) + p->scale_offset);
     return v;
-}
-
-// A tag per call for the Stage-1 arrival counters: counters left by any
-// earlier call (this process or another, or never cleared) carry another tag.
-uint32_t next_call_tag() {
-    static std::atomic<uint32_t> tag{(uint32_t)std::chrono::steady_clock::now().time_since_epoch().count() | 1u};
-    return tag.fetch_add(1u, std::memory_order_relaxed);
 }
 
 }  // namespace

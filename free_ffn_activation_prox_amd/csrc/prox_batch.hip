@@ -182,10 +182,6 @@ struct PbArgs {
     float* key_tap;           // [B][F] or null
 };
 
-// Cache policy of a buffer access (gfx950): bit 4 = sc1.  With it a store or
-// load is coherent across the chip's L2 caches, like a device-scope atomic.
-constexpr int kCoherent = 16;
-
 constexpr int kPbRS = 136;    // LDS row stride of a transposed channel, in bf16 (128 + 8)
 constexpr int kPbWave = 2 * 16 * kPbRS;   // bf16 per wave region
 

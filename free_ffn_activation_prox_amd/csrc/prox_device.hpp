@@ -37,6 +37,10 @@ __device__ __forceinline__ uint4 buf_load16(__amdgpu_buffer_rsrc_t r, uint32_t v
     return make_uint4(v.x, v.y, v.z, v.w);
 }
 
+// Cache policy of a buffer access (gfx950): bit 4 = sc1.  With it a store or
+// load is coherent across the chip's L2 caches, like a device-scope atomic.
+constexpr int kCoherent = 16;
+
 // Arrival at a split tile: the counter holds (call tag << 32 | arrivals).  The
 // arrival that completes the tile stores 0 back, so every call leaves its
 // counters clear (a replayed graph reuses one tag); a counter holding anything

@@ -200,6 +200,7 @@ void clear_error();
 prox_status fail(prox_status st, const char* fmt, ...);
 prox_status hip_fail(hipError_t e, const char* where);
 int device_cus();
+uint32_t next_call_tag();
 
 // ---- paged 8-bit key/value cache (prox_kv.hip, prox_kv_attn.hip)
 hipError_t launch_kv_append(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* k, int64_t k_stride,

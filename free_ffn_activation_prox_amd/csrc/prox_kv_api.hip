@@ -59,7 +59,7 @@ prox_status check_heads(const prox_kv_cache* c, int32_t n_heads) {
 }
 
 prox_status launched(hipError_t e, const char* what) {
-    if (e == hipErrorInvalidConfiguration) return fail(PROX_E_UNSUPPORTED, "%s: too many blocks for one launch", what);
+    if (e == hipErrorInvalidConfiguration) return fail(PROX_E_UNSUPPORTED, "%s: the batch's bounds are too large for one call", what);
     return e == hipSuccess ? PROX_OK : hip_fail(e, what);
 }
 

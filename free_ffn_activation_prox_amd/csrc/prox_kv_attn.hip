@@ -4,62 +4,86 @@
 // scales sk, sv of each page:
 //   s_j = scale sk (q . kc_j),  o = sum_j exp(s_j - m) sv vc_j / sum_j exp(s_j - m)
 // in one pass over the pages with a running maximum m (base 2: log2(e) is
-// folded into the scale).  Codes are exact in bf16, so q . kc runs on the bf16
-// matrix cores without rounding an operand.  A softmax weight is rounded to
-// bf16 (half a step: 2^-9) for the product with the values; dividing by the sum
-// of the rounded weights keeps the result a weighted mean, and a row that
-// attends to one token alone exact.
+// folded into the scale).
+//
+// Arithmetic.  Both products run on v_mfma_f32_16x16x32_f16 with fp32 sums.
+//   codes  are exact in fp16.  An int8 code c is taken as 1024 + (c + 128): the
+//          byte put under the exponent bits 0x64, half an instruction a code
+//          where a conversion takes one and a half; the 1152 too many are
+//          subtracted as a start value of the sum, -1152 sum(q) and -1152
+//          sum(p), so the fp32 sums run over values up to 1279 / 127 times
+//          larger than the codes' own.
+//   q      (bf16, 8 bits) is scaled by a power of two to a largest value in
+//          [1, 2): exact in fp16 down to 2^-17 of the row's largest, and off
+//          by at most 2^-25 of that below.
+//   p      the softmax weights are rounded to fp16 (half a step: 2^-11) and
+//          held up to 2^14, so that fp16's normal numbers reach down to 2^-22
+//          of a row's largest.  The sum that the result is divided by is that
+//          of the rounded weights (a product with a row of constants), which
+//          keeps the result a weighted mean of the stored values.
+// m moves only when a score exceeds it by more than 2^6, so most pages rescale
+// nothing.
 //
 // A wave takes tiles of 16 rows that share a key head and walks their pages.
-// With K as the A operand and q as B, lane (g = l / 16, n = l % 16) gets the scores of row n and tokens
-// 16 t + 4 g + r of the page, t, r < 4; the V layout of the cache puts the
-// same tokens into lane group g, so the weights go straight into the second
-// product, whose result has row n in the same lanes: the running maximum, the
-// sums and the rescaling need no exchange but the maximum over the four g.
+// With K as the A operand and q as B, lane (g = l / 16, n = l % 16) gets the
+// scores of row n and tokens 16 t + 4 g + r of the page, t, r < 4; the V layout
+// of the cache puts the same tokens into lane group g, so the weights go
+// straight into the second product, whose result has row n in the same lanes:
+// nothing but the row's maximum crosses lanes.
 //
 // How the work is split.  A segment is one tile of rows (TQ tokens x HG query
 // heads of one key head) with the pages that some row of it sees; all segments'
-// pages form one line, cut into equal pieces, one for each wave of the grid,
-// whatever the lengths of the sequences.  A wave finds its piece from the
+// pages form one line, cut into pieces of equal length, one for each block,
+// whatever the lengths of the sequences.  A block finds its piece from the
 // lengths on the device (the host knows bounds only, and a captured call
-// follows the lengths).  A segment inside one piece is finished by its wave;
-// one that a cut divides leaves (maximum, sum, unnormalised result) of each
-// part in the workspace, at most two parts for each wave, and k_kv_join
-// combines them in order of position, so results do not depend on timing.
+// follows the lengths).  A short segment is not cut: it belongs to the block in
+// whose piece it begins.  A long one that a cut divides leaves (maximum, sum,
+// unnormalised result) of each part in the workspace, at most two parts for
+// each block, and the block that arrives last combines them in order of
+// position, so results do not depend on timing.
 #include "prox_kv.hpp"
 
 namespace prox {
 
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
 }
 
-// Eight codes -> eight bf16 (exact).
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    f16x2_t r;
+    r[0] = (_Float16)lo;
+    r[1] = (_Float16)hi;
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// Eight codes -> eight fp16: e4m3 as they are, int8 plus 1152.
 template <int KIND>
-__device__ __forceinline__ uint4 codes_bf16(uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ uint4 codes_f16(uint32_t lo, uint32_t hi) {
     if constexpr (KIND == PROX_KV_INT8) {
-        uint32_t o[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[4];
-            kv_values4<KIND>(h ? hi : lo, v);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)       // whole numbers below 2^8: the upper halves hold them
-                o[2 * h + e] = __builtin_amdgcn_perm(__float_as_uint(v[2 * e + 1]), __float_as_uint(v[2 * e]), 0x07060302u);
-        }
-        return make_uint4(o[0], o[1], o[2], o[3]);
+        const uint32_t a = lo ^ 0x80808080u, b = hi ^ 0x80808080u;
+        return make_uint4(__builtin_amdgcn_perm(0x64646464u, a, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u),
+                          __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u));
     } else {
-        return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 1.f, false)),
-                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 1.f, true)),
-                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.f, false)),
-                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.f, true)));
+        return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.f, true)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.f, true)));
     }
+}
+
+// What a product with a column of these constants gives: -1152 times the
+// operand's sum (int8), or the sum itself.
+template <int KIND>
+__device__ __forceinline__ uint4 constants() {
+    const uint32_t w = KIND == PROX_KV_INT8 ? 0xe480e480u : 0x3c003c00u;      // -1152 or 1, twice
+    return make_uint4(w, w, w, w);
 }
 
 // e4m3 codes with NaN taken as 0: slots that no token was written to may hold
@@ -70,10 +94,11 @@ __device__ __forceinline__ uint32_t no_nan_fp8(uint32_t w) {
 }
 
 __device__ __forceinline__ float over_groups_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    auto a = __builtin_amdgcn_permlane16_swap(__float_as_int(v), __float_as_int(v), false, false);
+    v = fmaxf(__int_as_float(a[0]), __int_as_float(a[1]));
+    auto b = __builtin_amdgcn_permlane32_swap(__float_as_int(v), __float_as_int(v), false, false);
+    return fmaxf(__int_as_float(b[0]), __int_as_float(b[1]));
 }
-__device__ __forceinline__ float over_groups_sum(float v) { return xor32_add(xor16_add(v)); }
 
 struct Attend {
     prox_kv_cache c;
@@ -81,13 +106,16 @@ struct Attend {
     const uint16_t* q;
     uint16_t* out;
     int64_t qs, os;
-    float* part_o;         // [workers][2][slot_rows][head_pad]
-    float2* part_ml;       // [workers][2][slot_rows]: maximum, sum
+    unsigned long long* arrived;   // [blocks]: arrivals of the cut segment that begins in a block's piece
+    float* part;                   // [blocks][2][slot_rows][head_pad + 4]: result, then maximum and sum
+    uint32_t part_bytes, tag;
     int rep, window;
     int HG, VH;            // query heads of a segment; segments of one tile of tokens (key heads x head groups)
     int TQ, tiles;         // tokens of a tile; most tiles of a sequence
-    int slot_rows, workers;
-    float scale2;          // scale * log2(e)
+    int slot_rows;
+    int no_cut, min_piece; // pages of a segment up to which it is not cut; least length of a piece
+    float scale2;          // |scale| * log2(e)
+    float sign;            // that of scale
 };
 
 // One tile of tokens of one sequence.
@@ -104,56 +132,88 @@ __device__ __forceinline__ Tile tile_of(const Attend& A, int s, int t) {
     x.n = min(x.R.rows - x.i0, A.TQ);
     const int cap = A.b.max_pages * kKvPage;
     const int p0 = x.R.first + x.i0, p1 = p0 + x.n;                  // positions p0 .. p1 - 1
-    const int hi = min(p1, cap), lo = A.window > 0 ? max(p0 - A.window + 1, 0) : 0;
+    const int hi = min(p1, cap), lo = A.window > 0 ? max(max(p0, 0) - A.window + 1, 0) : 0;
     const bool some = hi > 0 && lo < hi;
     x.pg0 = some ? lo / kKvPage : 0;
     x.pages = x.n <= 0 ? 0 : some ? (hi - 1) / kKvPage + 1 - x.pg0 : 1;
     return x;
 }
 
-__device__ __forceinline__ int64_t scan64(int64_t v, int l) {        // inclusive prefix sum over the wave
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-        const int64_t u = __shfl_up(v, m);
-        if (l >= m) v += u;
-    }
-    return v;
-}
+// A segment: key head and head group vh of tile t of sequence s, and the unit
+// of the line that it begins at.
+struct Place {
+    int s, t, vh, begin, pages;
+};
 
-// Pages (over all heads) of the tiles 0 .. count - 1 of the batch, tile =
-// sequence * A.tiles + tile of the sequence.
-__device__ __forceinline__ int64_t units_before(const Attend& A, int64_t count, int l) {
-    int64_t sum = 0;
-    for (int64_t j = l; j < count; j += 64) sum += tile_of(A, (int)(j / A.tiles), (int)(j % A.tiles)).pages;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
-    return sum * A.VH;
-}
+// The line of all segments' pages (below 2^31, checked on the host), seen by
+// one wave: 64 tiles at a time, tile j = sequence * A.tiles + tile of the
+// sequence, kept in registers where there are no more.
+struct Line {
+    const Attend& A;
+    int l, all, total;     // lane; tiles; units
+    int own, upto;         // this lane's tile of the last 64 looked at: its units, and those up to its end
 
-// The tile that holds unit x of the line, and the unit it begins at.
-__device__ __forceinline__ int64_t tile_at(const Attend& A, int64_t x, int l, int64_t* begin) {
-    const int64_t all = (int64_t)A.b.n_seq * A.tiles;
-    int64_t base = 0;
-    for (int64_t j0 = 0; j0 < all; j0 += 64) {
-        const int64_t j = j0 + l;
-        const int64_t own = j < all ? (int64_t)tile_of(A, (int)(j / A.tiles), (int)(j % A.tiles)).pages * A.VH : 0;
-        const int64_t upto = scan64(own, l);
-        const uint64_t past = __ballot(base + upto > x);
-        if (past) {
-            const int at = __builtin_ctzll(past);
-            *begin = base + __shfl(upto - own, at);
-            return j0 + at;
+    __device__ __forceinline__ void look(int j0, int base) {
+        const int j = j0 + l;
+        own = 0;
+        if (j < all) own = (A.tiles == 1 ? tile_of(A, j, 0) : tile_of(A, j / A.tiles, j % A.tiles)).pages * A.VH;
+        upto = own;
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const int u = __shfl_up(upto, m);
+            if (l >= m) upto += u;
         }
-        base += __shfl(upto, 63);
+        upto += base;
     }
-    *begin = base;
-    return all;
-}
+    __device__ __forceinline__ Line(const Attend& a, int lane) : A(a), l(lane), all(a.b.n_seq * a.tiles) {
+        total = 0;
+        for (int j0 = 0; j0 < all; j0 += 64) {
+            look(j0, total);
+            total = __builtin_amdgcn_readlane(upto, 63);
+        }
+    }
+    // x < total
+    __device__ __forceinline__ Place at(int x) {
+        int base = 0, j0 = 0;
+        if (all > 64)
+            for (;; j0 += 64) {
+                look(j0, base);
+                if (__ballot(upto > x) || j0 + 64 >= all) break;
+                base = __builtin_amdgcn_readlane(upto, 63);
+            }
+        const int on = __builtin_ctzll(__ballot(upto > x) | (1ull << 63));
+        const int units = __builtin_amdgcn_readlane(own, on), first = __builtin_amdgcn_readlane(upto, on) - units;
+        const uint32_t tile = (uint32_t)(j0 + on);
+        Place p;
+        p.s = (int)(tile / (uint32_t)A.tiles);
+        p.t = (int)(tile % (uint32_t)A.tiles);
+        p.pages = (int)((uint32_t)units / (uint32_t)A.VH);
+        p.vh = (int)((uint32_t)(x - first) / (uint32_t)p.pages);
+        p.begin = first + p.vh * p.pages;
+        return p;
+    }
+    // Where the piece that is cut at unit x begins in fact: behind the segment
+    // around x if that is a short one.
+    __device__ __forceinline__ int cut(int64_t x) {
+        if (x >= total) return total;
+        const Place p = at((int)x);
+        return x == p.begin || p.pages > A.no_cut ? (int)x : p.begin + p.pages;
+    }
+};
 
-__device__ __forceinline__ int64_t piece_begin(int64_t w, int64_t total, int workers) { return w * total / workers; }
-// The piece that holds unit x: the last w with piece_begin(w) <= x.
-__device__ __forceinline__ int64_t piece_of(int64_t x, int64_t total, int workers) {
-    return ((x + 1) * workers - 1) / total;
+// The segment after p.
+__device__ __forceinline__ void next_segment(const Attend& A, Place& p, Tile& T) {
+    p.begin += p.pages;
+    if (++p.vh < A.VH) return;
+    p.vh = 0;
+    do {
+        if (++p.t == A.tiles) {
+            p.t = 0;
+            ++p.s;
+        }
+        T = tile_of(A, p.s, p.t);       // called where a segment follows
+    } while (T.pages == 0);
+    p.pages = T.pages;
 }
 
 __device__ __forceinline__ uint2 bf16x4(f32x4_t v) {
@@ -167,286 +227,487 @@ __device__ __forceinline__ uint2 bf16x4(f32x4_t v) {
 // 1 / the softmax sum: 0 for a row that has seen nothing; a NaN sum stays.
 __device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); }
 
-// grid: A.workers waves, 64 threads each.  NT tiles of 16 rows a segment.
-template <int KIND, int NP, int NT>
-__global__ void __launch_bounds__(64) k_kv_attend(Attend A) {
-    const int l = threadIdx.x, n = l & 15, g = l >> 4;
-    const int hd = A.c.head_dim, cap = A.b.max_pages * kKvPage;
-    constexpr int kPageBytes = kKvPage * 64 * NP;
-    const int64_t total = units_before(A, (int64_t)A.b.n_seq * A.tiles, l);
-    const int64_t end = piece_begin(blockIdx.x + 1, total, A.workers);
-    int64_t x = piece_begin(blockIdx.x, total, A.workers);
-    if (x >= end) return;
-    int64_t begin;
-    int64_t tile = tile_at(A, x, l, &begin);
-    int s = __builtin_amdgcn_readfirstlane((int)(tile / A.tiles)), t = __builtin_amdgcn_readfirstlane((int)(tile % A.tiles));
-    Tile T = tile_of(A, s, t);
-    int vh = __builtin_amdgcn_readfirstlane((int)((x - begin) / T.pages));
-    int from = __builtin_amdgcn_readfirstlane((int)((x - begin) % T.pages));
+// Part (m, sum, v) joins (m0, s0, o).
+__device__ __forceinline__ void join(float& m0, float& s0, f32x4_t& o, float m, float sum, f32x4_t v) {
+    const float mn = fmaxf(m0, m), base = mn > -INFINITY ? mn : 0.f;
+    const float f = __builtin_amdgcn_exp2f(m0 - base), e = __builtin_amdgcn_exp2f(m - base);
+    m0 = mn;
+    s0 = s0 * f + sum * e;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = o[r] * f + v[r] * e;
+}
 
-    while (x < end) {
-        const int upto = (int)min((int64_t)T.pages, from + (end - x));
-        const int groups = A.VH / A.c.n_kv, head = vh / groups, grp = vh % groups;
-        const int nh = min(A.HG, A.rep - grp * A.HG);                  // heads of this segment
-        uint4 q[NT][NP][2];
+// Where row r of segment (T, vh) goes: its output, or null for a row that the
+// segment does not have.
+__device__ __forceinline__ uint16_t* out_row(const Attend& A, const Tile& T, int vh, int r) {
+    const int groups = A.VH / A.c.n_kv, head = vh / groups, grp = vh % groups;
+    const int i = r / A.HG, hq = grp * A.HG + r % A.HG;
+    if (i >= T.n || hq >= A.rep) return nullptr;
+    return A.out + (int64_t)(T.R.q0 + T.i0 + i) * A.os + (int64_t)(head * A.rep + hq) * A.c.head_dim;
+}
+
+// A weight's rows hold up to 2^(kTop + kSlack): see "Arithmetic" above.
+constexpr float kTop = 8.f, kSlack = 6.f;
+
+// One wave's walk over pages `from` .. `upto` - 1 of a segment for the rows
+// r0 .. r0 + 16 NT - 1 of its tile.
+template <int KIND, int NP, int NT>
+struct Walk {
+    static constexpr int kPageBytes = kKvPage * 64 * NP;
+    f32x4_t o[NT][4 * NP];      // lane (g, n): channels 16 d + 4 g + r of row 16 u + n
+    float m[NT], sum[NT];
+    bool live[NT];
+
+    __device__ __forceinline__ void run(const Attend& A, const Place& P, const Tile& T, int from, int upto, int r0, int l) {
+        const int n = l & 15, g = l >> 4, hd = A.c.head_dim, cap = A.b.max_pages * kKvPage;
+        const int groups = A.VH / A.c.n_kv, head = P.vh / groups, grp = P.vh % groups;
+        const int32_t* table = A.b.block_table + (size_t)P.s * A.b.max_pages + T.pg0;
+        const int ctx = T.R.first + T.R.n;                         // slots from here on hold no token
+        const uint8_t* kbase = static_cast<const uint8_t*>(A.c.k) + (size_t)head * kPageBytes + l * 16;
+        const uint8_t* vbase = static_cast<const uint8_t*>(A.c.v) + (size_t)head * kPageBytes + l * 16;
+
+        // a page of the segment, -1 where the table names none; its codes and scale
+        auto page_at = [&](int p) {
+            const int id = table[min(p, upto - 1)];
+            return id >= 0 && id < A.c.n_pages ? id : -1;
+        };
+        uint4 kf[4 * NP], vf[4 * NP];
+        float ks, vs;
+        auto load_k = [&](int page) {
+            const size_t at = (size_t)max(page, 0) * A.c.n_kv;
+            const uint4* p = reinterpret_cast<const uint4*>(kbase + at * kPageBytes);
+#pragma unroll
+            for (int d = 0; d < 4 * NP; ++d) kf[d] = p[d * 64];
+            ks = A.c.k_scale[at + head];
+        };
+        auto load_v = [&](int page) {
+            const size_t at = (size_t)max(page, 0) * A.c.n_kv;
+            const uint4* p = reinterpret_cast<const uint4*>(vbase + at * kPageBytes);
+#pragma unroll
+            for (int d = 0; d < 4 * NP; ++d) vf[d] = p[d * 64];
+            vs = A.c.v_scale[at + head];
+        };
+
+        int page = page_at(from), page_n = page_at(from + 1);
+        load_k(page);
+
+        // The rows: what they see, and q scaled to fp16.
         int key_lo[NT], key_hi[NT];
-        int64_t row_at[NT];                                            // row of the batch and its head, as one
-        bool live[NT];
+        uint4 q[NT][NP][2];
+        float row_scale[NT], bias[NT];
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const int r = 16 * u + n, i = T.i0 + r / A.HG, hq = r % A.HG;
-            live[u] = r / A.HG < T.n && hq < nh;
+            const int r = r0 + 16 * u + n, i = T.i0 + r / A.HG, hq = grp * A.HG + r % A.HG;
+            live[u] = r / A.HG < T.n && hq < A.rep;
             const int pos = T.R.first + i;
             const bool sees = live[u] && pos >= 0 && pos < cap;
-            key_lo[u] = sees && A.window > 0 ? max(pos - A.window + 1, 0) : 0;
-            key_hi[u] = sees ? pos + 1 : 0;
-            row_at[u] = live[u] ? (int64_t)(T.R.q0 + i) : 0;
-            const int h = head * A.rep + grp * A.HG + hq;
-            const uint16_t* src = A.q + row_at[u] * A.qs + (int64_t)h * hd;
+            key_lo[u] = sees && A.window > 0 ? pos - A.window + 1 : 0;
+            key_hi[u] = sees ? pos + 1 : (live[u] ? 0 : 0x7fffffff);    // a row that is not there is not masked
+            const uint16_t* src = A.q + (int64_t)(T.R.q0 + (live[u] ? i : 0)) * A.qs +
+                                  (int64_t)(head * A.rep + (live[u] ? hq : 0)) * hd;
+            uint32_t big = 0;
 #pragma unroll
             for (int a = 0; a < NP; ++a)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int ch = 64 * a + 16 * g + 8 * e;
-                    q[u][a][e] = live[u] && ch < hd ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0, 0, 0, 0);
-                }
-        }
-        const int ctx = T.R.first + T.R.n;                             // slots from here on hold no token
-        f32x4_t o[NT][4 * NP];
-        float m[NT], sum[NT];
+                    const uint4 x = live[u] && ch < hd ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0, 0, 0, 0);
+                    q[u][a][e] = x;
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
+                    for (int f = 0; f < 4; ++f) big = max(big, max(w[f] & 0x7fff0000u, (w[f] << 16) & 0x7fff0000u));
+                }
+            big = __float_as_uint(over_groups_max(__uint_as_float(big > 0x7f800000u ? 0x7f800000u : big)));
+            // 2^-E and 2^E with E the exponent of the row's largest value; 1 for a row of zeros or with an infinity or NaN
+            const uint32_t ex = big >> 23;
+            const bool one = ex == 0 || ex == 255;
+            const int E = one ? 0 : (int)ex - 127;
+            const float down = ldexpf(A.sign, -E);
+            row_scale[u] = ldexpf(A.scale2, E);
+            f32x4_t b4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int a = 0; a < NP; ++a)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 x = q[u][a][e];
+                    q[u][a][e] = make_uint4(pack_f16(bf16_lo(x.x) * down, bf16_hi(x.x) * down),
+                                            pack_f16(bf16_lo(x.y) * down, bf16_hi(x.y) * down),
+                                            pack_f16(bf16_lo(x.z) * down, bf16_hi(x.z) * down),
+                                            pack_f16(bf16_lo(x.w) * down, bf16_hi(x.w) * down));
+                    if constexpr (KIND == PROX_KV_INT8) b4 = mfma16(constants<KIND>(), q[u][a][e], b4);
+                }
+            bias[u] = b4[0];
             m[u] = -INFINITY;
             sum[u] = 0.f;
 #pragma unroll
             for (int d = 0; d < 4 * NP; ++d) o[u][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
 
-        for (int pg = T.pg0 + from; pg < T.pg0 + upto; ++pg) {
-            const int page = A.b.block_table[(size_t)s * A.b.max_pages + pg];
-            if (page < 0 || page >= A.c.n_pages) continue;
-            const size_t where = (size_t)page * A.c.n_kv + head;
-            const uint4* kc = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(A.c.k) + where * kPageBytes) + l;
-            const uint4* vc = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(A.c.v) + where * kPageBytes) + l;
-            const float ks = A.c.k_scale[where] * A.scale2, vs = A.c.v_scale[where];
-            float w[NT][4][4];
+        for (int p = from; p < upto; ++p) {
+            load_v(page);
+            f32x4_t w[NT][4];
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                f32x4_t acc[NT];
+            for (int t = 0; t < 4; ++t) {
 #pragma unroll
-                for (int u = 0; u < NT; ++u) acc[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                for (int u = 0; u < NT; ++u) w[u][t] = f32x4_t{bias[u], bias[u], bias[u], bias[u]};
 #pragma unroll
                 for (int a = 0; a < NP; ++a) {
-                    const uint4 c = kc[(a * 4 + tt) * 64];
-                    const uint4 k0 = codes_bf16<KIND>(c.x, c.y), k1 = codes_bf16<KIND>(c.z, c.w);
+                    const uint4 c = kf[a * 4 + t];
+                    const uint4 k0 = codes_f16<KIND>(c.x, c.y), k1 = codes_f16<KIND>(c.z, c.w);
 #pragma unroll
-                    for (int u = 0; u < NT; ++u) acc[u] = mfma16(k0, q[u][a][0], acc[u]);
+                    for (int u = 0; u < NT; ++u) w[u][t] = mfma16(k0, q[u][a][0], w[u][t]);
 #pragma unroll
-                    for (int u = 0; u < NT; ++u) acc[u] = mfma16(k1, q[u][a][1], acc[u]);
+                    for (int u = 0; u < NT; ++u) w[u][t] = mfma16(k1, q[u][a][1], w[u][t]);
                 }
-#pragma unroll
-                for (int u = 0; u < NT; ++u)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int key = pg * kKvPage + 16 * tt + 4 * g + r;
-                        w[u][tt][r] = key >= key_lo[u] && key < key_hi[u] ? acc[u][r] * ks : -INFINITY;
-                    }
             }
-            uint32_t p[NT][4][2];
-            float keep[NT];
+            const float ks_p = ks;
+            const int base_key = (T.pg0 + p) * kKvPage;
+            const bool gone = page < 0, clean = KIND == PROX_KV_FP8 && (gone || base_key + kKvPage > ctx);
+            if (p + 1 < upto) {                                     // the next page's keys while this one is weighed
+                page = page_n;
+                load_k(page);
+                page_n = page_at(p + 2);
+            }
+            // keys that a row does not see; most pages are seen whole by every row
+            bool open = !gone;
+#pragma unroll
+            for (int u = 0; u < NT; ++u) open = open && key_lo[u] <= base_key && key_hi[u] >= base_key + kKvPage;
+            if (__ballot(open) != ~0ull) {
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    const int s_lo = key_lo[u] - base_key, s_hi = gone ? 0 : key_hi[u] - base_key;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int slot = 16 * t + 4 * g + r;
+                            w[u][t][r] = slot >= s_lo && slot < s_hi ? w[u][t][r] : -INFINITY;
+                        }
+                }
+            }
+            float fac[NT], top[NT];
+            bool grow = false;
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
+                // not 0 (a page of zeros): 0 x -inf would be NaN; the scores of such a page vanish all the same
+                fac[u] = fmaxf(ks_p * row_scale[u], 1e-37f);
                 float most = w[u][0][0];
 #pragma unroll
                 for (int e = 1; e < 16; ++e) most = fmaxf(most, w[u][e >> 2][e & 3]);
-                const float m_new = fmaxf(m[u], over_groups_max(most));
-                const float base = m_new > -INFINITY ? m_new : 0.f;    // a row that has seen nothing yet
-                keep[u] = __builtin_amdgcn_exp2f(m[u] - base);
-                m[u] = m_new;
-                sum[u] *= keep[u];
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-                        b2 e;
-                        e[0] = (__bf16)__builtin_amdgcn_exp2f(w[u][tt][2 * r] - base);
-                        e[1] = (__bf16)__builtin_amdgcn_exp2f(w[u][tt][2 * r + 1] - base);
-                        p[u][tt][r] = __builtin_bit_cast(uint32_t, e);
-                        sum[u] += bf16_lo(p[u][tt][r]) + bf16_hi(p[u][tt][r]);
-                    }
+                top[u] = over_groups_max(most) * fac[u];
+                grow = grow || top[u] > m[u] + kSlack;
             }
-            const bool tail = KIND == PROX_KV_FP8 && (pg + 1) * kKvPage > ctx;
-#pragma unroll
-            for (int d = 0; d < 4 * NP; ++d) {
-                uint4 c = vc[d * 64];
-                if (tail) c = make_uint4(no_nan_fp8(c.x), no_nan_fp8(c.y), no_nan_fp8(c.z), no_nan_fp8(c.w));
-                const uint4 v0 = codes_bf16<KIND>(c.x, c.y), v1 = codes_bf16<KIND>(c.z, c.w);
+            if (__ballot(grow)) {
 #pragma unroll
                 for (int u = 0; u < NT; ++u) {
-                    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-                    acc = mfma16(v0, make_uint4(p[u][0][0], p[u][0][1], p[u][1][0], p[u][1][1]), acc);
-                    acc = mfma16(v1, make_uint4(p[u][2][0], p[u][2][1], p[u][3][0], p[u][3][1]), acc);
+                    const float mn = fmaxf(m[u], top[u]), base = mn > -INFINITY ? mn : 0.f;
+                    const float keep = __builtin_amdgcn_exp2f(m[u] - base);
+                    m[u] = mn;
+                    sum[u] *= keep;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[u][d][r] = fmaf(acc[r], vs, o[u][d][r] * keep[u]);
+                    for (int d = 0; d < 4 * NP; ++d) o[u][d] *= keep;
+                }
+            }
+            uint4 pw[NT][2];
+            f32x4_t start[NT];
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const float base = (m[u] > -INFINITY ? m[u] : 0.f) - kTop;
+                uint32_t e[4][2];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        e[t][r] = pack_f16(__builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r], fac[u], -base)),
+                                           __builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r + 1], fac[u], -base)));
+                pw[u][0] = make_uint4(e[0][0], e[0][1], e[1][0], e[1][1]);
+                pw[u][1] = make_uint4(e[2][0], e[2][1], e[3][0], e[3][1]);
+                f32x4_t c = {0.f, 0.f, 0.f, 0.f};
+                c = mfma16(constants<KIND>(), pw[u][0], c);
+                c = mfma16(constants<KIND>(), pw[u][1], c);
+                if constexpr (KIND == PROX_KV_INT8) {
+                    sum[u] = fmaf(c[0], -1.f / 1152.f, sum[u]);
+                    start[u] = c;
+                } else {
+                    sum[u] += c[0];
+                    start[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < 4 * NP; ++d) {
+                uint4 c = vf[d];
+                if (clean) c = make_uint4(no_nan_fp8(c.x), no_nan_fp8(c.y), no_nan_fp8(c.z), no_nan_fp8(c.w));
+                const uint4 v0 = codes_f16<KIND>(c.x, c.y), v1 = codes_f16<KIND>(c.z, c.w);
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    f32x4_t acc = mfma16(v0, pw[u][0], start[u]);
+                    acc = mfma16(v1, pw[u][1], acc);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[u][d][r] = fmaf(acc[r], vs, o[u][d][r]);
                 }
             }
         }
+    }
+};
 
-        const bool done = from == 0 && upto == T.pages;
-        const size_t slot = (size_t)blockIdx.x * 2 + (from == 0 ? 1 : 0);
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
-            const float total_sum = over_groups_sum(sum[u]);
-            if (!live[u]) continue;
-            const int r = 16 * u + n;
-            if (done) {
-                const float inv = inverse(total_sum);
-                uint16_t* to = A.out + row_at[u] * A.os + (int64_t)(head * A.rep + grp * A.HG + r % A.HG) * hd;
-#pragma unroll
-                for (int d = 0; d < 4 * NP; ++d)
-                    if (16 * d + 4 * g < hd) *reinterpret_cast<uint2*>(to + 16 * d + 4 * g) = bf16x4(o[u][d] * inv);
-            } else {
-                const size_t pr = slot * A.slot_rows + r;
-                if (g == 0) A.part_ml[pr] = make_float2(m[u], total_sum);
-#pragma unroll
-                for (int d = 0; d < 4 * NP; ++d)
-                    *reinterpret_cast<f32x4_t*>(A.part_o + pr * (64 * NP) + 16 * d + 4 * g) = o[u][d];
-            }
-        }
+// Blocks of up to kWaves waves.
+//   ROWS false (a tile of 16 rows at most): the waves cut the block's piece
+//     among themselves once more and meet at its end, where segments that
+//     several waves worked on are put together in LDS.
+//     LDS: [waves][2][slot_rows][64 NP + 4] floats
+//   ROWS true: a tile of 16 NT rows for each wave; the waves walk the same pages.
+// Rows of cut segments go to the workspace.
+template <int KIND, int NP, int NT, bool ROWS, int kWaves>
+__global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
+    extern __shared__ __align__(16) float lds[];
+    __shared__ int tag_s[16];                     // segment (its first unit) of each wave's two slots, -1: none
+    __shared__ int done_s[2];
+    constexpr int RW = 64 * NP + 4;               // floats of a row in a slot: result, maximum, sum
+    constexpr int LPR = 16 * NP;                  // lanes of a row, four channels each
+    const int l = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), n = l & 15, g = l >> 4;
+    const int WV = blockDim.x >> 6;
+    const int hd = A.c.head_dim;
+    Line line(A, l);
+    const int piece = (int)max((uint32_t)line.total / gridDim.x + 1, (uint32_t)A.min_piece);
+    if ((int64_t)blockIdx.x * piece >= line.total) return;
+    const int b0 = line.cut((int64_t)blockIdx.x * piece), b1 = line.cut((int64_t)(blockIdx.x + 1) * piece);
+    if (b0 >= b1) return;
+    const __amdgpu_buffer_rsrc_t rp = make_rsrc(A.part, A.part_bytes);
+    bool sent = false;
+    // a row of a part in the workspace: bytes
+    auto part_at = [&](int block, bool begins, int r) {
+        return ((2u * (uint32_t)block + (begins ? 1u : 0u)) * (uint32_t)A.slot_rows + (uint32_t)r) * (uint32_t)(RW * 4);
+    };
 
-        x += upto - from;
-        from = 0;
-        if (x < end && ++vh == A.VH) {
-            vh = 0;
-            do {
-                if (++t == A.tiles) {
-                    t = 0;
-                    ++s;
+    int x = b0, end = b1;
+    if (!ROWS) {
+        x = b0 + (int)((int64_t)(b1 - b0) * wv / WV);
+        end = b0 + (int)((int64_t)(b1 - b0) * (wv + 1) / WV);
+        if (l < 2) tag_s[2 * wv + l] = -1;
+    }
+    if (x < end) {
+        Place P = line.at(x);
+        Tile T = tile_of(A, P.s, P.t);
+        for (;;) {
+            const int from = x - P.begin, upto = min(P.pages, end - P.begin);
+            const int r0 = ROWS ? 16 * NT * wv : 0;
+            Walk<KIND, NP, NT> w;
+            if (!ROWS || r0 < T.n * A.HG) {
+                w.run(A, P, T, from, upto, r0, l);
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    const int r = r0 + 16 * u + n;
+                    if (from == 0 && upto == P.pages) {
+                        uint16_t* to = w.live[u] ? out_row(A, T, P.vh, r) : nullptr;
+                        const float inv = inverse(w.sum[u]);
+                        if (to)
+#pragma unroll
+                            for (int d = 0; d < 4 * NP; ++d)
+                                if (16 * d + 4 * g < hd) *reinterpret_cast<uint2*>(to + 16 * d + 4 * g) = bf16x4(w.o[u][d] * inv);
+                    } else if (!ROWS) {
+                        const int slot = 2 * wv + (from == 0 ? 1 : 0);
+                        if (l == 0) tag_s[slot] = P.begin;
+                        if (n < A.slot_rows) {
+                            float* to = lds + (slot * A.slot_rows + n) * RW;
+#pragma unroll
+                            for (int d = 0; d < 4 * NP; ++d) *reinterpret_cast<f32x4_t*>(to + 16 * d + 4 * g) = w.o[u][d];
+                            if (g == 0) *reinterpret_cast<float2*>(to + 64 * NP) = make_float2(w.m[u], w.sum[u]);
+                        }
+                    } else if (w.live[u]) {
+                        const uint32_t at = part_at(blockIdx.x, from == 0, r);
+#pragma unroll
+                        for (int d = 0; d < 4 * NP; ++d)
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, w.o[u][d]), rp,
+                                                                   (int)(at + 4 * (16 * d + 4 * g)), 0, kCoherent);
+                        if (g == 0) {
+                            const u32x2_t ms = {__float_as_uint(w.m[u]), __float_as_uint(w.sum[u])};
+                            __builtin_amdgcn_raw_buffer_store_b64(ms, rp, (int)(at + 256 * NP), 0, kCoherent);
+                        }
+                    }
                 }
-                T = tile_of(A, s, t);                                   // x < end <= total: a tile follows
-            } while (T.pages == 0);
-        }
-    }
-}
-
-// Joins the parts of the segments that more than one wave worked on.  Block:
-// one segment and RB of its rows, 256 threads as 64 NP / 4 lanes for each row
-// and part; the parts of a row are summed in order of position within a lane
-// group and the groups in order, always the same way.
-template <int NP, int RB>
-__global__ void __launch_bounds__(256) k_kv_join(Attend A, int row_blocks) {
-    constexpr int LPR = 16 * NP;                 // lanes of one row, four channels each
-    constexpr int GR = 256 / LPR;                // lane groups
-    __shared__ float4 acc_s[GR][LPR];
-    __shared__ float2 ml_s[GR];
-    const int l = threadIdx.x & 63;
-    const int64_t seg = blockIdx.x / row_blocks;
-    const int rb = blockIdx.x % row_blocks, vh = (int)(seg % A.VH);
-    const int64_t tile = seg / A.VH;
-    const int s = (int)(tile / A.tiles);
-    const Tile T = tile_of(A, s, (int)(tile % A.tiles));
-    if (T.pages == 0) return;
-    const int64_t all = (int64_t)A.b.n_seq * A.tiles;
-    const int64_t before = units_before(A, tile, l);
-    int64_t total = before;
-    for (int64_t j = tile + l; j - l < all; j += 64) {
-        int64_t v = j < all ? (int64_t)tile_of(A, (int)(j / A.tiles), (int)(j % A.tiles)).pages * A.VH : 0;
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
-        total += v;
-    }
-    const int64_t a = before + (int64_t)vh * T.pages;
-    const int w0 = (int)piece_of(a, total, A.workers), w1 = (int)piece_of(a + T.pages - 1, total, A.workers);
-    if (w0 == w1) return;
-    const int groups = A.VH / A.c.n_kv, head = vh / groups, grp = vh % groups;
-    const int nh = min(A.HG, A.rep - grp * A.HG);
-    const int lane = threadIdx.x % LPR, gr = threadIdx.x / LPR;
-    const bool in = gr < GR;                     // NP = 3: 16 threads are over
-    const int parts = w1 - w0 + 1;
-    for (int r = rb * RB; r < min((rb + 1) * RB, A.TQ * A.HG); ++r) {
-        const int i = T.i0 + r / A.HG, hq = r % A.HG;
-        if (r / A.HG >= T.n || hq >= nh) continue;                      // uniform
-        float m = -INFINITY, sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int pb = gr * parts / GR, pe = in ? (gr + 1) * parts / GR : 0;
-        for (int p = pb; p < pe; ++p) {
-            // a wave whose piece is empty (more waves than pages) has no part
-            if (piece_begin(w0 + p, total, A.workers) == piece_begin(w0 + p + 1, total, A.workers)) continue;
-            const size_t pr = ((size_t)(w0 + p) * 2 + (p == 0 ? 1 : 0)) * A.slot_rows + r;
-            const float2 ml = A.part_ml[pr];
-            const float4 v = reinterpret_cast<const float4*>(A.part_o + pr * (64 * NP))[lane];
-            const float mn = fmaxf(m, ml.x), base = mn > -INFINITY ? mn : 0.f;
-            const float f = __builtin_amdgcn_exp2f(m - base), e = __builtin_amdgcn_exp2f(ml.x - base);
-            m = mn;
-            sum = sum * f + ml.y * e;
-            o = make_float4(o.x * f + v.x * e, o.y * f + v.y * e, o.z * f + v.z * e, o.w * f + v.w * e);
-        }
-        __syncthreads();
-        if (in) {
-            acc_s[gr][lane] = o;
-            if (lane == 0) ml_s[gr] = make_float2(m, sum);
-        }
-        __syncthreads();
-        if (gr == 0) {
-            for (int p = 1; p < GR; ++p) {
-                const float2 ml = ml_s[p];
-                const float4 v = acc_s[p][lane];
-                const float mn = fmaxf(m, ml.x), base = mn > -INFINITY ? mn : 0.f;
-                const float f = __builtin_amdgcn_exp2f(m - base), e = __builtin_amdgcn_exp2f(ml.x - base);
-                m = mn;
-                sum = sum * f + ml.y * e;
-                o = make_float4(o.x * f + v.x * e, o.y * f + v.y * e, o.z * f + v.z * e, o.w * f + v.w * e);
             }
-            const float inv = inverse(sum);
-            if (4 * lane < A.c.head_dim)
-                *reinterpret_cast<uint2*>(A.out + (int64_t)(T.R.q0 + i) * A.os +
-                                          (int64_t)(head * A.rep + grp * A.HG + hq) * A.c.head_dim + 4 * lane) =
-                    bf16x4(f32x4_t{o.x * inv, o.y * inv, o.z * inv, o.w * inv});
+            if (ROWS) sent = sent || from != 0 || upto != P.pages;
+            x = P.begin + upto;
+            if (x >= end) break;
+            next_segment(A, P, T);
+        }
+    }
+
+    if (!ROWS) {
+        // The slots in order of position; neighbours of one segment are put
+        // together by all threads: thread = (row, four channels) of one of them.
+        __syncthreads();
+        for (int i = 0; i < 2 * WV;) {
+            const int tag = tag_s[i];
+            if (tag < 0) {
+                ++i;
+                continue;
+            }
+            int j = i + 1;
+            while (j < 2 * WV && (tag_s[j] < 0 || tag_s[j] == tag)) ++j;
+            const Place P = line.at(tag);
+            const Tile T = tile_of(A, P.s, P.t);
+            const bool whole = tag >= b0 && tag + P.pages <= b1;
+            for (int e = threadIdx.x; e < A.slot_rows * LPR; e += blockDim.x) {
+                const int r = e / LPR, c4 = 4 * (e % LPR);
+                float m = -INFINITY, sum = 0.f;
+                f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+                for (int k = i; k < j; ++k) {
+                    if (tag_s[k] < 0) continue;
+                    const float* from = lds + (k * A.slot_rows + r) * RW;
+                    const float2 ms = *reinterpret_cast<const float2*>(from + 64 * NP);
+                    join(m, sum, o, ms.x, ms.y, *reinterpret_cast<const f32x4_t*>(from + c4));
+                }
+                if (whole) {
+                    uint16_t* to = out_row(A, T, P.vh, r);
+                    if (to && c4 < hd) *reinterpret_cast<uint2*>(to + c4) = bf16x4(o * inverse(sum));
+                } else {
+                    const uint32_t at = part_at(blockIdx.x, tag >= b0, r);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), rp, (int)(at + 4 * c4), 0, kCoherent);
+                    if (c4 == 0) {
+                        const u32x2_t ms = {__float_as_uint(m), __float_as_uint(sum)};
+                        __builtin_amdgcn_raw_buffer_store_b64(ms, rp, (int)(at + 256 * NP), 0, kCoherent);
+                    }
+                }
+            }
+            sent = sent || !whole;
+            i = j;
+        }
+    }
+    if (!sent) return;                            // uniform over the block
+
+    // Arrivals: of the segment that continues into this piece, and of the one
+    // that goes on behind it (the same one if it spans the piece).
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's stores have completed
+    __syncthreads();
+    Place S[2];
+    bool have[2];
+    S[0] = line.at(b0);
+    have[0] = S[0].begin < b0;
+    S[1] = line.at(b1 - 1);
+    have[1] = S[1].begin >= b0 && S[1].begin + S[1].pages > b1;
+    if (threadIdx.x == 0)
+        for (int k = 0; k < 2; ++k)
+            if (have[k]) {
+                const int w0 = S[k].begin / piece, w1 = (S[k].begin + S[k].pages - 1) / piece;
+                done_s[k] = tile_arrive(A.arrived + w0, A.tag, w1 - w0 + 1);
+            }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        if (!have[k] || !done_s[k]) continue;
+        const Tile T = tile_of(A, S[k].s, S[k].t);
+        const int w0 = S[k].begin / piece, parts = (S[k].begin + S[k].pages - 1) / piece - w0 + 1;
+        const int lanes = A.slot_rows * LPR;                            // (row, four channels)
+        const int PG = max((int)blockDim.x / lanes, 1);                 // groups of parts, each in order
+        __syncthreads();                                                // LDS is free
+        for (int e0 = 0; e0 < lanes; e0 += blockDim.x) {
+            const int pg = PG > 1 ? (int)threadIdx.x / lanes : 0;
+            const int e = PG > 1 ? (int)threadIdx.x % lanes : e0 + (int)threadIdx.x;
+            const int r = e / LPR, c4 = 4 * (e % LPR);
+            uint16_t* to = e < lanes ? out_row(A, T, S[k].vh, r) : nullptr;    // a row that is not there was not stored
+            const bool in = to && pg < PG;
+            float m = -INFINITY, sum = 0.f;
+            f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+            if (in) {
+                const int pe = (pg + 1) * parts / PG;
+                for (int p0 = pg * parts / PG; p0 < pe; p0 += 8) {
+                    u32x4_t v[8];
+                    u32x2_t ms[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int p = min(p0 + u, pe - 1);
+                        const uint32_t at = part_at(w0 + p, p == 0, r);
+                        v[u] = __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 4 * c4), 0, kCoherent);
+                        ms[u] = __builtin_amdgcn_raw_buffer_load_b64(rp, (int)(at + 256 * NP), 0, kCoherent);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (p0 + u < pe)
+                            join(m, sum, o, __uint_as_float(ms[u].x), __uint_as_float(ms[u].y), __builtin_bit_cast(f32x4_t, v[u]));
+                }
+            }
+            if (PG > 1) {
+                float* mine = lds + (pg * lanes + e) * 8;
+                if (in) {
+                    *reinterpret_cast<f32x4_t*>(mine) = o;
+                    *reinterpret_cast<float2*>(mine + 4) = make_float2(m, sum);
+                }
+                __syncthreads();
+                if (in && pg == 0)
+                    for (int u = 1; u < PG; ++u) {
+                        const float* from = lds + (u * lanes + e) * 8;
+                        const float2 ms = *reinterpret_cast<const float2*>(from + 4);
+                        join(m, sum, o, ms.x, ms.y, *reinterpret_cast<const f32x4_t*>(from));
+                    }
+            }
+            if (in && pg == 0 && c4 < hd) *reinterpret_cast<uint2*>(to + c4) = bf16x4(o * inverse(sum));
         }
     }
 }
 
 // How a call is split (host): a function of the bounds that the batch gives.
 struct Split {
-    int NT, HG, VH, TQ, tiles, slot_rows, workers;
-    size_t part_o, bytes;      // workspace: offset of the results behind the maxima and sums; size
+    bool rows;                   // a tile of rows for each wave
+    int NT, HG, VH, TQ, tiles, slot_rows, waves, blocks, no_cut, min_piece;
+    int64_t units;               // bound of the line's length
+    size_t part_at, part_bytes, lds, bytes;
 };
+
+// Most waves of a block where the waves share a tile: wide heads take more
+// registers than 8 waves have.
+constexpr int few_waves(int NP) { return NP <= 2 ? 8 : 4; }
 
 Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     Split p;
-    const int rep = n_heads / c.n_kv;
-    p.NT = (int64_t)b.max_q * rep <= 16 || c.head_pad > 128 ? 1 : 2;
-    const int RT = 16 * p.NT;
+    const int rep = n_heads / c.n_kv, NP = c.head_pad / 64;
+    const int64_t most_rows = (int64_t)b.max_q * rep;
+    p.rows = most_rows > 16;
+    p.NT = p.rows && most_rows > 64 && NP <= 2 ? 2 : 1;
+    const int RT = p.rows ? 64 * p.NT : 16;
     const int groups = (rep + RT - 1) / RT;
     p.HG = (rep + groups - 1) / groups;
     p.VH = c.n_kv * groups;
     p.TQ = RT / p.HG;
     p.tiles = (b.max_q + p.TQ - 1) / p.TQ;
     p.slot_rows = (p.TQ < b.max_q ? p.TQ : b.max_q) * p.HG;
-    const int64_t most = (int64_t)b.n_seq * p.VH * p.tiles * b.max_pages;
-    const int64_t cap = (int64_t)device_cus() * 8;
-    p.workers = (int)(most < cap ? most : cap);
-    const size_t rows = (size_t)p.workers * 2 * p.slot_rows;
-    p.part_o = align_up(rows * sizeof(float2), 256);
-    p.bytes = p.part_o + rows * c.head_pad * sizeof(float);
+    p.no_cut = p.rows ? 8 : 32;
+    p.min_piece = 8;
+    const size_t row = (size_t)(c.head_pad + 4) * sizeof(float);
+    p.waves = 4;
+    p.lds = 0;
+    if (!p.rows) {
+        p.waves = few_waves(NP);
+        while (p.waves * 2 * p.slot_rows * row > 150 * 1024) p.waves /= 2;
+        p.lds = p.waves * 2 * p.slot_rows * row;
+    }
+    if (p.lds < (size_t)p.waves * 64 * 32) p.lds = (size_t)p.waves * 64 * 32;     // the join of parts: 8 floats a thread
+    p.units = (int64_t)b.n_seq * p.VH * p.tiles;
+    p.units = p.units > 0x7fffffffll ? p.units : p.units * b.max_pages;
+    const int64_t most = p.units / p.min_piece + 1, cap = (int64_t)device_cus() * 2;
+    p.blocks = (int)(most < cap ? most : cap);
+    p.part_at = align_up((size_t)p.blocks * sizeof(unsigned long long), 256);
+    p.part_bytes = (size_t)p.blocks * 2 * p.slot_rows * row;
+    p.bytes = p.part_at + p.part_bytes;
     return p;
+}
+
+template <int KIND, int NP, int NT, bool ROWS, int kWaves>
+hipError_t attend_launch(const Attend& A, const Split& p, hipStream_t s) {
+    if (p.lds > 48 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void*)k_kv_attend<KIND, NP, NT, ROWS, kWaves>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((k_kv_attend<KIND, NP, NT, ROWS, kWaves>), dim3((uint32_t)p.blocks), dim3(64 * p.waves), p.lds, s, A);
+    return hipGetLastError();
 }
 
 template <int KIND, int NP>
 hipError_t attend_np(const Attend& A, const Split& p, hipStream_t s) {
-    const int64_t segs = (int64_t)A.b.n_seq * A.tiles * A.VH;
-    const int rb = p.NT == 1 ? p.slot_rows : 1;
-    if (segs * rb > 0x7fffffffll) return hipErrorInvalidConfiguration;
-    const dim3 grid((uint32_t)p.workers), join((uint32_t)(segs * rb));
-    if (p.NT == 1) {
-        hipLaunchKernelGGL((k_kv_attend<KIND, NP, 1>), grid, dim3(64), 0, s, A);
-        hipLaunchKernelGGL((k_kv_join<NP, 1>), join, dim3(256), 0, s, A, rb);
-    } else if constexpr (NP <= 2) {
-        hipLaunchKernelGGL((k_kv_attend<KIND, NP, 2>), grid, dim3(64), 0, s, A);
-        hipLaunchKernelGGL((k_kv_join<NP, 32>), join, dim3(256), 0, s, A, rb);
-    }
-    return hipGetLastError();
+    if (!p.rows) return attend_launch<KIND, NP, 1, false, few_waves(NP)>(A, p, s);
+    if constexpr (NP <= 2)
+        if (p.NT == 2) return attend_launch<KIND, NP, 2, true, 4>(A, p, s);
+    return attend_launch<KIND, NP, 1, true, 4>(A, p, s);
 }
 
 template <int KIND>
@@ -462,13 +723,14 @@ hipError_t attend_kind(const Attend& A, const Split& p, hipStream_t s) {
 }  // namespace
 
 size_t kv_attention_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
-    return align_up(split_of(c, b, n_heads).bytes + 1, 256);
+    return b.max_q > 0 ? align_up(split_of(c, b, n_heads).bytes, 256) : 256;
 }
 
 hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride,
                                int n_heads, float scale, int window, uint16_t* out, int64_t out_stride,
                                void* workspace, hipStream_t s) {
     const Split p = split_of(c, b, n_heads);
+    if (p.units > 0x7fffffffll) return hipErrorInvalidConfiguration;
     Attend A{};
     A.c = c;
     A.b = b;
@@ -476,8 +738,10 @@ hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, c
     A.out = out;
     A.qs = q_stride;
     A.os = out_stride;
-    A.part_ml = static_cast<float2*>(workspace);
-    A.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_o);
+    A.arrived = static_cast<unsigned long long*>(workspace);
+    A.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_at);
+    A.part_bytes = (uint32_t)p.part_bytes;
+    A.tag = next_call_tag();
     A.rep = n_heads / c.n_kv;
     A.window = window;
     A.HG = p.HG;
@@ -485,8 +749,10 @@ hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, c
     A.TQ = p.TQ;
     A.tiles = p.tiles;
     A.slot_rows = p.slot_rows;
-    A.workers = p.workers;
-    A.scale2 = scale * 1.4426950408889634f;
+    A.no_cut = p.no_cut;
+    A.min_piece = p.min_piece;
+    A.scale2 = fabsf(scale) * 1.4426950408889634f;
+    A.sign = scale < 0.f ? -1.f : 1.f;
     return c.kind == PROX_KV_INT8 ? attend_kind<PROX_KV_INT8>(A, p, s) : attend_kind<PROX_KV_FP8>(A, p, s);
 }
 

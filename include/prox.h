@@ -401,8 +401,9 @@ size_t prox_kv_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, i
  *            only: never read before the call wrote it.  Calls that share a
  *            workspace must not overlap in time.
  * Scores, softmax statistics and sums are fp32; a softmax weight is rounded to
- * bf16 for the product with the values, and the sum it is divided by is that
- * of the rounded weights. */
+ * fp16 for the product with the values, and the sum it is divided by is that
+ * of the rounded weights.  The batch's bounds multiplied (n_seq, n_heads,
+ * max_q / 16, max_pages) should stay below 2^31 (PROX_E_UNSUPPORTED otherwise). */
 prox_status prox_kv_attention(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
                               int32_t n_heads, float scale, int32_t window, void* out, int64_t out_stride,
                               void* workspace, size_t ws_bytes, void* stream);

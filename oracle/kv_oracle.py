@@ -159,23 +159,30 @@ def gather(cache: Cache, table, s, lo, hi):
 
 def attention(cache: Cache, table, ctx, q_start, max_q, q, scale, window=0, n_out=None):
     """q float64 [n_tokens][H][hd].  Returns (out, tol): float64 results (NaN on
-    rows that no sequence has) and a bound of the kernel's error at each:
+    rows that no sequence has) and a bound of the kernel's error at each.
 
-    Weights p_j are rounded to bf16, relative error at most u = 2^-8, and carry
-    the error eta of fp32 scores (hd + 8 roundings of 2^-24 of scale *
-    sum_d |q_d k_d|, as an absolute error of the exponent) and of exp2 (2^-21).
-    The result is the mean with the rounded weights' own sum below it, so with
-    relative errors e_j of the weights it moves by sum_j w_j e_j (v_j - o) to
-    first order.  fp32 sums over the keys add (n + 64) 2^-24 sum_j w_j |v_j|,
-    and the bf16 result is rounded by at most 2^-8 |o|.  A weight is relative to
-    the row's largest, 1, so the sum below it is at least 1; one under 2^-126 is
-    no normal fp32 number and may be taken as 0, which moves the result by at
-    most 2^-126 max|v| for each key."""
+    Weights p_j are rounded to fp16: relative error at most u = 2^-11, or 2^-33
+    of the largest weight where they are fp16 subnormals (they are held 2^8
+    larger).  The result is the mean with the rounded weights' own sum below it,
+    so relative errors e_j of the weights move it by sum_j w_j e_j (v_j - o) to
+    first order.  e_j also holds the score's error (of the exponent, absolute):
+      - fp32 sums of hd products: for e4m3 at most hd + 8 roundings of 2^-24 of
+        scale sum_d |q_d k_d|; for int8, whose codes are taken as 1024 + 128 + c
+        with -1152 sum(q) as start, hd / 2 roundings (a matrix instruction adds
+        32 products with no more than 8) of sums up to (1152 + 1279) sum(|q|)
+        units of the key's scale;
+      - q's channels below 2^-17 of the row's largest are off by 2^-25 of that;
+    and 2^-21 for exp2.  The sums over the keys: for int8 20 roundings a page of
+    sums up to (1152 + 1279) w_j units of the value's scale, and one rounding
+    of the running result a page, as for e4m3 (plus the products' own, 20).  The
+    bf16 result is rounded by at most 2^-8 |o|.  A weight under 2^-126 of the
+    row's largest is no normal fp32 number and may be taken as 0."""
     T, H, hd = q.shape
     out = np.full((T, H, hd), np.nan)
     tol = np.zeros((T, H, hd))
     rep = H // cache.n_kv
-    u = 2.0 ** -8
+    u, r24, big = 2.0 ** -11, 2.0 ** -24, 1152 + 1279
+    int8 = cache.kind == "int8"
     vals = {}
     for s, row, pos in rows_of(q_start, ctx, T, max_q):
         if pos < 0 or pos >= PAGE * table.shape[1]:
@@ -183,8 +190,10 @@ def attention(cache: Cache, table, ctx, q_start, max_q, q, scale, window=0, n_ou
             continue
         if s not in vals:
             last = min(int(ctx[s]), PAGE * table.shape[1])
-            vals[s] = gather(cache, table, s, 0, max(last, 1))
-        K, V, there = vals[s]
+            got = gather(cache, table, s, 0, max(last, 1))
+            page = np.where(got[2], table[s, np.arange(max(last, 1)) // PAGE], 0)
+            vals[s] = got + (cache.ks[page].astype(np.float64), cache.vs[page].astype(np.float64))
+        K, V, there, KS, VS = vals[s]
         lo = max(0, pos - window + 1) if window else 0
         see = np.flatnonzero(there[lo:pos + 1]) + lo
         if see.size == 0:
@@ -196,9 +205,18 @@ def attention(cache: Cache, table, ctx, q_start, max_q, q, scale, window=0, n_ou
             w = np.exp(z - z.max())
             w /= w.sum()
             o = w @ v
-            eta = (hd + 8) * 2.0 ** -24 * abs(scale) * (np.abs(k) @ np.abs(q[row, h])) + 2.0 ** -21
-            e = 1.02 * (u + eta)
+            aq = np.abs(q[row, h])
+            unit_k, unit_v = KS[see, h // rep], VS[see, h // rep]
+            if int8:
+                eta = hd / 2 * r24 * big * unit_k * aq.sum() + 8 * r24 * (np.abs(k) @ aq)
+            else:
+                eta = (hd + 8) * r24 * (np.abs(k) @ aq)
+            eta = abs(scale) * (eta + 2.0 ** -25 * aq.max() * np.abs(k).sum(-1)) + 2.0 ** -21
+            pages = see.size / PAGE + 2
+            sums = (pages + 20) * r24 * (w @ np.abs(v))
+            if int8:
+                sums = sums + 20 * r24 * big * (w @ unit_v)
             out[row, h] = o
-            tol[row, h] = (u * np.abs(o) + (w * e) @ np.abs(v - o) + (see.size + 64) * 2.0 ** -24 * (w @ np.abs(v))
-                           + see.size * 2.0 ** -126 * np.abs(v).max(0) + 1e-37)
+            tol[row, h] = (2.0 ** -8 * np.abs(o) + (w * (1.02 * (u + eta))) @ np.abs(v - o) + sums
+                           + see.size * 2.0 ** -33 * np.abs(v - o).max(0) + 1e-37)
     return out, tol

@@ -306,6 +306,27 @@ def test_attention_unwritten_slots_and_spread_values():
                 w.attend(b, start, scale=scale)
 
 
+def test_attention_many_tiny_weights_beside_a_large_one():
+    # one key with weight 1 and value 0, thousands of weight 2^-24 each: their
+    # sum, 2^-12, is the whole result
+    for kind in ("int8", "fp8"):
+        n, hd = 4097, 64
+        w = World(kind, 2, 1, hd, [n], seed=41)
+        k, v = torch.zeros(n, 1, hd, dtype=torch.bfloat16), w.rows(n, 1).cpu().abs() + 1
+        k[0, 0, 0] = 1.0
+        v[0] = 0
+        b, start = w.batch([n])
+        w.P.kv_append(w.c, b, k.cuda(), v.cuda())
+        KO.append(w.o, w.table, w.ctx, start, n, f64(k), f64(v))
+        w.same_cache()
+        q = torch.zeros(n, 2, hd, dtype=torch.bfloat16, device="cuda")
+        q[:, :, 0] = 1.0
+        for new in (1, 100):
+            b, start = w.batch([new], advance=False)
+            out, _ = w.attend(b, start, q=q[:new].clone(), scale=24.0 * float(np.log(2.0)))
+            assert float(out[-1].float().abs().min()) > 2e-4
+
+
 def test_attention_bad_query_stays_in_its_row():
     w = World("int8", 4, 1, 128, [200], seed=17)
     settle(w, [200])
