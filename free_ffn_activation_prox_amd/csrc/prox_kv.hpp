@@ -68,6 +68,14 @@ __device__ __forceinline__ uint32_t kv_codes4(const float x[4]) {
     }
 }
 
+// A load at an address that is the same for the whole wave, from memory that no
+// kernel of this call writes: through the constant address space it is a scalar
+// load, which vector loads in flight do not have to come back for.
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p) {
+    return *(const __attribute__((address_space(4))) T*)p;
+}
+
 // The rows of sequence s: rows q0 .. q0 + n - 1 (clamped to the batch), of
 // which the first `rows` are worked on; row i has position first + i.
 struct KvRows {

@@ -192,13 +192,6 @@ struct Line {
         p.begin = first + p.vh * p.pages;
         return p;
     }
-    // Where the piece that is cut at unit x begins in fact: behind the segment
-    // around x if that is a short one.
-    __device__ __forceinline__ int cut(int64_t x) {
-        if (x >= total) return total;
-        const Place p = at((int)x);
-        return x == p.begin || p.pages > A.no_cut ? (int)x : p.begin + p.pages;
-    }
 };
 
 // The segment after p.
@@ -263,29 +256,33 @@ struct Walk {
         const int groups = A.VH / A.c.n_kv, head = P.vh / groups, grp = P.vh % groups;
         const int32_t* table = A.b.block_table + (size_t)P.s * A.b.max_pages + T.pg0;
         const int ctx = T.R.first + T.R.n;                         // slots from here on hold no token
-        const uint8_t* kbase = static_cast<const uint8_t*>(A.c.k) + (size_t)head * kPageBytes + l * 16;
-        const uint8_t* vbase = static_cast<const uint8_t*>(A.c.v) + (size_t)head * kPageBytes + l * 16;
+        const uint8_t* kbase = static_cast<const uint8_t*>(A.c.k) + (size_t)head * kPageBytes;
+        const uint8_t* vbase = static_cast<const uint8_t*>(A.c.v) + (size_t)head * kPageBytes;
 
-        // a page of the segment, -1 where the table names none; its codes and scale
+        // A page of the segment, -1 where the table names none or the segment
+        // has none; its codes and scale.  A page that is not there is a buffer
+        // of no bytes: its loads return zeros and touch no memory, and the
+        // number of loads in flight is the same in every turn of the loop, so
+        // that waiting for V leaves the next page's K on its way.
         auto page_at = [&](int p) {
-            const int id = table[min(p, upto - 1)];
-            return id >= 0 && id < A.c.n_pages ? id : -1;
+            const int id = uniform_load(table + min(p, upto - 1));
+            return p < upto && id >= 0 && id < A.c.n_pages ? id : -1;
         };
         uint4 kf[4 * NP], vf[4 * NP];
         float ks, vs;
         auto load_k = [&](int page) {
             const size_t at = (size_t)max(page, 0) * A.c.n_kv;
-            const uint4* p = reinterpret_cast<const uint4*>(kbase + at * kPageBytes);
+            const __amdgpu_buffer_rsrc_t r = make_rsrc(kbase + at * kPageBytes, page >= 0 ? kPageBytes : 0);
 #pragma unroll
-            for (int d = 0; d < 4 * NP; ++d) kf[d] = p[d * 64];
-            ks = A.c.k_scale[at + head];
+            for (int d = 0; d < 4 * NP; ++d) kf[d] = buf_load16(r, l * 16, d * 1024);
+            ks = uniform_load(A.c.k_scale + at + head);
         };
         auto load_v = [&](int page) {
             const size_t at = (size_t)max(page, 0) * A.c.n_kv;
-            const uint4* p = reinterpret_cast<const uint4*>(vbase + at * kPageBytes);
+            const __amdgpu_buffer_rsrc_t r = make_rsrc(vbase + at * kPageBytes, page >= 0 ? kPageBytes : 0);
 #pragma unroll
-            for (int d = 0; d < 4 * NP; ++d) vf[d] = p[d * 64];
-            vs = A.c.v_scale[at + head];
+            for (int d = 0; d < 4 * NP; ++d) vf[d] = buf_load16(r, l * 16, d * 1024);
+            vs = uniform_load(A.c.v_scale + at + head);
         };
 
         int page = page_at(from), page_n = page_at(from + 1);
@@ -345,6 +342,7 @@ struct Walk {
 
         for (int p = from; p < upto; ++p) {
             load_v(page);
+            __builtin_amdgcn_sched_barrier(0);                      // on their way before the first product
             f32x4_t w[NT][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -362,12 +360,11 @@ struct Walk {
             }
             const float ks_p = ks;
             const int base_key = (T.pg0 + p) * kKvPage;
-            const bool gone = page < 0, clean = KIND == PROX_KV_FP8 && (gone || base_key + kKvPage > ctx);
-            if (p + 1 < upto) {                                     // the next page's keys while this one is weighed
-                page = page_n;
-                load_k(page);
-                page_n = page_at(p + 2);
-            }
+            const bool gone = page < 0, clean = KIND == PROX_KV_FP8 && base_key + kKvPage > ctx;
+            page = page_n;                                          // the next page's keys while this one is weighed
+            load_k(page);
+            page_n = page_at(p + 2);
+            __builtin_amdgcn_sched_barrier(0);
             // keys that a row does not see; most pages are seen whole by every row
             bool open = !gone;
 #pragma unroll
@@ -458,9 +455,10 @@ struct Walk {
 //   ROWS true: a tile of 16 NT rows for each wave; the waves walk the same pages.
 // Rows of cut segments go to the workspace.
 template <int KIND, int NP, int NT, bool ROWS, int kWaves>
-__global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
+__global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Attend A) {
     extern __shared__ __align__(16) float lds[];
-    __shared__ int tag_s[16];                     // segment (its first unit) of each wave's two slots, -1: none
+    __shared__ Place place_s[16];                 // segment of each wave's two slots, begin -1: none
+    __shared__ Place cut_s[2];                    // the segments that reach over the piece's begin and over its end
     __shared__ int done_s[2];
     constexpr int RW = 64 * NP + 4;               // floats of a row in a slot: result, maximum, sum
     constexpr int LPR = 16 * NP;                  // lanes of a row, four channels each
@@ -470,8 +468,27 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
     Line line(A, l);
     const int piece = (int)max((uint32_t)line.total / gridDim.x + 1, (uint32_t)A.min_piece);
     if ((int64_t)blockIdx.x * piece >= line.total) return;
-    const int b0 = line.cut((int64_t)blockIdx.x * piece), b1 = line.cut((int64_t)(blockIdx.x + 1) * piece);
-    if (b0 >= b1) return;
+    // where the piece begins and ends, and the place of this wave's first unit:
+    // one turn each of a loop that stays a loop (code that runs once is fetched once)
+    int b0 = 0, b1 = 0, x = 0, end = 0;
+    Place P;
+#pragma nounroll
+    for (int k = 0; k < 3; ++k) {
+        int64_t at = k < 2 ? ((int64_t)blockIdx.x + k) * piece : x;
+        if (at < line.total) {
+            P = line.at((int)at);
+            if (k < 2 && at != P.begin && P.pages <= A.no_cut) at = P.begin + P.pages;   // behind a short segment
+        } else {
+            at = line.total;
+        }
+        if (k == 0) b0 = (int)at;
+        if (k == 1) {
+            b1 = (int)at;
+            if (b0 >= b1) return;
+            x = ROWS ? b0 : b0 + (int)((int64_t)(b1 - b0) * wv / WV);
+            end = ROWS ? b1 : b0 + (int)((int64_t)(b1 - b0) * (wv + 1) / WV);
+        }
+    }
     const __amdgpu_buffer_rsrc_t rp = make_rsrc(A.part, A.part_bytes);
     bool sent = false;
     // a row of a part in the workspace: bytes
@@ -479,14 +496,9 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
         return ((2u * (uint32_t)block + (begins ? 1u : 0u)) * (uint32_t)A.slot_rows + (uint32_t)r) * (uint32_t)(RW * 4);
     };
 
-    int x = b0, end = b1;
-    if (!ROWS) {
-        x = b0 + (int)((int64_t)(b1 - b0) * wv / WV);
-        end = b0 + (int)((int64_t)(b1 - b0) * (wv + 1) / WV);
-        if (l < 2) tag_s[2 * wv + l] = -1;
-    }
+    if (!ROWS && l < 2) place_s[2 * wv + l].begin = -1;
+    if (threadIdx.x < 2) cut_s[threadIdx.x].begin = -1;
     if (x < end) {
-        Place P = line.at(x);
         Tile T = tile_of(A, P.s, P.t);
         for (;;) {
             const int from = x - P.begin, upto = min(P.pages, end - P.begin);
@@ -506,7 +518,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
                                 if (16 * d + 4 * g < hd) *reinterpret_cast<uint2*>(to + 16 * d + 4 * g) = bf16x4(w.o[u][d] * inv);
                     } else if (!ROWS) {
                         const int slot = 2 * wv + (from == 0 ? 1 : 0);
-                        if (l == 0) tag_s[slot] = P.begin;
+                        if (l == 0) place_s[slot] = P;
                         if (n < A.slot_rows) {
                             float* to = lds + (slot * A.slot_rows + n) * RW;
 #pragma unroll
@@ -526,7 +538,10 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
                     }
                 }
             }
-            if (ROWS) sent = sent || from != 0 || upto != P.pages;
+            if (ROWS && (from != 0 || upto != P.pages)) {
+                sent = true;
+                if (threadIdx.x == 0) cut_s[from != 0 ? 0 : 1] = P;
+            }
             x = P.begin + upto;
             if (x >= end) break;
             next_segment(A, P, T);
@@ -538,22 +553,21 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
         // together by all threads: thread = (row, four channels) of one of them.
         __syncthreads();
         for (int i = 0; i < 2 * WV;) {
-            const int tag = tag_s[i];
-            if (tag < 0) {
+            const Place P = place_s[i];
+            if (P.begin < 0) {
                 ++i;
                 continue;
             }
             int j = i + 1;
-            while (j < 2 * WV && (tag_s[j] < 0 || tag_s[j] == tag)) ++j;
-            const Place P = line.at(tag);
+            while (j < 2 * WV && (place_s[j].begin < 0 || place_s[j].begin == P.begin)) ++j;
             const Tile T = tile_of(A, P.s, P.t);
-            const bool whole = tag >= b0 && tag + P.pages <= b1;
+            const bool whole = P.begin >= b0 && P.begin + P.pages <= b1;
             for (int e = threadIdx.x; e < A.slot_rows * LPR; e += blockDim.x) {
                 const int r = e / LPR, c4 = 4 * (e % LPR);
                 float m = -INFINITY, sum = 0.f;
                 f32x4_t o = {0.f, 0.f, 0.f, 0.f};
                 for (int k = i; k < j; ++k) {
-                    if (tag_s[k] < 0) continue;
+                    if (place_s[k].begin < 0) continue;
                     const float* from = lds + (k * A.slot_rows + r) * RW;
                     const float2 ms = *reinterpret_cast<const float2*>(from + 64 * NP);
                     join(m, sum, o, ms.x, ms.y, *reinterpret_cast<const f32x4_t*>(from + c4));
@@ -562,7 +576,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
                     uint16_t* to = out_row(A, T, P.vh, r);
                     if (to && c4 < hd) *reinterpret_cast<uint2*>(to + c4) = bf16x4(o * inverse(sum));
                 } else {
-                    const uint32_t at = part_at(blockIdx.x, tag >= b0, r);
+                    const uint32_t at = part_at(blockIdx.x, P.begin >= b0, r);
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), rp, (int)(at + 4 * c4), 0, kCoherent);
                     if (c4 == 0) {
                         const u32x2_t ms = {__float_as_uint(m), __float_as_uint(sum)};
@@ -570,7 +584,10 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
                     }
                 }
             }
-            sent = sent || !whole;
+            if (!whole) {
+                sent = true;
+                if (threadIdx.x == 0) cut_s[P.begin < b0 ? 0 : 1] = P;
+            }
             i = j;
         }
     }
@@ -580,23 +597,22 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
     // that goes on behind it (the same one if it spans the piece).
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's stores have completed
     __syncthreads();
-    Place S[2];
-    bool have[2];
-    S[0] = line.at(b0);
-    have[0] = S[0].begin < b0;
-    S[1] = line.at(b1 - 1);
-    have[1] = S[1].begin >= b0 && S[1].begin + S[1].pages > b1;
-    if (threadIdx.x == 0)
-        for (int k = 0; k < 2; ++k)
-            if (have[k]) {
-                const int w0 = S[k].begin / piece, w1 = (S[k].begin + S[k].pages - 1) / piece;
-                done_s[k] = tile_arrive(A.arrived + w0, A.tag, w1 - w0 + 1);
-            }
+    if (threadIdx.x < 2) {
+        const Place S = cut_s[threadIdx.x];
+        int done = 0;
+        if (S.begin >= 0) {
+            const int w0 = S.begin / piece, w1 = (S.begin + S.pages - 1) / piece;
+            done = tile_arrive(A.arrived + w0, A.tag, w1 - w0 + 1);
+        }
+        done_s[threadIdx.x] = done;
+    }
     __syncthreads();
+#pragma nounroll
     for (int k = 0; k < 2; ++k) {
-        if (!have[k] || !done_s[k]) continue;
-        const Tile T = tile_of(A, S[k].s, S[k].t);
-        const int w0 = S[k].begin / piece, parts = (S[k].begin + S[k].pages - 1) / piece - w0 + 1;
+        if (!done_s[k]) continue;
+        const Place S = cut_s[k];
+        const Tile T = tile_of(A, S.s, S.t);
+        const int w0 = S.begin / piece, parts = (S.begin + S.pages - 1) / piece - w0 + 1;
         const int lanes = A.slot_rows * LPR;                            // (row, four channels)
         const int PG = max((int)blockDim.x / lanes, 1);                 // groups of parts, each in order
         __syncthreads();                                                // LDS is free
@@ -604,7 +620,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_attend(Attend A) {
             const int pg = PG > 1 ? (int)threadIdx.x / lanes : 0;
             const int e = PG > 1 ? (int)threadIdx.x % lanes : e0 + (int)threadIdx.x;
             const int r = e / LPR, c4 = 4 * (e % LPR);
-            uint16_t* to = e < lanes ? out_row(A, T, S[k].vh, r) : nullptr;    // a row that is not there was not stored
+            uint16_t* to = e < lanes ? out_row(A, T, S.vh, r) : nullptr;    // a row that is not there was not stored
             const bool in = to && pg < PG;
             float m = -INFINITY, sum = 0.f;
             f32x4_t o = {0.f, 0.f, 0.f, 0.f};
