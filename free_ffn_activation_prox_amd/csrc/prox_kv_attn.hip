@@ -110,6 +110,7 @@ struct Attend {
     float* part;                   // [blocks][2][slot_rows][head_pad + 4]: result, then maximum and sum
     uint32_t part_bytes, tag;
     int rep, window;
+    uint32_t HG_inv;       // 2^16 / HG, rounded up
     int HG, VH;            // query heads of a segment; segments of one tile of tokens (key heads x head groups)
     int TQ, tiles;         // tokens of a tile; most tiles of a sequence
     int slot_rows;
@@ -125,9 +126,9 @@ struct Tile {
     int pg0, pages;        // pages that some row sees: pg0 .. pg0 + pages - 1; at least one (0: no such tile)
 };
 
-__device__ __forceinline__ Tile tile_of(const Attend& A, int s, int t) {
+__device__ __forceinline__ Tile tile_of(const Attend& A, const KvRows& R, int t) {
     Tile x;
-    x.R = kv_rows(A.b, s);
+    x.R = R;
     x.i0 = t * A.TQ;
     x.n = min(x.R.rows - x.i0, A.TQ);
     const int cap = A.b.max_pages * kKvPage;
@@ -151,13 +152,23 @@ struct Place {
 struct Line {
     const Attend& A;
     int l, all, total;     // lane; tiles; units
-    int own, upto;         // this lane's tile of the last 64 looked at: its units, and those up to its end
+    KvRows R;              // this lane's tile of the last 64 looked at: its sequence's rows,
+    int pages, upto;       // its pages, and the units up to its end
 
     __device__ __forceinline__ void look(int j0, int base) {
         const int j = j0 + l;
-        own = 0;
-        if (j < all) own = (A.tiles == 1 ? tile_of(A, j, 0) : tile_of(A, j / A.tiles, j % A.tiles)).pages * A.VH;
-        upto = own;
+        R = KvRows{0, 0, 0, 0};
+        pages = 0;
+        if (j < all) {
+            int s = j, t = 0;
+            if (A.tiles > 1) {
+                s = (int)((uint32_t)j / (uint32_t)A.tiles);
+                t = j - s * A.tiles;
+            }
+            R = kv_rows(A.b, s);
+            pages = tile_of(A, R, t).pages;
+        }
+        upto = pages * A.VH;
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
             const int u = __shfl_up(upto, m);
@@ -173,7 +184,7 @@ struct Line {
         }
     }
     // x < total
-    __device__ __forceinline__ Place at(int x) {
+    __device__ __forceinline__ Place at(int x, Tile& T) {
         int base = 0, j0 = 0;
         if (all > 64)
             for (;; j0 += 64) {
@@ -182,14 +193,20 @@ struct Line {
                 base = __builtin_amdgcn_readlane(upto, 63);
             }
         const int on = __builtin_ctzll(__ballot(upto > x) | (1ull << 63));
-        const int units = __builtin_amdgcn_readlane(own, on), first = __builtin_amdgcn_readlane(upto, on) - units;
-        const uint32_t tile = (uint32_t)(j0 + on);
         Place p;
-        p.s = (int)(tile / (uint32_t)A.tiles);
-        p.t = (int)(tile % (uint32_t)A.tiles);
-        p.pages = (int)((uint32_t)units / (uint32_t)A.VH);
+        p.s = j0 + on;
+        p.t = 0;
+        if (A.tiles > 1) {
+            const uint32_t tile = (uint32_t)p.s;
+            p.s = (int)(tile / (uint32_t)A.tiles);
+            p.t = (int)tile - p.s * A.tiles;
+        }
+        p.pages = __builtin_amdgcn_readlane(pages, on);
+        const int first = __builtin_amdgcn_readlane(upto, on) - p.pages * A.VH;
         p.vh = (int)((uint32_t)(x - first) / (uint32_t)p.pages);
         p.begin = first + p.vh * p.pages;
+        T = tile_of(A, KvRows{__builtin_amdgcn_readlane(R.q0, on), __builtin_amdgcn_readlane(R.n, on),
+                              __builtin_amdgcn_readlane(R.rows, on), __builtin_amdgcn_readlane(R.first, on)}, p.t);
         return p;
     }
 };
@@ -204,7 +221,7 @@ __device__ __forceinline__ void next_segment(const Attend& A, Place& p, Tile& T)
             p.t = 0;
             ++p.s;
         }
-        T = tile_of(A, p.s, p.t);       // called where a segment follows
+        T = tile_of(A, kv_rows(A.b, p.s), p.t);      // called where a segment follows
     } while (T.pages == 0);
     p.pages = T.pages;
 }
@@ -230,13 +247,24 @@ __device__ __forceinline__ void join(float& m0, float& s0, f32x4_t& o, float m, 
     for (int r = 0; r < 4; ++r) o[r] = o[r] * f + v[r] * e;
 }
 
-// Where row r of segment (T, vh) goes: its output, or null for a row that the
-// segment does not have.
-__device__ __forceinline__ uint16_t* out_row(const Attend& A, const Tile& T, int vh, int r) {
-    const int groups = A.VH / A.c.n_kv, head = vh / groups, grp = vh % groups;
-    const int i = r / A.HG, hq = grp * A.HG + r % A.HG;
-    if (i >= T.n || hq >= A.rep) return nullptr;
-    return A.out + (int64_t)(T.R.q0 + T.i0 + i) * A.os + (int64_t)(head * A.rep + hq) * A.c.head_dim;
+// What the rows of a segment need to be put together later.
+struct Seg {
+    int begin, pages;      // units of the line
+    int vh, row0, n;       // key head and head group; rows of the batch row0 .. row0 + n - 1
+};
+__device__ __forceinline__ Seg seg_of(const Place& P, const Tile& T) {
+    return Seg{P.begin, P.pages, P.vh, T.R.q0 + T.i0, T.n};
+}
+
+// r / A.HG for r < 256 (HG <= 128: r times the rounding of 2^16 / HG stays below 2^16 / HG)
+__device__ __forceinline__ int token_of(const Attend& A, int r) { return (int)((uint32_t)r * A.HG_inv >> 16); }
+
+// Where row r of a segment goes, or null for a row that the segment does not have.
+__device__ __forceinline__ uint16_t* out_row(const Attend& A, const Seg& S, int r) {
+    const int groups = A.VH / A.c.n_kv, head = S.vh / groups, grp = S.vh - head * groups;
+    const int i = token_of(A, r), hq = grp * A.HG + r - i * A.HG;
+    if (i >= S.n || hq >= A.rep) return nullptr;
+    return A.out + (int64_t)(S.row0 + i) * A.os + (int64_t)(head * A.rep + hq) * A.c.head_dim;
 }
 
 // A weight's rows hold up to 2^(kTop + kSlack): see "Arithmetic" above.
@@ -253,11 +281,34 @@ struct Walk {
 
     __device__ __forceinline__ void run(const Attend& A, const Place& P, const Tile& T, int from, int upto, int r0, int l) {
         const int n = l & 15, g = l >> 4, hd = A.c.head_dim, cap = A.b.max_pages * kKvPage;
-        const int groups = A.VH / A.c.n_kv, head = P.vh / groups, grp = P.vh % groups;
+        const int groups = A.VH / A.c.n_kv, head = P.vh / groups, grp = P.vh - head * groups;
         const int32_t* table = A.b.block_table + (size_t)P.s * A.b.max_pages + T.pg0;
         const int ctx = T.R.first + T.R.n;                         // slots from here on hold no token
         const uint8_t* kbase = static_cast<const uint8_t*>(A.c.k) + (size_t)head * kPageBytes;
         const uint8_t* vbase = static_cast<const uint8_t*>(A.c.v) + (size_t)head * kPageBytes;
+
+        // The rows, and what they see.
+        int key_lo[NT], key_hi[NT];
+        uint4 q[NT][NP][2];
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const int r = r0 + 16 * u + n, k = token_of(A, r), i = T.i0 + k, hq = grp * A.HG + r - k * A.HG;
+            live[u] = k < T.n && hq < A.rep;
+            const int pos = T.R.first + i;
+            const bool sees = live[u] && pos >= 0 && pos < cap;
+            key_lo[u] = sees && A.window > 0 ? pos - A.window + 1 : 0;
+            key_hi[u] = sees ? pos + 1 : (live[u] ? 0 : 0x7fffffff);    // a row that is not there is not masked
+            const uint16_t* src = A.q + (int64_t)(T.R.q0 + (live[u] ? i : 0)) * A.qs +
+                                  (int64_t)(head * A.rep + (live[u] ? hq : 0)) * hd;
+#pragma unroll
+            for (int a = 0; a < NP; ++a)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int ch = 64 * a + 16 * g + 8 * e;
+                    q[u][a][e] = live[u] && ch < hd ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0, 0, 0, 0);
+                }
+        }
+        __builtin_amdgcn_sched_barrier(0);                          // q is on its way
 
         // A page of the segment, -1 where the table names none or the segment
         // has none; its codes and scale.  A page that is not there is a buffer
@@ -288,28 +339,18 @@ struct Walk {
         int page = page_at(from), page_n = page_at(from + 1);
         load_k(page);
 
-        // The rows: what they see, and q scaled to fp16.
-        int key_lo[NT], key_hi[NT];
-        uint4 q[NT][NP][2];
+        __builtin_amdgcn_sched_barrier(0);                          // and the first keys
+
+        // q scaled to fp16
         float row_scale[NT], bias[NT];
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const int r = r0 + 16 * u + n, i = T.i0 + r / A.HG, hq = grp * A.HG + r % A.HG;
-            live[u] = r / A.HG < T.n && hq < A.rep;
-            const int pos = T.R.first + i;
-            const bool sees = live[u] && pos >= 0 && pos < cap;
-            key_lo[u] = sees && A.window > 0 ? pos - A.window + 1 : 0;
-            key_hi[u] = sees ? pos + 1 : (live[u] ? 0 : 0x7fffffff);    // a row that is not there is not masked
-            const uint16_t* src = A.q + (int64_t)(T.R.q0 + (live[u] ? i : 0)) * A.qs +
-                                  (int64_t)(head * A.rep + (live[u] ? hq : 0)) * hd;
             uint32_t big = 0;
 #pragma unroll
             for (int a = 0; a < NP; ++a)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int ch = 64 * a + 16 * g + 8 * e;
-                    const uint4 x = live[u] && ch < hd ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0, 0, 0, 0);
-                    q[u][a][e] = x;
+                    const uint4 x = q[u][a][e];
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int f = 0; f < 4; ++f) big = max(big, max(w[f] & 0x7fff0000u, (w[f] << 16) & 0x7fff0000u));
@@ -457,8 +498,8 @@ struct Walk {
 template <int KIND, int NP, int NT, bool ROWS, int kWaves>
 __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Attend A) {
     extern __shared__ __align__(16) float lds[];
-    __shared__ Place place_s[16];                 // segment of each wave's two slots, begin -1: none
-    __shared__ Place cut_s[2];                    // the segments that reach over the piece's begin and over its end
+    __shared__ Seg seg_s[16];                     // segment of each wave's two slots, begin -1: none
+    __shared__ Seg cut_s[2];                      // the segments that reach over the piece's begin and over its end
     __shared__ int done_s[2];
     constexpr int RW = 64 * NP + 4;               // floats of a row in a slot: result, maximum, sum
     constexpr int LPR = 16 * NP;                  // lanes of a row, four channels each
@@ -472,11 +513,12 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
     // one turn each of a loop that stays a loop (code that runs once is fetched once)
     int b0 = 0, b1 = 0, x = 0, end = 0;
     Place P;
+    Tile T;
 #pragma nounroll
     for (int k = 0; k < 3; ++k) {
         int64_t at = k < 2 ? ((int64_t)blockIdx.x + k) * piece : x;
         if (at < line.total) {
-            P = line.at((int)at);
+            P = line.at((int)at, T);
             if (k < 2 && at != P.begin && P.pages <= A.no_cut) at = P.begin + P.pages;   // behind a short segment
         } else {
             at = line.total;
@@ -496,10 +538,9 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
         return ((2u * (uint32_t)block + (begins ? 1u : 0u)) * (uint32_t)A.slot_rows + (uint32_t)r) * (uint32_t)(RW * 4);
     };
 
-    if (!ROWS && l < 2) place_s[2 * wv + l].begin = -1;
+    if (!ROWS && l < 2) seg_s[2 * wv + l].begin = -1;
     if (threadIdx.x < 2) cut_s[threadIdx.x].begin = -1;
     if (x < end) {
-        Tile T = tile_of(A, P.s, P.t);
         for (;;) {
             const int from = x - P.begin, upto = min(P.pages, end - P.begin);
             const int r0 = ROWS ? 16 * NT * wv : 0;
@@ -510,7 +551,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                 for (int u = 0; u < NT; ++u) {
                     const int r = r0 + 16 * u + n;
                     if (from == 0 && upto == P.pages) {
-                        uint16_t* to = w.live[u] ? out_row(A, T, P.vh, r) : nullptr;
+                        uint16_t* to = w.live[u] ? out_row(A, seg_of(P, T), r) : nullptr;
                         const float inv = inverse(w.sum[u]);
                         if (to)
 #pragma unroll
@@ -518,7 +559,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                                 if (16 * d + 4 * g < hd) *reinterpret_cast<uint2*>(to + 16 * d + 4 * g) = bf16x4(w.o[u][d] * inv);
                     } else if (!ROWS) {
                         const int slot = 2 * wv + (from == 0 ? 1 : 0);
-                        if (l == 0) place_s[slot] = P;
+                        if (l == 0) seg_s[slot] = seg_of(P, T);
                         if (n < A.slot_rows) {
                             float* to = lds + (slot * A.slot_rows + n) * RW;
 #pragma unroll
@@ -540,7 +581,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
             }
             if (ROWS && (from != 0 || upto != P.pages)) {
                 sent = true;
-                if (threadIdx.x == 0) cut_s[from != 0 ? 0 : 1] = P;
+                if (threadIdx.x == 0) cut_s[from != 0 ? 0 : 1] = seg_of(P, T);
             }
             x = P.begin + upto;
             if (x >= end) break;
@@ -552,31 +593,37 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
         // The slots in order of position; neighbours of one segment are put
         // together by all threads: thread = (row, four channels) of one of them.
         __syncthreads();
-        for (int i = 0; i < 2 * WV;) {
-            const Place P = place_s[i];
-            if (P.begin < 0) {
-                ++i;
-                continue;
-            }
-            int j = i + 1;
-            while (j < 2 * WV && (place_s[j].begin < 0 || place_s[j].begin == P.begin)) ++j;
-            const Tile T = tile_of(A, P.s, P.t);
-            const bool whole = P.begin >= b0 && P.begin + P.pages <= b1;
+        const int begin = l < 2 * WV ? seg_s[l].begin : -1;
+        for (uint64_t left = __ballot(begin >= 0); left;) {
+            const int i = __builtin_ctzll(left);
+            const uint64_t same = __ballot(begin == __builtin_amdgcn_readlane(begin, i));
+            left &= ~same;
+            const int j = 64 - __builtin_clzll(same);               // slots i .. j - 1, empty ones between them
+            const Seg S = seg_s[i];
+            const bool whole = S.begin >= b0 && S.begin + S.pages <= b1;
             for (int e = threadIdx.x; e < A.slot_rows * LPR; e += blockDim.x) {
                 const int r = e / LPR, c4 = 4 * (e % LPR);
                 float m = -INFINITY, sum = 0.f;
                 f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-                for (int k = i; k < j; ++k) {
-                    if (place_s[k].begin < 0) continue;
-                    const float* from = lds + (k * A.slot_rows + r) * RW;
-                    const float2 ms = *reinterpret_cast<const float2*>(from + 64 * NP);
-                    join(m, sum, o, ms.x, ms.y, *reinterpret_cast<const f32x4_t*>(from + c4));
+                for (int k0 = i; k0 < j; k0 += 4) {
+                    float2 ms[4];
+                    f32x4_t v[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int k = (same >> (k0 + u)) & 1 ? k0 + u : i;
+                        const float* from = lds + (k * A.slot_rows + r) * RW;
+                        ms[u] = *reinterpret_cast<const float2*>(from + 64 * NP);
+                        v[u] = *reinterpret_cast<const f32x4_t*>(from + c4);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if ((same >> (k0 + u)) & 1) join(m, sum, o, ms[u].x, ms[u].y, v[u]);
                 }
                 if (whole) {
-                    uint16_t* to = out_row(A, T, P.vh, r);
+                    uint16_t* to = out_row(A, S, r);
                     if (to && c4 < hd) *reinterpret_cast<uint2*>(to + c4) = bf16x4(o * inverse(sum));
                 } else {
-                    const uint32_t at = part_at(blockIdx.x, P.begin >= b0, r);
+                    const uint32_t at = part_at(blockIdx.x, S.begin >= b0, r);
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), rp, (int)(at + 4 * c4), 0, kCoherent);
                     if (c4 == 0) {
                         const u32x2_t ms = {__float_as_uint(m), __float_as_uint(sum)};
@@ -586,9 +633,8 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
             }
             if (!whole) {
                 sent = true;
-                if (threadIdx.x == 0) cut_s[P.begin < b0 ? 0 : 1] = P;
+                if (threadIdx.x == 0) cut_s[S.begin < b0 ? 0 : 1] = S;
             }
-            i = j;
         }
     }
     if (!sent) return;                            // uniform over the block
@@ -598,7 +644,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's stores have completed
     __syncthreads();
     if (threadIdx.x < 2) {
-        const Place S = cut_s[threadIdx.x];
+        const Seg S = cut_s[threadIdx.x];
         int done = 0;
         if (S.begin >= 0) {
             const int w0 = S.begin / piece, w1 = (S.begin + S.pages - 1) / piece;
@@ -610,8 +656,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
 #pragma nounroll
     for (int k = 0; k < 2; ++k) {
         if (!done_s[k]) continue;
-        const Place S = cut_s[k];
-        const Tile T = tile_of(A, S.s, S.t);
+        const Seg S = cut_s[k];
         const int w0 = S.begin / piece, parts = (S.begin + S.pages - 1) / piece - w0 + 1;
         const int lanes = A.slot_rows * LPR;                            // (row, four channels)
         const int PG = max((int)blockDim.x / lanes, 1);                 // groups of parts, each in order
@@ -620,7 +665,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
             const int pg = PG > 1 ? (int)threadIdx.x / lanes : 0;
             const int e = PG > 1 ? (int)threadIdx.x % lanes : e0 + (int)threadIdx.x;
             const int r = e / LPR, c4 = 4 * (e % LPR);
-            uint16_t* to = e < lanes ? out_row(A, T, S.vh, r) : nullptr;    // a row that is not there was not stored
+            uint16_t* to = e < lanes ? out_row(A, S, r) : nullptr;    // a row that is not there was not stored
             const bool in = to && pg < PG;
             float m = -INFINITY, sum = 0.f;
             f32x4_t o = {0.f, 0.f, 0.f, 0.f};
@@ -699,7 +744,7 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     if (p.lds < (size_t)p.waves * 64 * 32) p.lds = (size_t)p.waves * 64 * 32;     // the join of parts: 8 floats a thread
     p.units = (int64_t)b.n_seq * p.VH * p.tiles;
     p.units = p.units > 0x7fffffffll ? p.units : p.units * b.max_pages;
-    const int64_t most = p.units / p.min_piece + 1, cap = (int64_t)device_cus() * 2;
+    const int64_t most = p.units / p.min_piece + 1, cap = (int64_t)device_cus() * (p.rows ? 2 : 1);
     p.blocks = (int)(most < cap ? most : cap);
     p.part_at = align_up((size_t)p.blocks * sizeof(unsigned long long), 256);
     p.part_bytes = (size_t)p.blocks * 2 * p.slot_rows * row;
@@ -761,6 +806,7 @@ hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, c
     A.rep = n_heads / c.n_kv;
     A.window = window;
     A.HG = p.HG;
+    A.HG_inv = (65536u + (uint32_t)p.HG - 1) / (uint32_t)p.HG;
     A.VH = p.VH;
     A.TQ = p.TQ;
     A.tiles = p.tiles;
