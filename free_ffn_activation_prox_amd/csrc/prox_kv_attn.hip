@@ -21,8 +21,13 @@
 //          of a row's largest.  The sum that the result is divided by is that
 //          of the rounded weights (a product with a row of constants), which
 //          keeps the result a weighted mean of the stored values.
-// m moves only when a score exceeds it by more than 2^6, so most pages rescale
-// nothing.
+//   sv     goes into the weights: p sv / s with s the largest sv so far, one
+//          more term of the exponent, so the values' sums stay in the matrix
+//          unit's accumulators from page to page; the sum of the weights takes
+//          it out again.  A page whose sv is below 2^-12 s takes a path of its
+//          own, since its weights would be fp16 subnormals.
+// m and s move only when a score exceeds m by more than 2^6 or an sv exceeds s,
+// so most pages rescale nothing.
 //
 // A wave takes tiles of 16 rows that share a key head and walks their pages.
 // With K as the A operand and q as B, lane (g = l / 16, n = l % 16) gets the
@@ -32,12 +37,13 @@
 // nothing but the row's maximum crosses lanes.
 //
 // How the work is split.  A segment is one tile of rows (TQ tokens x HG query
-// heads of one key head) with the pages that some row of it sees; all segments'
-// pages form one line, cut into pieces of equal length, one for each block,
-// whatever the lengths of the sequences.  A block finds its piece from the
-// lengths on the device (the host knows bounds only, and a captured call
-// follows the lengths).  A short segment is not cut: it belongs to the block in
-// whose piece it begins.  A long one that a cut divides leaves (maximum, sum,
+// heads of one key head) with the pages that some row of it sees.  All segments
+// form one line, a unit for each page and a few for what a segment costs by
+// itself, cut into pieces of equal length, one for each block, whatever the
+// lengths of the sequences.  A block finds its piece from the lengths on the
+// device (the host knows bounds only, and a captured call follows the lengths).
+// A cut moves to a segment's border where the segment is short or the border
+// near.  A segment that a cut divides leaves (maximum, sum,
 // unnormalised result) of each part in the workspace, at most two parts for
 // each block, and the block that arrives last combines them in order of
 // position, so results do not depend on timing.
@@ -110,11 +116,13 @@ struct Attend {
     float* part;                   // [blocks][2][slot_rows][head_pad + 4]: result, then maximum and sum
     uint32_t part_bytes, tag;
     int rep, window;
-    uint32_t HG_inv;       // 2^16 / HG, rounded up
+    uint32_t HG_inv;       // 2^17 / HG, rounded up
     int HG, VH;            // query heads of a segment; segments of one tile of tokens (key heads x head groups)
     int TQ, tiles;         // tokens of a tile; most tiles of a sequence
     int slot_rows;
-    int no_cut, min_piece; // pages of a segment up to which it is not cut; least length of a piece
+    int seg_cost;          // units of a segment besides its pages
+    int no_cut, min_part;  // pages of a segment up to which it is not cut, and least pages of a part
+    int min_piece;         // least length of a piece
     float scale2;          // |scale| * log2(e)
     float sign;            // that of scale
 };
@@ -146,7 +154,21 @@ struct Place {
     int s, t, vh, begin, pages;
 };
 
-// The line of all segments' pages (below 2^31, checked on the host), seen by
+// Where a cut at unit x falls that lies in a segment of `pages` pages beginning
+// at `begin`: there, or at the segment's nearer border.
+__device__ __forceinline__ int cut_in(const Attend& A, int x, int begin, int pages) {
+    const int d = x - begin, len = pages + A.seg_cost;
+    if (pages <= A.no_cut) return 2 * d < len ? begin : begin + len;
+    return d < A.seg_cost + A.min_part ? begin : d > len - A.min_part ? begin + len : x;
+}
+// The blocks w0 .. w1 that work on such a segment.
+__device__ __forceinline__ void blocks_of(const Attend& A, int piece, int begin, int pages, int& w0, int& w1) {
+    const int lo = begin + A.seg_cost + A.min_part, hi = begin + A.seg_cost + pages - A.min_part;   // cuts fall in lo .. hi
+    w0 = (lo + piece - 1) / piece - 1;
+    w1 = hi / piece;
+}
+
+// The line of all segments (below 2^31, checked on the host), seen by
 // one wave: 64 tiles at a time, tile j = sequence * A.tiles + tile of the
 // sequence, kept in registers where there are no more.
 struct Line {
@@ -168,7 +190,7 @@ struct Line {
             R = kv_rows(A.b, s);
             pages = tile_of(A, R, t).pages;
         }
-        upto = pages * A.VH;
+        upto = pages > 0 ? (pages + A.seg_cost) * A.VH : 0;
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
             const int u = __shfl_up(upto, m);
@@ -202,9 +224,9 @@ struct Line {
             p.t = (int)tile - p.s * A.tiles;
         }
         p.pages = __builtin_amdgcn_readlane(pages, on);
-        const int first = __builtin_amdgcn_readlane(upto, on) - p.pages * A.VH;
-        p.vh = (int)((uint32_t)(x - first) / (uint32_t)p.pages);
-        p.begin = first + p.vh * p.pages;
+        const int len = p.pages + A.seg_cost, first = __builtin_amdgcn_readlane(upto, on) - len * A.VH;
+        p.vh = (int)((uint32_t)(x - first) / (uint32_t)len);
+        p.begin = first + p.vh * len;
         T = tile_of(A, KvRows{__builtin_amdgcn_readlane(R.q0, on), __builtin_amdgcn_readlane(R.n, on),
                               __builtin_amdgcn_readlane(R.rows, on), __builtin_amdgcn_readlane(R.first, on)}, p.t);
         return p;
@@ -213,7 +235,7 @@ struct Line {
 
 // The segment after p.
 __device__ __forceinline__ void next_segment(const Attend& A, Place& p, Tile& T) {
-    p.begin += p.pages;
+    p.begin += p.pages + A.seg_cost;
     if (++p.vh < A.VH) return;
     p.vh = 0;
     do {
@@ -256,8 +278,8 @@ __device__ __forceinline__ Seg seg_of(const Place& P, const Tile& T) {
     return Seg{P.begin, P.pages, P.vh, T.R.q0 + T.i0, T.n};
 }
 
-// r / A.HG for r < 256 (HG <= 128: r times the rounding of 2^16 / HG stays below 2^16 / HG)
-__device__ __forceinline__ int token_of(const Attend& A, int r) { return (int)((uint32_t)r * A.HG_inv >> 16); }
+// r / A.HG for r < 256, HG <= 256: r times the rounding of 2^17 / HG stays below 2^17 / HG
+__device__ __forceinline__ int token_of(const Attend& A, int r) { return (int)((uint32_t)r * A.HG_inv >> 17); }
 
 // Where row r of a segment goes, or null for a row that the segment does not have.
 __device__ __forceinline__ uint16_t* out_row(const Attend& A, const Seg& S, int r) {
@@ -269,36 +291,34 @@ __device__ __forceinline__ uint16_t* out_row(const Attend& A, const Seg& S, int 
 
 // A weight's rows hold up to 2^(kTop + kSlack): see "Arithmetic" above.
 constexpr float kTop = 8.f, kSlack = 6.f;
+constexpr float kLeast = 0x1p-12f;     // least vs / s that goes into the weights
 
-// One wave's walk over pages `from` .. `upto` - 1 of a segment for the rows
-// r0 .. r0 + 16 NT - 1 of its tile.
+// The rows r0 .. r0 + 16 NT - 1 of a segment's tile in one wave: what they see,
+// q, and the running maxima, sums and results.
 template <int KIND, int NP, int NT>
-struct Walk {
-    static constexpr int kPageBytes = kKvPage * 64 * NP;
-    f32x4_t o[NT][4 * NP];      // lane (g, n): channels 16 d + 4 g + r of row 16 u + n
+struct Rows {
+    f32x4_t o[NT][4 * NP];      // lane (g, n): channels 16 d + 4 g + r of row 16 u + n, in units of s
     float m[NT], sum[NT];
+    float over[NT];             // int8: what the 1152 too many of the codes have added to every channel of o, negative
+    float s;                    // the largest scale of the values so far
     bool live[NT];
+    int key_lo[NT], key_hi[NT]; // positions that the row sees: key_lo .. key_hi - 1
+    uint4 q[NT][NP][2];
+    float row_scale[NT], bias[NT];
 
-    __device__ __forceinline__ void run(const Attend& A, const Place& P, const Tile& T, int from, int upto, int r0, int l) {
+    // Where the rows are, and their q on its way.
+    __device__ __forceinline__ void load(const Attend& A, const Seg& S, int pos0, int r0, int l) {
         const int n = l & 15, g = l >> 4, hd = A.c.head_dim, cap = A.b.max_pages * kKvPage;
-        const int groups = A.VH / A.c.n_kv, head = P.vh / groups, grp = P.vh - head * groups;
-        const int32_t* table = A.b.block_table + (size_t)P.s * A.b.max_pages + T.pg0;
-        const int ctx = T.R.first + T.R.n;                         // slots from here on hold no token
-        const uint8_t* kbase = static_cast<const uint8_t*>(A.c.k) + (size_t)head * kPageBytes;
-        const uint8_t* vbase = static_cast<const uint8_t*>(A.c.v) + (size_t)head * kPageBytes;
-
-        // The rows, and what they see.
-        int key_lo[NT], key_hi[NT];
-        uint4 q[NT][NP][2];
+        const int groups = A.VH / A.c.n_kv, head = S.vh / groups, grp = S.vh - head * groups;
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const int r = r0 + 16 * u + n, k = token_of(A, r), i = T.i0 + k, hq = grp * A.HG + r - k * A.HG;
-            live[u] = k < T.n && hq < A.rep;
-            const int pos = T.R.first + i;
+            const int r = r0 + 16 * u + n, i = token_of(A, r), hq = grp * A.HG + r - i * A.HG;
+            live[u] = i < S.n && hq < A.rep;
+            const int pos = pos0 + i;
             const bool sees = live[u] && pos >= 0 && pos < cap;
             key_lo[u] = sees && A.window > 0 ? pos - A.window + 1 : 0;
             key_hi[u] = sees ? pos + 1 : (live[u] ? 0 : 0x7fffffff);    // a row that is not there is not masked
-            const uint16_t* src = A.q + (int64_t)(T.R.q0 + (live[u] ? i : 0)) * A.qs +
+            const uint16_t* src = A.q + (int64_t)(S.row0 + (live[u] ? i : 0)) * A.qs +
                                   (int64_t)(head * A.rep + (live[u] ? hq : 0)) * hd;
 #pragma unroll
             for (int a = 0; a < NP; ++a)
@@ -308,41 +328,10 @@ struct Walk {
                     q[u][a][e] = live[u] && ch < hd ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0, 0, 0, 0);
                 }
         }
-        __builtin_amdgcn_sched_barrier(0);                          // q is on its way
+    }
 
-        // A page of the segment, -1 where the table names none or the segment
-        // has none; its codes and scale.  A page that is not there is a buffer
-        // of no bytes: its loads return zeros and touch no memory, and the
-        // number of loads in flight is the same in every turn of the loop, so
-        // that waiting for V leaves the next page's K on its way.
-        auto page_at = [&](int p) {
-            const int id = uniform_load(table + min(p, upto - 1));
-            return p < upto && id >= 0 && id < A.c.n_pages ? id : -1;
-        };
-        uint4 kf[4 * NP], vf[4 * NP];
-        float ks, vs;
-        auto load_k = [&](int page) {
-            const size_t at = (size_t)max(page, 0) * A.c.n_kv;
-            const __amdgpu_buffer_rsrc_t r = make_rsrc(kbase + at * kPageBytes, page >= 0 ? kPageBytes : 0);
-#pragma unroll
-            for (int d = 0; d < 4 * NP; ++d) kf[d] = buf_load16(r, l * 16, d * 1024);
-            ks = uniform_load(A.c.k_scale + at + head);
-        };
-        auto load_v = [&](int page) {
-            const size_t at = (size_t)max(page, 0) * A.c.n_kv;
-            const __amdgpu_buffer_rsrc_t r = make_rsrc(vbase + at * kPageBytes, page >= 0 ? kPageBytes : 0);
-#pragma unroll
-            for (int d = 0; d < 4 * NP; ++d) vf[d] = buf_load16(r, l * 16, d * 1024);
-            vs = uniform_load(A.c.v_scale + at + head);
-        };
-
-        int page = page_at(from), page_n = page_at(from + 1);
-        load_k(page);
-
-        __builtin_amdgcn_sched_barrier(0);                          // and the first keys
-
-        // q scaled to fp16
-        float row_scale[NT], bias[NT];
+    // q scaled to fp16; nothing seen yet.
+    __device__ __forceinline__ void begin(const Attend& A) {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             uint32_t big = 0;
@@ -376,117 +365,328 @@ struct Walk {
                 }
             bias[u] = b4[0];
             m[u] = -INFINITY;
-            sum[u] = 0.f;
+            sum[u] = over[u] = 0.f;
 #pragma unroll
             for (int d = 0; d < 4 * NP; ++d) o[u][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
+        s = 0.f;
+    }
 
-        for (int p = from; p < upto; ++p) {
-            load_v(page);
-            __builtin_amdgcn_sched_barrier(0);                      // on their way before the first product
-            f32x4_t w[NT][4];
+    // The scores of one page, in units of fac: keys(a, t, x, y) gives the two
+    // operands of channels 64 a and tokens 16 t.
+    template <typename K>
+    __device__ __forceinline__ void scores(f32x4_t (&w)[NT][4], K keys) const {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 4; ++t) {
 #pragma unroll
-                for (int u = 0; u < NT; ++u) w[u][t] = f32x4_t{bias[u], bias[u], bias[u], bias[u]};
+            for (int u = 0; u < NT; ++u) w[u][t] = f32x4_t{bias[u], bias[u], bias[u], bias[u]};
 #pragma unroll
-                for (int a = 0; a < NP; ++a) {
-                    const uint4 c = kf[a * 4 + t];
-                    const uint4 k0 = codes_f16<KIND>(c.x, c.y), k1 = codes_f16<KIND>(c.z, c.w);
+            for (int a = 0; a < NP; ++a) {
+                uint4 k0, k1;
+                keys(a, t, k0, k1);
 #pragma unroll
-                    for (int u = 0; u < NT; ++u) w[u][t] = mfma16(k0, q[u][a][0], w[u][t]);
+                for (int u = 0; u < NT; ++u) w[u][t] = mfma16(k0, q[u][a][0], w[u][t]);
 #pragma unroll
-                    for (int u = 0; u < NT; ++u) w[u][t] = mfma16(k1, q[u][a][1], w[u][t]);
-                }
+                for (int u = 0; u < NT; ++u) w[u][t] = mfma16(k1, q[u][a][1], w[u][t]);
             }
-            const float ks_p = ks;
-            const int base_key = (T.pg0 + p) * kKvPage;
-            const bool gone = page < 0, clean = KIND == PROX_KV_FP8 && base_key + kKvPage > ctx;
-            page = page_n;                                          // the next page's keys while this one is weighed
-            load_k(page);
-            page_n = page_at(p + 2);
-            __builtin_amdgcn_sched_barrier(0);
-            // keys that a row does not see; most pages are seen whole by every row
-            bool open = !gone;
+        }
+    }
+
+    // Masks the scores of positions base_key .. + 63 (none is seen if `gone`)
+    // and moves m and s where this page needs it.
+    __device__ __forceinline__ void limits(f32x4_t (&w)[NT][4], float (&fac)[NT], int base_key, bool gone, float ks, float vs,
+                                           int l) {
+        const int g = l >> 4;
+        // keys that a row does not see; most pages are seen whole by every row
+        bool open = !gone;
 #pragma unroll
-            for (int u = 0; u < NT; ++u) open = open && key_lo[u] <= base_key && key_hi[u] >= base_key + kKvPage;
-            if (__ballot(open) != ~0ull) {
-#pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    const int s_lo = key_lo[u] - base_key, s_hi = gone ? 0 : key_hi[u] - base_key;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int slot = 16 * t + 4 * g + r;
-                            w[u][t][r] = slot >= s_lo && slot < s_hi ? w[u][t][r] : -INFINITY;
-                        }
-                }
-            }
-            float fac[NT], top[NT];
-            bool grow = false;
+        for (int u = 0; u < NT; ++u) open = open && key_lo[u] <= base_key && key_hi[u] >= base_key + kKvPage;
+        if (__ballot(open) != ~0ull) {
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
-                // not 0 (a page of zeros): 0 x -inf would be NaN; the scores of such a page vanish all the same
-                fac[u] = fmaxf(ks_p * row_scale[u], 1e-37f);
-                float most = w[u][0][0];
-#pragma unroll
-                for (int e = 1; e < 16; ++e) most = fmaxf(most, w[u][e >> 2][e & 3]);
-                top[u] = over_groups_max(most) * fac[u];
-                grow = grow || top[u] > m[u] + kSlack;
-            }
-            if (__ballot(grow)) {
-#pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    const float mn = fmaxf(m[u], top[u]), base = mn > -INFINITY ? mn : 0.f;
-                    const float keep = __builtin_amdgcn_exp2f(m[u] - base);
-                    m[u] = mn;
-                    sum[u] *= keep;
-#pragma unroll
-                    for (int d = 0; d < 4 * NP; ++d) o[u][d] *= keep;
-                }
-            }
-            uint4 pw[NT][2];
-            f32x4_t start[NT];
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                const float base = (m[u] > -INFINITY ? m[u] : 0.f) - kTop;
-                uint32_t e[4][2];
+                const int s_lo = key_lo[u] - base_key, s_hi = gone ? 0 : key_hi[u] - base_key;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        e[t][r] = pack_f16(__builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r], fac[u], -base)),
-                                           __builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r + 1], fac[u], -base)));
-                pw[u][0] = make_uint4(e[0][0], e[0][1], e[1][0], e[1][1]);
-                pw[u][1] = make_uint4(e[2][0], e[2][1], e[3][0], e[3][1]);
-                f32x4_t c = {0.f, 0.f, 0.f, 0.f};
-                c = mfma16(constants<KIND>(), pw[u][0], c);
-                c = mfma16(constants<KIND>(), pw[u][1], c);
-                if constexpr (KIND == PROX_KV_INT8) {
-                    sum[u] = fmaf(c[0], -1.f / 1152.f, sum[u]);
-                    start[u] = c;
-                } else {
-                    sum[u] += c[0];
-                    start[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                }
+                    for (int r = 0; r < 4; ++r) {
+                        const int slot = 16 * t + 4 * g + r;
+                        w[u][t][r] = slot >= s_lo && slot < s_hi ? w[u][t][r] : -INFINITY;
+                    }
+            }
+        }
+        float top[NT];
+        bool grow = vs > s;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            // not 0 (a page of zeros): 0 x -inf would be NaN; the scores of such a page vanish all the same
+            fac[u] = fmaxf(ks * row_scale[u], 1e-37f);
+            float most = w[u][0][0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) most = fmaxf(most, w[u][e >> 2][e & 3]);
+            top[u] = over_groups_max(most) * fac[u];
+            grow = grow || top[u] > m[u] + kSlack;
+        }
+        if (__ballot(grow)) {
+            const float sn = fmaxf(s, vs), f = sn > 0.f ? s / sn : 1.f;
+            s = sn;
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const float mn = fmaxf(m[u], top[u]), base = mn > -INFINITY ? mn : 0.f;
+                const float keep = __builtin_amdgcn_exp2f(m[u] - base);
+                m[u] = mn;
+                sum[u] *= keep;
+                over[u] *= keep * f;
+#pragma unroll
+                for (int d = 0; d < 4 * NP; ++d) o[u][d] *= keep * f;
+            }
+        }
+    }
+
+    // The weights of a page, 2^shift times what m says, as operands; c: what
+    // the product with the constants gives.
+    __device__ __forceinline__ void weights(const f32x4_t (&w)[NT][4], const float (&fac)[NT], float shift, uint4 (&pw)[NT][2]) const {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const float base = (m[u] > -INFINITY ? m[u] : 0.f) - shift;
+            uint32_t e[4][2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    e[t][r] = pack_f16(__builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r], fac[u], -base)),
+                                       __builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r + 1], fac[u], -base)));
+            pw[u][0] = make_uint4(e[0][0], e[0][1], e[1][0], e[1][1]);
+            pw[u][1] = make_uint4(e[2][0], e[2][1], e[3][0], e[3][1]);
+        }
+    }
+    __device__ __forceinline__ f32x4_t of_constants(const uint4 (&pw)[2]) const {
+        f32x4_t c = {0.f, 0.f, 0.f, 0.f};
+        c = mfma16(constants<KIND>(), pw[0], c);
+        return mfma16(constants<KIND>(), pw[1], c);
+    }
+
+    // The values of a page: vals(d, x, y) gives the two operands of channels 16 d.
+    // `ratio` = vs / s, of which the weights hold `held` (1 or ratio).
+    template <typename V>
+    __device__ __forceinline__ void values(const uint4 (&pw)[NT][2], float ratio, V vals) {
+        constexpr float kUnit = KIND == PROX_KV_INT8 ? -1.f / 1152.f : 1.f;
+        if (ratio >= kLeast) {
+            const float back = kUnit / ratio;
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const float c = of_constants(pw[u])[0];
+                sum[u] = fmaf(c, back, sum[u]);
+                if constexpr (KIND == PROX_KV_INT8) over[u] += c;
             }
 #pragma unroll
             for (int d = 0; d < 4 * NP; ++d) {
-                uint4 c = vf[d];
-                if (clean) c = make_uint4(no_nan_fp8(c.x), no_nan_fp8(c.y), no_nan_fp8(c.z), no_nan_fp8(c.w));
-                const uint4 v0 = codes_f16<KIND>(c.x, c.y), v1 = codes_f16<KIND>(c.z, c.w);
+                uint4 v0, v1;
+                vals(d, v0, v1);
+#pragma unroll
+                for (int u = 0; u < NT; ++u) o[u][d] = mfma16(v0, pw[u][0], o[u][d]);
+#pragma unroll
+                for (int u = 0; u < NT; ++u) o[u][d] = mfma16(v1, pw[u][1], o[u][d]);
+            }
+        } else {
+            float c[NT];
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                c[u] = of_constants(pw[u])[0];
+                sum[u] = fmaf(c[u], kUnit, sum[u]);
+                if constexpr (KIND == PROX_KV_INT8) over[u] = fmaf(c[u], ratio, over[u]);
+            }
+#pragma unroll
+            for (int d = 0; d < 4 * NP; ++d) {
+                uint4 v0, v1;
+                vals(d, v0, v1);
 #pragma unroll
                 for (int u = 0; u < NT; ++u) {
-                    f32x4_t acc = mfma16(v0, pw[u][0], start[u]);
+                    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+                    acc = mfma16(v0, pw[u][0], acc);
                     acc = mfma16(v1, pw[u][1], acc);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[u][d][r] = fmaf(acc[r], vs, o[u][d][r]);
+                    for (int r = 0; r < 4; ++r) o[u][d][r] = fmaf(acc[r], ratio, o[u][d][r]);
                 }
             }
         }
     }
+    // vs / s, and what the weights' exponents take of it: all of it down to 2^-12.
+    __device__ __forceinline__ float ratio_of(float vs) const { return s > 0.f ? vs / s : 0.f; }
+    static __device__ __forceinline__ float shift_of(float ratio) { return kTop + (ratio >= kLeast ? __builtin_amdgcn_logf(ratio) : 0.f); }
+
+    // The results in their own units, behind the last page.
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int d = 0; d < 4 * NP; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[u][d][r] = (o[u][d][r] + over[u]) * s;
+    }
 };
+
+// Pages of one segment for one wave.  A page that is not there (the table
+// names none, or the segment has none) is a buffer of no bytes: its loads
+// return zeros and touch no memory, and the number of loads in flight is the
+// same in every turn of a loop.
+template <int NP>
+struct Pages {
+    static constexpr int kBytes = kKvPage * 64 * NP;
+    const Attend& A;
+    const int32_t* table;
+    int head, upto;
+    __device__ __forceinline__ Pages(const Attend& a, const Place& P, const Tile& T, int up)
+        : A(a), table(a.b.block_table + (size_t)P.s * a.b.max_pages + T.pg0), head(P.vh / (a.VH / a.c.n_kv)), upto(up) {}
+    __device__ __forceinline__ int at(int p) const {
+        const int id = uniform_load(table + min(p, upto - 1));
+        return p < upto && id >= 0 && id < A.c.n_pages ? id : -1;
+    }
+    __device__ __forceinline__ size_t where(int page) const { return (size_t)max(page, 0) * A.c.n_kv + head; }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t codes(const void* base, int page) const {
+        return make_rsrc(static_cast<const uint8_t*>(base) + where(page) * kBytes, page >= 0 ? kBytes : 0);
+    }
+    __device__ __forceinline__ float k_scale(int page) const { return uniform_load(A.c.k_scale + where(page)); }
+    __device__ __forceinline__ float v_scale(int page) const { return uniform_load(A.c.v_scale + where(page)); }
+};
+
+// One wave walks pages from .. upto - 1 by itself: the next page's keys are
+// loaded while this one is weighed, its values while its keys are multiplied.
+template <int KIND, int NP, int NT>
+__device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& A, const Place& P, const Tile& T, int from,
+                                           int upto, int r0, int l) {
+    const Pages<NP> pages(A, P, T, upto);
+    const int ctx = T.R.first + T.R.n;                             // slots from here on hold no token
+    w.load(A, seg_of(P, T), T.R.first + T.i0, r0, l);
+    __builtin_amdgcn_sched_barrier(0);                              // q is on its way
+    uint4 kf[4 * NP], vf[4 * NP];
+    float ks, vs;
+    auto load_k = [&](int page) {
+        const __amdgpu_buffer_rsrc_t r = pages.codes(A.c.k, page);
+#pragma unroll
+        for (int d = 0; d < 4 * NP; ++d) kf[d] = buf_load16(r, l * 16, d * 1024);
+        ks = pages.k_scale(page);
+    };
+    int page = pages.at(from), page_n = pages.at(from + 1);
+    load_k(page);
+    __builtin_amdgcn_sched_barrier(0);                              // and the first keys
+    w.begin(A);
+    for (int p = from; p < upto; ++p) {
+        const __amdgpu_buffer_rsrc_t r = pages.codes(A.c.v, page);
+#pragma unroll
+        for (int d = 0; d < 4 * NP; ++d) vf[d] = buf_load16(r, l * 16, d * 1024);
+        vs = pages.v_scale(page);
+        __builtin_amdgcn_sched_barrier(0);                          // on their way before the first product
+        const int base_key = (T.pg0 + p) * kKvPage;
+        const bool gone = page < 0, clean = KIND == PROX_KV_FP8 && base_key + kKvPage > ctx;
+        f32x4_t sc[NT][4];
+        float fac[NT];
+        w.scores(sc, [&](int a, int t, uint4& x, uint4& y) {
+            const uint4 c = kf[a * 4 + t];
+            x = codes_f16<KIND>(c.x, c.y);
+            y = codes_f16<KIND>(c.z, c.w);
+        });
+        const float ks_p = ks;
+        page = page_n;
+        load_k(page);
+        page_n = pages.at(p + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        w.limits(sc, fac, base_key, gone, ks_p, vs, l);
+        const float ratio = w.ratio_of(vs);
+        uint4 pw[NT][2];
+        w.weights(sc, fac, w.shift_of(ratio), pw);
+        w.values(pw, ratio, [&](int d, uint4& x, uint4& y) {
+            uint4 c = vf[d];
+            if (clean) c = make_uint4(no_nan_fp8(c.x), no_nan_fp8(c.y), no_nan_fp8(c.z), no_nan_fp8(c.w));
+            x = codes_f16<KIND>(c.x, c.y);
+            y = codes_f16<KIND>(c.z, c.w);
+        });
+    }
+    w.finish();
+}
+
+// The waves of a block walk the same pages, each for its own rows.  A page is
+// loaded once for the block, each wave turning its share of the codes to fp16
+// operands in LDS (two pages' worth: one is filled while the other is used),
+// so a page costs the block one barrier.
+// LDS: keys [2][4 NP x 2 operands][64] uint4, values the same.
+template <int KIND, int NP, int NT, int kWaves>
+__device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds, const Attend& A, const Place& P,
+                                              const Tile& T, int from, int upto, int wv, int l) {
+    constexpr int kChunks = 4 * NP;                                 // kilobytes of codes of K, and of V
+    constexpr int kOwn = (kChunks + kWaves - 1) / kWaves;           // a wave's: chunks wv, wv + kWaves, ...
+    constexpr int kSize = kChunks * 128;                            // uint4 of a page's operands
+    const Pages<NP> pages(A, P, T, upto);
+    const int ctx = T.R.first + T.R.n;
+    const int r0 = 16 * NT * wv;
+    const bool busy = r0 < T.n * A.HG;                              // a wave without rows only fills
+    w.load(A, seg_of(P, T), T.R.first + T.i0, r0, l);
+    uint4* const kl = lds + l;
+    uint4* const vl = lds + 2 * kSize + l;
+    uint4 kc[kOwn], vc[kOwn];
+    auto load = [&](uint4 (&c)[kOwn], const void* base, int page) {
+        const __amdgpu_buffer_rsrc_t r = pages.codes(base, page);
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            const int ch = wv + j * kWaves;                         // past the last chunk: past the buffer, zeros
+            c[j] = buf_load16(r, l * 16 + ch * 1024, 0);
+        }
+    };
+    auto fill = [&](uint4* to, const uint4 (&c)[kOwn], bool clean) {
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            const int ch = wv + j * kWaves;
+            if (kChunks % kWaves && ch >= kChunks) continue;
+            uint4 x = c[j];
+            if (clean) x = make_uint4(no_nan_fp8(x.x), no_nan_fp8(x.y), no_nan_fp8(x.z), no_nan_fp8(x.w));
+            to[(2 * ch) * 64] = codes_f16<KIND>(x.x, x.y);
+            to[(2 * ch + 1) * 64] = codes_f16<KIND>(x.z, x.w);
+        }
+    };
+    auto unclean = [&](int p) { return KIND == PROX_KV_FP8 && (T.pg0 + p + 1) * kKvPage > ctx; };
+    int page = pages.at(from), page_n = pages.at(from + 1);
+    load(kc, A.c.k, page);
+    load(vc, A.c.v, page);
+    float ks = pages.k_scale(page), vs = pages.v_scale(page);
+    w.begin(A);
+    lds_barrier();                                                  // the last segment's pages are done with
+    fill(kl, kc, false);
+    load(kc, A.c.k, page_n);
+    fill(vl, vc, unclean(from));
+    load(vc, A.c.v, page_n);
+    lds_barrier();
+    for (int p = from; p < upto; ++p) {
+        const int buf = (p - from) & 1;
+        const int page_nn = pages.at(p + 2);
+        const float ks_n = pages.k_scale(page_n), vs_n = pages.v_scale(page_n);
+        if (busy) {
+            f32x4_t sc[NT][4];
+            float fac[NT];
+            w.scores(sc, [&](int a, int t, uint4& x, uint4& y) {
+                x = kl[buf * kSize + (2 * (a * 4 + t)) * 64];
+                y = kl[buf * kSize + (2 * (a * 4 + t) + 1) * 64];
+            });
+            w.limits(sc, fac, (T.pg0 + p) * kKvPage, page < 0, ks, vs, l);
+            const float ratio = w.ratio_of(vs);
+            uint4 pw[NT][2];
+            w.weights(sc, fac, w.shift_of(ratio), pw);
+            w.values(pw, ratio, [&](int d, uint4& x, uint4& y) {
+                x = vl[buf * kSize + (2 * d) * 64];
+                y = vl[buf * kSize + (2 * d + 1) * 64];
+            });
+        }
+        // the other half was used a turn ago
+        fill(vl + (buf ^ 1) * kSize, vc, unclean(p + 1));
+        load(vc, A.c.v, page_nn);
+        fill(kl + (buf ^ 1) * kSize, kc, false);
+        load(kc, A.c.k, page_nn);
+        page = page_n;
+        page_n = page_nn;
+        ks = ks_n;
+        vs = vs_n;
+        lds_barrier();
+    }
+    w.finish();
+}
 
 // Blocks of up to kWaves waves.
 //   ROWS false (a tile of 16 rows at most): the waves cut the block's piece
@@ -519,7 +719,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
         int64_t at = k < 2 ? ((int64_t)blockIdx.x + k) * piece : x;
         if (at < line.total) {
             P = line.at((int)at, T);
-            if (k < 2 && at != P.begin && P.pages <= A.no_cut) at = P.begin + P.pages;   // behind a short segment
+            if (k < 2) at = cut_in(A, (int)at, P.begin, P.pages);
         } else {
             at = line.total;
         }
@@ -542,11 +742,14 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
     if (threadIdx.x < 2) cut_s[threadIdx.x].begin = -1;
     if (x < end) {
         for (;;) {
-            const int from = x - P.begin, upto = min(P.pages, end - P.begin);
+            const int first = P.begin + A.seg_cost;                 // the unit of page 0
+            const int from = max(x - first, 0), upto = min(P.pages, end - first);
+            if (ROWS || from < upto) {
             const int r0 = ROWS ? 16 * NT * wv : 0;
-            Walk<KIND, NP, NT> w;
+            Rows<KIND, NP, NT> w;
+            if constexpr (ROWS) walk_together<KIND, NP, NT, kWaves>(w, reinterpret_cast<uint4*>(lds), A, P, T, from, upto, wv, l);
+            else walk_alone<KIND, NP, NT>(w, A, P, T, from, upto, 0, l);
             if (!ROWS || r0 < T.n * A.HG) {
-                w.run(A, P, T, from, upto, r0, l);
 #pragma unroll
                 for (int u = 0; u < NT; ++u) {
                     const int r = r0 + 16 * u + n;
@@ -583,7 +786,8 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                 sent = true;
                 if (threadIdx.x == 0) cut_s[from != 0 ? 0 : 1] = seg_of(P, T);
             }
-            x = P.begin + upto;
+            }
+            x = first + P.pages;
             if (x >= end) break;
             next_segment(A, P, T);
         }
@@ -600,7 +804,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
             left &= ~same;
             const int j = 64 - __builtin_clzll(same);               // slots i .. j - 1, empty ones between them
             const Seg S = seg_s[i];
-            const bool whole = S.begin >= b0 && S.begin + S.pages <= b1;
+            const bool whole = S.begin >= b0 && S.begin + S.pages + A.seg_cost <= b1;
             for (int e = threadIdx.x; e < A.slot_rows * LPR; e += blockDim.x) {
                 const int r = e / LPR, c4 = 4 * (e % LPR);
                 float m = -INFINITY, sum = 0.f;
@@ -647,7 +851,8 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
         const Seg S = cut_s[threadIdx.x];
         int done = 0;
         if (S.begin >= 0) {
-            const int w0 = S.begin / piece, w1 = (S.begin + S.pages - 1) / piece;
+            int w0, w1;
+            blocks_of(A, piece, S.begin, S.pages, w0, w1);
             done = tile_arrive(A.arrived + w0, A.tag, w1 - w0 + 1);
         }
         done_s[threadIdx.x] = done;
@@ -657,51 +862,81 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
     for (int k = 0; k < 2; ++k) {
         if (!done_s[k]) continue;
         const Seg S = cut_s[k];
-        const int w0 = S.begin / piece, parts = (S.begin + S.pages - 1) / piece - w0 + 1;
-        const int lanes = A.slot_rows * LPR;                            // (row, four channels)
-        const int PG = max((int)blockDim.x / lanes, 1);                 // groups of parts, each in order
+        int w0, w1;
+        blocks_of(A, piece, S.begin, S.pages, w0, w1);
+        const int parts = w1 - w0 + 1;
+        const int lanes = A.slot_rows * LPR, bd = blockDim.x;           // (row, four channels)
+        auto load = [&](int p, int e, u32x4_t& v, u32x2_t& ms) {
+            const uint32_t at = part_at(w0 + p, p == 0, e / LPR);
+            v = __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 16 * (e % LPR)), 0, kCoherent);
+            ms = __builtin_amdgcn_raw_buffer_load_b64(rp, (int)(at + 256 * NP), 0, kCoherent);
+        };
+        auto store = [&](int e, f32x4_t o, float sum) {
+            uint16_t* to = out_row(A, S, e / LPR);
+            if (to && 4 * (e % LPR) < hd) *reinterpret_cast<uint2*>(to + 4 * (e % LPR)) = bf16x4(o * inverse(sum));
+        };
+        if (2 * lanes > bd) {
+            // many rows and few parts: a thread joins four (row, four channels) at once
+            for (int e0 = threadIdx.x; e0 < lanes; e0 += 4 * bd) {
+                float m[4], sum[4];
+                f32x4_t o[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    m[u] = -INFINITY;
+                    sum[u] = 0.f;
+                    o[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                }
+                for (int p0 = 0; p0 < parts; p0 += 2) {
+                    u32x4_t v[2][4];
+                    u32x2_t ms[2][4];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) load(min(p0 + q, parts - 1), min(e0 + u * bd, lanes - 1), v[q][u], ms[q][u]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (p0 + q < parts)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                join(m[u], sum[u], o[u], __uint_as_float(ms[q][u].x), __uint_as_float(ms[q][u].y),
+                                     __builtin_bit_cast(f32x4_t, v[q][u]));
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (e0 + u * bd < lanes) store(e0 + u * bd, o[u], sum[u]);
+            }
+            continue;
+        }
+        // few rows and many parts: groups of threads take parts in order, eight at once, then the groups are joined
+        const int PG = bd / lanes, pg = (int)threadIdx.x / lanes, e = (int)threadIdx.x % lanes;
+        float m = -INFINITY, sum = 0.f;
+        f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+        if (pg < PG) {
+            const int pe = (pg + 1) * parts / PG;
+            for (int p0 = pg * parts / PG; p0 < pe; p0 += 8) {
+                u32x4_t v[8];
+                u32x2_t ms[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) load(min(p0 + u, pe - 1), e, v[u], ms[u]);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (p0 + u < pe)
+                        join(m, sum, o, __uint_as_float(ms[u].x), __uint_as_float(ms[u].y), __builtin_bit_cast(f32x4_t, v[u]));
+            }
+        }
         __syncthreads();                                                // LDS is free
-        for (int e0 = 0; e0 < lanes; e0 += blockDim.x) {
-            const int pg = PG > 1 ? (int)threadIdx.x / lanes : 0;
-            const int e = PG > 1 ? (int)threadIdx.x % lanes : e0 + (int)threadIdx.x;
-            const int r = e / LPR, c4 = 4 * (e % LPR);
-            uint16_t* to = e < lanes ? out_row(A, S, r) : nullptr;    // a row that is not there was not stored
-            const bool in = to && pg < PG;
-            float m = -INFINITY, sum = 0.f;
-            f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-            if (in) {
-                const int pe = (pg + 1) * parts / PG;
-                for (int p0 = pg * parts / PG; p0 < pe; p0 += 8) {
-                    u32x4_t v[8];
-                    u32x2_t ms[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int p = min(p0 + u, pe - 1);
-                        const uint32_t at = part_at(w0 + p, p == 0, r);
-                        v[u] = __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 4 * c4), 0, kCoherent);
-                        ms[u] = __builtin_amdgcn_raw_buffer_load_b64(rp, (int)(at + 256 * NP), 0, kCoherent);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        if (p0 + u < pe)
-                            join(m, sum, o, __uint_as_float(ms[u].x), __uint_as_float(ms[u].y), __builtin_bit_cast(f32x4_t, v[u]));
-                }
+        if (pg < PG) {
+            *reinterpret_cast<f32x4_t*>(lds + threadIdx.x * 8) = o;
+            *reinterpret_cast<float2*>(lds + threadIdx.x * 8 + 4) = make_float2(m, sum);
+        }
+        __syncthreads();
+        if (pg == 0) {
+            for (int u = 1; u < PG; ++u) {
+                const float* from = lds + (u * lanes + e) * 8;
+                const float2 ms = *reinterpret_cast<const float2*>(from + 4);
+                join(m, sum, o, ms.x, ms.y, *reinterpret_cast<const f32x4_t*>(from));
             }
-            if (PG > 1) {
-                float* mine = lds + (pg * lanes + e) * 8;
-                if (in) {
-                    *reinterpret_cast<f32x4_t*>(mine) = o;
-                    *reinterpret_cast<float2*>(mine + 4) = make_float2(m, sum);
-                }
-                __syncthreads();
-                if (in && pg == 0)
-                    for (int u = 1; u < PG; ++u) {
-                        const float* from = lds + (u * lanes + e) * 8;
-                        const float2 ms = *reinterpret_cast<const float2*>(from + 4);
-                        join(m, sum, o, ms.x, ms.y, *reinterpret_cast<const f32x4_t*>(from));
-                    }
-            }
-            if (in && pg == 0 && c4 < hd) *reinterpret_cast<uint2*>(to + c4) = bf16x4(o * inverse(sum));
+            store(e, o, sum);
         }
     }
 }
@@ -709,7 +944,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
 // How a call is split (host): a function of the bounds that the batch gives.
 struct Split {
     bool rows;                   // a tile of rows for each wave
-    int NT, HG, VH, TQ, tiles, slot_rows, waves, blocks, no_cut, min_piece;
+    int NT, HG, VH, TQ, tiles, slot_rows, waves, blocks, seg_cost, no_cut, min_part, min_piece;
     int64_t units;               // bound of the line's length
     size_t part_at, part_bytes, lds, bytes;
 };
@@ -717,34 +952,36 @@ struct Split {
 // Most waves of a block where the waves share a tile: wide heads take more
 // registers than 8 waves have.
 constexpr int few_waves(int NP) { return NP <= 2 ? 8 : 4; }
+constexpr int kRowWaves = 8;     // waves of a block where each has rows of its own
 
 Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     Split p;
     const int rep = n_heads / c.n_kv, NP = c.head_pad / 64;
     const int64_t most_rows = (int64_t)b.max_q * rep;
     p.rows = most_rows > 16;
-    p.NT = p.rows && most_rows > 64 && NP <= 2 ? 2 : 1;
-    const int RT = p.rows ? 64 * p.NT : 16;
+    p.waves = p.rows ? kRowWaves : few_waves(NP);
+    p.NT = p.rows && most_rows > 16 * kRowWaves && NP <= 2 ? 2 : 1;
+    const int RT = p.rows ? 16 * p.NT * kRowWaves : 16;
     const int groups = (rep + RT - 1) / RT;
     p.HG = (rep + groups - 1) / groups;
     p.VH = c.n_kv * groups;
     p.TQ = RT / p.HG;
     p.tiles = (b.max_q + p.TQ - 1) / p.TQ;
     p.slot_rows = (p.TQ < b.max_q ? p.TQ : b.max_q) * p.HG;
-    p.no_cut = p.rows ? 8 : 32;
+    p.seg_cost = p.rows ? 3 : 1;
+    p.no_cut = p.rows ? 12 : 32;
+    p.min_part = p.rows ? 4 : 8;
     p.min_piece = 8;
     const size_t row = (size_t)(c.head_pad + 4) * sizeof(float);
-    p.waves = 4;
-    p.lds = 0;
+    p.lds = 32 * 1024 * (size_t)NP;                     // two pages of fp16 operands
     if (!p.rows) {
-        p.waves = few_waves(NP);
         while (p.waves * 2 * p.slot_rows * row > 150 * 1024) p.waves /= 2;
         p.lds = p.waves * 2 * p.slot_rows * row;
     }
     if (p.lds < (size_t)p.waves * 64 * 32) p.lds = (size_t)p.waves * 64 * 32;     // the join of parts: 8 floats a thread
     p.units = (int64_t)b.n_seq * p.VH * p.tiles;
-    p.units = p.units > 0x7fffffffll ? p.units : p.units * b.max_pages;
-    const int64_t most = p.units / p.min_piece + 1, cap = (int64_t)device_cus() * (p.rows ? 2 : 1);
+    p.units = p.units > 0x7fffffffll ? p.units : p.units * (b.max_pages + p.seg_cost);
+    const int64_t most = p.units / p.min_piece + 1, cap = (int64_t)device_cus() * 1;
     p.blocks = (int)(most < cap ? most : cap);
     p.part_at = align_up((size_t)p.blocks * sizeof(unsigned long long), 256);
     p.part_bytes = (size_t)p.blocks * 2 * p.slot_rows * row;
@@ -767,8 +1004,8 @@ template <int KIND, int NP>
 hipError_t attend_np(const Attend& A, const Split& p, hipStream_t s) {
     if (!p.rows) return attend_launch<KIND, NP, 1, false, few_waves(NP)>(A, p, s);
     if constexpr (NP <= 2)
-        if (p.NT == 2) return attend_launch<KIND, NP, 2, true, 4>(A, p, s);
-    return attend_launch<KIND, NP, 1, true, 4>(A, p, s);
+        if (p.NT == 2) return attend_launch<KIND, NP, 2, true, kRowWaves>(A, p, s);
+    return attend_launch<KIND, NP, 1, true, kRowWaves>(A, p, s);
 }
 
 template <int KIND>
@@ -806,12 +1043,14 @@ hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, c
     A.rep = n_heads / c.n_kv;
     A.window = window;
     A.HG = p.HG;
-    A.HG_inv = (65536u + (uint32_t)p.HG - 1) / (uint32_t)p.HG;
+    A.HG_inv = (131072u + (uint32_t)p.HG - 1) / (uint32_t)p.HG;
     A.VH = p.VH;
     A.TQ = p.TQ;
     A.tiles = p.tiles;
     A.slot_rows = p.slot_rows;
+    A.seg_cost = p.seg_cost;
     A.no_cut = p.no_cut;
+    A.min_part = p.min_part;
     A.min_piece = p.min_piece;
     A.scale2 = fabsf(scale) * 1.4426950408889634f;
     A.sign = scale < 0.f ? -1.f : 1.f;
