@@ -21,13 +21,15 @@
 //          of a row's largest.  The sum that the result is divided by is that
 //          of the rounded weights (a product with a row of constants), which
 //          keeps the result a weighted mean of the stored values.
-//   sv     goes into the weights: p sv / s with s the largest sv so far, one
+//   sv     goes into the weights: p sv / s with s the unit of the sums, one
 //          more term of the exponent, so the values' sums stay in the matrix
 //          unit's accumulators from page to page; the sum of the weights takes
-//          it out again.  A page whose sv is below 2^-12 s takes a path of its
-//          own, since its weights would be fp16 subnormals.
-// m and s move only when a score exceeds m by more than 2^6 or an sv exceeds s,
-// so most pages rescale nothing.
+//          it out again.  s moves where sv / s leaves 2^-12 .. 1, for below that
+//          the weights would be fp16 subnormals (down by 2^80 at most at once:
+//          what values so much smaller than others add may be off by 2^-85 of
+//          the larger ones).
+// m and s move only when a score exceeds m by more than 2^6 or an sv leaves its
+// range, so most pages rescale nothing.
 //
 // A wave takes tiles of 16 rows that share a key head and walks their pages.
 // With K as the A operand and q as B, lane (g = l / 16, n = l % 16) gets the
@@ -300,7 +302,7 @@ struct Rows {
     f32x4_t o[NT][4 * NP];      // lane (g, n): channels 16 d + 4 g + r of row 16 u + n, in units of s
     float m[NT], sum[NT];
     float over[NT];             // int8: what the 1152 too many of the codes have added to every channel of o, negative
-    float s;                    // the largest scale of the values so far
+    float s;                    // unit of o
     bool live[NT];
     int key_lo[NT], key_hi[NT]; // positions that the row sees: key_lo .. key_hi - 1
     uint4 q[NT][NP][2];
@@ -415,7 +417,7 @@ struct Rows {
             }
         }
         float top[NT];
-        bool grow = vs > s;
+        bool grow = vs > s || (vs > 0.f && vs < s * kLeast);
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             // not 0 (a page of zeros): 0 x -inf would be NaN; the scores of such a page vanish all the same
@@ -427,7 +429,7 @@ struct Rows {
             grow = grow || top[u] > m[u] + kSlack;
         }
         if (__ballot(grow)) {
-            const float sn = fmaxf(s, vs), f = sn > 0.f ? s / sn : 1.f;
+            const float sn = vs > s || (vs > 0.f && vs < s * kLeast) ? fmaxf(vs, s * 0x1p-80f) : s, f = sn > 0.f ? s / sn : 1.f;
             s = sn;
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
@@ -465,54 +467,87 @@ struct Rows {
         return mfma16(constants<KIND>(), pw[1], c);
     }
 
-    // The values of a page: vals(d, x, y) gives the two operands of channels 16 d.
-    // `ratio` = vs / s, of which the weights hold `held` (1 or ratio).
+    // The values of a page: vals(d, x, y) gives the two operands of channels
+    // 16 d; the weights hold `ratio`.
     template <typename V>
     __device__ __forceinline__ void values(const uint4 (&pw)[NT][2], float ratio, V vals) {
-        constexpr float kUnit = KIND == PROX_KV_INT8 ? -1.f / 1152.f : 1.f;
-        if (ratio >= kLeast) {
-            const float back = kUnit / ratio;
+        weigh(pw, ratio);
 #pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                const float c = of_constants(pw[u])[0];
-                sum[u] = fmaf(c, back, sum[u]);
-                if constexpr (KIND == PROX_KV_INT8) over[u] += c;
-            }
+        for (int d = 0; d < 4 * NP; ++d) {
+            uint4 v0, v1;
+            vals(d, v0, v1);
 #pragma unroll
-            for (int d = 0; d < 4 * NP; ++d) {
-                uint4 v0, v1;
-                vals(d, v0, v1);
+            for (int u = 0; u < NT; ++u) o[u][d] = mfma16(v0, pw[u][0], o[u][d]);
 #pragma unroll
-                for (int u = 0; u < NT; ++u) o[u][d] = mfma16(v0, pw[u][0], o[u][d]);
-#pragma unroll
-                for (int u = 0; u < NT; ++u) o[u][d] = mfma16(v1, pw[u][1], o[u][d]);
-            }
-        } else {
-            float c[NT];
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                c[u] = of_constants(pw[u])[0];
-                sum[u] = fmaf(c[u], kUnit, sum[u]);
-                if constexpr (KIND == PROX_KV_INT8) over[u] = fmaf(c[u], ratio, over[u]);
-            }
-#pragma unroll
-            for (int d = 0; d < 4 * NP; ++d) {
-                uint4 v0, v1;
-                vals(d, v0, v1);
-#pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-                    acc = mfma16(v0, pw[u][0], acc);
-                    acc = mfma16(v1, pw[u][1], acc);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[u][d][r] = fmaf(acc[r], ratio, o[u][d][r]);
-                }
-            }
+            for (int u = 0; u < NT; ++u) o[u][d] = mfma16(v1, pw[u][1], o[u][d]);
         }
     }
-    // vs / s, and what the weights' exponents take of it: all of it down to 2^-12.
-    __device__ __forceinline__ float ratio_of(float vs) const { return s > 0.f ? vs / s : 0.f; }
-    static __device__ __forceinline__ float shift_of(float ratio) { return kTop + (ratio >= kLeast ? __builtin_amdgcn_logf(ratio) : 0.f); }
+    // scores() and values() from operands in LDS (k, v: this lane's of operand
+    // 0, 64 apart): the next few are read before the products of the last few,
+    // since a read takes as long as eight products.
+    static constexpr int kFew = 2 * NP;
+    static __device__ __forceinline__ void fetch(uint4 (&f)[kFew], const uint4* at) {
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) f[i] = at[i * 64];
+    }
+    __device__ __forceinline__ void scores_lds(f32x4_t (&w)[NT][4], const uint4* k) const {
+        uint4 f[2][kFew];
+        // operand 2 (a 4 + t) + e of the keys: those of one t, for all a
+        auto read = [&](int t) {
+#pragma unroll
+            for (int a = 0; a < NP; ++a)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) f[t & 1][2 * a + e] = k[(2 * (a * 4 + t) + e) * 64];
+        };
+        read(0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (t < 3) read(t + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < NT; ++u) w[u][t] = f32x4_t{bias[u], bias[u], bias[u], bias[u]};
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+#pragma unroll
+                for (int u = 0; u < NT; ++u) w[u][t] = mfma16(f[t & 1][i], q[u][i >> 1][i & 1], w[u][t]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // first: the first kFew operands, read before
+    __device__ __forceinline__ void values_lds(const uint4 (&pw)[NT][2], float ratio, const uint4* v, const uint4 (&first)[kFew]) {
+        uint4 f[2][kFew];
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) f[0][i] = first[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                   // channels 16 NP j ..
+            if (j < 3) fetch(f[(j + 1) & 1], v + (j + 1) * kFew * 64);
+            __builtin_amdgcn_sched_barrier(0);
+            if (j == 0) weigh(pw, ratio);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int u = 0; u < NT; ++u)
+                        o[u][j * NP + i] = mfma16(f[j & 1][2 * i + e], pw[u][e], o[u][j * NP + i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // The weights' own sums.
+    __device__ __forceinline__ void weigh(const uint4 (&pw)[NT][2], float ratio) {
+        const float back = (KIND == PROX_KV_INT8 ? -1.f / 1152.f : 1.f) * __builtin_amdgcn_rcpf(ratio);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const float c = of_constants(pw[u])[0];
+            sum[u] = fmaf(c, back, sum[u]);
+            if constexpr (KIND == PROX_KV_INT8) over[u] += c;
+        }
+    }
+    // vs / s as the weights take it (a page of zeros takes none of it).
+    __device__ __forceinline__ float ratio_of(float vs) const {
+        return vs > 0.f ? fmaxf(vs * __builtin_amdgcn_rcpf(s), kLeast) : 1.f;
+    }
+    static __device__ __forceinline__ float shift_of(float ratio) { return kTop + __builtin_amdgcn_logf(ratio); }
 
     // The results in their own units, behind the last page.
     __device__ __forceinline__ void finish() {
@@ -528,25 +563,42 @@ struct Rows {
 // Pages of one segment for one wave.  A page that is not there (the table
 // names none, or the segment has none) is a buffer of no bytes: its loads
 // return zeros and touch no memory, and the number of loads in flight is the
-// same in every turn of a loop.
+// same in every turn of a loop.  Lane i keeps what the table and the scales
+// say of page base + i: a turn of a loop reads a lane and waits for no memory
+// (scalar loads would hold up every wait for LDS, which counts them too).
 template <int NP>
 struct Pages {
     static constexpr int kBytes = kKvPage * 64 * NP;
     const Attend& A;
     const int32_t* table;
-    int head, upto;
-    __device__ __forceinline__ Pages(const Attend& a, const Place& P, const Tile& T, int up)
-        : A(a), table(a.b.block_table + (size_t)P.s * a.b.max_pages + T.pg0), head(P.vh / (a.VH / a.c.n_kv)), upto(up) {}
-    __device__ __forceinline__ int at(int p) const {
-        const int id = uniform_load(table + min(p, upto - 1));
-        return p < upto && id >= 0 && id < A.c.n_pages ? id : -1;
+    int head, upto, base, id;
+    float ks, vs;
+    __device__ __forceinline__ Pages(const Attend& a, const Place& P, const Tile& T, int from, int up, int l)
+        : A(a), table(a.b.block_table + (size_t)P.s * a.b.max_pages + T.pg0), head(P.vh / (a.VH / a.c.n_kv)), upto(up) {
+        look(from, l);
+    }
+    __device__ __forceinline__ void look(int p, int l) {
+        base = p;
+        id = table[min(p + l, upto - 1)];
+        id = p + l < upto && id >= 0 && id < A.c.n_pages ? id : -1;
+        ks = A.c.k_scale[where(id)];
+        vs = A.c.v_scale[where(id)];
+    }
+    // pages p .. p + 2 are looked at next
+    __device__ __forceinline__ void follow(int p, int l) {
+        if (p + 2 >= base + 64) look(p, l);
+    }
+    __device__ __forceinline__ int at(int p) const { return __builtin_amdgcn_readlane(id, p - base); }
+    __device__ __forceinline__ float k_scale(int p) const {
+        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), p - base));
+    }
+    __device__ __forceinline__ float v_scale(int p) const {
+        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), p - base));
     }
     __device__ __forceinline__ size_t where(int page) const { return (size_t)max(page, 0) * A.c.n_kv + head; }
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t codes(const void* base, int page) const {
-        return make_rsrc(static_cast<const uint8_t*>(base) + where(page) * kBytes, page >= 0 ? kBytes : 0);
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t codes(const void* at, int page) const {
+        return make_rsrc(static_cast<const uint8_t*>(at) + where(page) * kBytes, page >= 0 ? kBytes : 0);
     }
-    __device__ __forceinline__ float k_scale(int page) const { return uniform_load(A.c.k_scale + where(page)); }
-    __device__ __forceinline__ float v_scale(int page) const { return uniform_load(A.c.v_scale + where(page)); }
 };
 
 // One wave walks pages from .. upto - 1 by itself: the next page's keys are
@@ -554,30 +606,25 @@ struct Pages {
 template <int KIND, int NP, int NT>
 __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& A, const Place& P, const Tile& T, int from,
                                            int upto, int r0, int l) {
-    const Pages<NP> pages(A, P, T, upto);
+    Pages<NP> pages(A, P, T, from, upto, l);
     const int ctx = T.R.first + T.R.n;                             // slots from here on hold no token
     w.load(A, seg_of(P, T), T.R.first + T.i0, r0, l);
-    __builtin_amdgcn_sched_barrier(0);                              // q is on its way
     uint4 kf[4 * NP], vf[4 * NP];
-    float ks, vs;
-    auto load_k = [&](int page) {
-        const __amdgpu_buffer_rsrc_t r = pages.codes(A.c.k, page);
+    auto load = [&](uint4 (&f)[4 * NP], const void* base, int page) {
+        const __amdgpu_buffer_rsrc_t r = pages.codes(base, page);
 #pragma unroll
-        for (int d = 0; d < 4 * NP; ++d) kf[d] = buf_load16(r, l * 16, d * 1024);
-        ks = pages.k_scale(page);
+        for (int d = 0; d < 4 * NP; ++d) f[d] = buf_load16(r, l * 16, d * 1024);
     };
-    int page = pages.at(from), page_n = pages.at(from + 1);
-    load_k(page);
-    __builtin_amdgcn_sched_barrier(0);                              // and the first keys
+    load(kf, A.c.k, pages.at(from));
+    __builtin_amdgcn_sched_barrier(0);                              // q and the first keys are on their way
     w.begin(A);
     for (int p = from; p < upto; ++p) {
-        const __amdgpu_buffer_rsrc_t r = pages.codes(A.c.v, page);
-#pragma unroll
-        for (int d = 0; d < 4 * NP; ++d) vf[d] = buf_load16(r, l * 16, d * 1024);
-        vs = pages.v_scale(page);
-        __builtin_amdgcn_sched_barrier(0);                          // on their way before the first product
+        pages.follow(p, l);
+        const int page = pages.at(p);
+        load(vf, A.c.v, page);
+        __builtin_amdgcn_sched_barrier(0);                          // before the first product
         const int base_key = (T.pg0 + p) * kKvPage;
-        const bool gone = page < 0, clean = KIND == PROX_KV_FP8 && base_key + kKvPage > ctx;
+        const bool clean = KIND == PROX_KV_FP8 && base_key + kKvPage > ctx;
         f32x4_t sc[NT][4];
         float fac[NT];
         w.scores(sc, [&](int a, int t, uint4& x, uint4& y) {
@@ -585,12 +632,10 @@ __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& 
             x = codes_f16<KIND>(c.x, c.y);
             y = codes_f16<KIND>(c.z, c.w);
         });
-        const float ks_p = ks;
-        page = page_n;
-        load_k(page);
-        page_n = pages.at(p + 2);
+        load(kf, A.c.k, pages.at(p + 1));
         __builtin_amdgcn_sched_barrier(0);
-        w.limits(sc, fac, base_key, gone, ks_p, vs, l);
+        const float vs = pages.v_scale(p);
+        w.limits(sc, fac, base_key, page < 0, pages.k_scale(p), vs, l);
         const float ratio = w.ratio_of(vs);
         uint4 pw[NT][2];
         w.weights(sc, fac, w.shift_of(ratio), pw);
@@ -615,7 +660,7 @@ __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds,
     constexpr int kChunks = 4 * NP;                                 // kilobytes of codes of K, and of V
     constexpr int kOwn = (kChunks + kWaves - 1) / kWaves;           // a wave's: chunks wv, wv + kWaves, ...
     constexpr int kSize = kChunks * 128;                            // uint4 of a page's operands
-    const Pages<NP> pages(A, P, T, upto);
+    Pages<NP> pages(A, P, T, from, upto, l);
     const int ctx = T.R.first + T.R.n;
     const int r0 = 16 * NT * wv;
     const bool busy = r0 < T.n * A.HG;                              // a wave without rows only fills
@@ -643,46 +688,36 @@ __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds,
         }
     };
     auto unclean = [&](int p) { return KIND == PROX_KV_FP8 && (T.pg0 + p + 1) * kKvPage > ctx; };
-    int page = pages.at(from), page_n = pages.at(from + 1);
-    load(kc, A.c.k, page);
-    load(vc, A.c.v, page);
-    float ks = pages.k_scale(page), vs = pages.v_scale(page);
+    load(kc, A.c.k, pages.at(from));
+    load(vc, A.c.v, pages.at(from));
     w.begin(A);
     lds_barrier();                                                  // the last segment's pages are done with
     fill(kl, kc, false);
-    load(kc, A.c.k, page_n);
+    load(kc, A.c.k, pages.at(from + 1));
     fill(vl, vc, unclean(from));
-    load(vc, A.c.v, page_n);
+    load(vc, A.c.v, pages.at(from + 1));
     lds_barrier();
     for (int p = from; p < upto; ++p) {
         const int buf = (p - from) & 1;
-        const int page_nn = pages.at(p + 2);
-        const float ks_n = pages.k_scale(page_n), vs_n = pages.v_scale(page_n);
+        pages.follow(p, l);
         if (busy) {
             f32x4_t sc[NT][4];
             float fac[NT];
-            w.scores(sc, [&](int a, int t, uint4& x, uint4& y) {
-                x = kl[buf * kSize + (2 * (a * 4 + t)) * 64];
-                y = kl[buf * kSize + (2 * (a * 4 + t) + 1) * 64];
-            });
-            w.limits(sc, fac, (T.pg0 + p) * kKvPage, page < 0, ks, vs, l);
+            w.scores_lds(sc, kl + buf * kSize);
+            uint4 first[Rows<KIND, NP, NT>::kFew];
+            w.fetch(first, vl + buf * kSize);
+            const float vs = pages.v_scale(p);
+            w.limits(sc, fac, (T.pg0 + p) * kKvPage, pages.at(p) < 0, pages.k_scale(p), vs, l);
             const float ratio = w.ratio_of(vs);
             uint4 pw[NT][2];
             w.weights(sc, fac, w.shift_of(ratio), pw);
-            w.values(pw, ratio, [&](int d, uint4& x, uint4& y) {
-                x = vl[buf * kSize + (2 * d) * 64];
-                y = vl[buf * kSize + (2 * d + 1) * 64];
-            });
+            w.values_lds(pw, ratio, vl + buf * kSize, first);
         }
         // the other half was used a turn ago
         fill(vl + (buf ^ 1) * kSize, vc, unclean(p + 1));
-        load(vc, A.c.v, page_nn);
+        load(vc, A.c.v, pages.at(p + 2));
         fill(kl + (buf ^ 1) * kSize, kc, false);
-        load(kc, A.c.k, page_nn);
-        page = page_n;
-        page_n = page_nn;
-        ks = ks_n;
-        vs = vs_n;
+        load(kc, A.c.k, pages.at(p + 2));
         lds_barrier();
     }
     w.finish();
@@ -981,7 +1016,7 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     if (p.lds < (size_t)p.waves * 64 * 32) p.lds = (size_t)p.waves * 64 * 32;     // the join of parts: 8 floats a thread
     p.units = (int64_t)b.n_seq * p.VH * p.tiles;
     p.units = p.units > 0x7fffffffll ? p.units : p.units * (b.max_pages + p.seg_cost);
-    const int64_t most = p.units / p.min_piece + 1, cap = (int64_t)device_cus() * 1;
+    const int64_t most = p.units / p.min_piece + 1, cap = device_cus();
     p.blocks = (int)(most < cap ? most : cap);
     p.part_at = align_up((size_t)p.blocks * sizeof(unsigned long long), 256);
     p.part_bytes = (size_t)p.blocks * 2 * p.slot_rows * row;
