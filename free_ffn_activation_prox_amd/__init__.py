@@ -12,7 +12,6 @@ quantized proxy -> shared channel mask -> exact sparse SwiGLU).
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -429,16 +428,30 @@ def _need(ok: bool, what: str) -> None:
 
 
 def _on(stream, device):
-    """(stream pointer, context) of a call on tensors of `device`: the given
-    stream, else the device's current one; the context makes the device the
-    current one where it is not."""
+    """(stream pointer, whether the device is the current one) of a call on
+    tensors of `device`: the given stream, else the device's current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return _raw_stream(device.index), _current_device() == device.index
+    if stream.device != device:
         raise ValueError("stream and tensors are on different devices")
-    if device.index == torch.cuda.current_device():
-        return stream.cuda_stream, contextlib.nullcontext()
-    return stream.cuda_stream, torch.cuda.device(device)
+    return stream.cuda_stream, _current_device() == device.index
+
+
+# the current stream's handle and the current device, without the objects that
+# torch.cuda makes around them (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _kv_call(fn, where, device, here, *args):
+    """One call of the library with `device` as the current device."""
+    if here:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != PROX_OK:
+        _check(st, where)
 
 
 class KVCache:
@@ -464,6 +477,7 @@ class KVCache:
         self.device = k.device
         self._c = _KVCache(KV_KINDS[kind], self.n_pages, self.n_kv, self.head_dim, hp, k.data_ptr(), v.data_ptr(),
                            k_scale.data_ptr(), v_scale.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def alloc(cls, kind: str, n_pages: int, n_kv: int, head_dim: int, device="cuda") -> "KVCache":
@@ -500,17 +514,19 @@ class KVBatch:
         self.device = ctx_len.device
         self._c = _KVBatch(n_seq, self.n_tokens, self.max_q, int(block_table.shape[1]), ctx_len.data_ptr(),
                            block_table.data_ptr(), 0 if q_start is None else q_start.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
 
-def _kv_rows(name, t, batch, heads, hd, device):
-    """Row stride of an activation [n_tokens][heads][hd] (heads adjacent)."""
-    _need(t.dtype == torch.bfloat16 and t.is_cuda and t.device == device, f"{name} must be bf16 on the cache's device")
-    _need(t.dim() == 3 and t.shape[0] == batch.n_tokens and (heads is None or t.shape[1] == heads) and t.shape[2] == hd,
-          f"{name} must be [n_tokens][heads][head_dim]")
-    if t.shape[0] == 0:
-        return t.shape[1] * hd
-    _need(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == hd), f"{name}: the heads of a token must be adjacent")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * hd)
+def _kv_rows(name, t, n, heads, hd, device):
+    """Row stride of an activation [n][heads][hd] (heads adjacent)."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or t.device != device:
+        raise ValueError(f"{name} must be bf16 on the cache's device")
+    if len(shape) != 3 or shape[0] != n or shape[2] != hd or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [n_tokens][heads][head_dim]")
+    if n > 0 and (stride[2] != 1 or (stride[1] != hd and shape[1] != 1)):
+        raise ValueError(f"{name}: the heads of a token must be adjacent")
+    return stride[0] if n > 1 else max(stride[0], shape[1] * hd)
 
 
 def kv_append(cache: KVCache, batch: KVBatch, k, v, *, rot=None, q=None, q_out=None, g_q=None, g_k=None,
@@ -521,43 +537,44 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, *, rot=None, q=None, q_out=N
     cos, sin of every position and pair, complex64 [rows][rot_dim / 2] or
     fp32 [rows][rot_dim / 2][2], rows >= 64 * max_pages.  Returns q normed and
     rotated (bf16; q_out, which may be q, or a new tensor), None without q."""
-    dev = cache.device
-    _need(batch.device == dev, "cache and batch are on different devices")
-    _need(pairing in ROPE_PAIRINGS, f"unknown pairing {pairing!r}")
-    hd = cache.head_dim
-    ks = _kv_rows("k", k, batch, cache.n_kv, hd, dev)
-    vs = _kv_rows("v", v, batch, cache.n_kv, hd, dev)
-    r = _KVRotation(None, 0, 0, ROPE_PAIRINGS[pairing], None, None, eps)
+    dev, hd, n = cache.device, cache.head_dim, batch.n_tokens
+    if batch.device != dev:
+        raise ValueError("cache and batch are on different devices")
+    if pairing not in ROPE_PAIRINGS:
+        raise ValueError(f"unknown pairing {pairing!r}")
+    ks = _kv_rows("k", k, n, cache.n_kv, hd, dev)
+    vs = _kv_rows("v", v, n, cache.n_kv, hd, dev)
+    rp, rows, dim = None, 0, 0
     if rot is not None:
-        _need(rot.is_contiguous() and rot.device == dev and (
-            rot.dtype == torch.complex64 and rot.dim() == 2
-            or rot.dtype == torch.float32 and rot.dim() == 3 and rot.shape[2] == 2),
-            "rot must be contiguous complex64 [rows][rot_dim / 2] or fp32 [rows][rot_dim / 2][2]")
-        r.rot, r.rot_rows, r.rot_dim = rot.data_ptr(), rot.shape[0], 2 * rot.shape[1]
-    for n, g in (("g_q", g_q), ("g_k", g_k)):
-        if g is not None:
-            _need(g.dtype == torch.float32 and g.device == dev and g.is_contiguous() and tuple(g.shape) == (hd,),
-                  f"{n} must be fp32 [head_dim]")
-            setattr(r, n, g.data_ptr())
+        if rot.device != dev or not rot.is_contiguous() or not (
+                rot.dtype is torch.complex64 and rot.dim() == 2
+                or rot.dtype is torch.float32 and rot.dim() == 3 and rot.shape[2] == 2):
+            raise ValueError("rot must be contiguous complex64 [rows][rot_dim / 2] or fp32 [rows][rot_dim / 2][2]")
+        rp, rows, dim = rot.data_ptr(), rot.shape[0], 2 * rot.shape[1]
+    for g in (g_q, g_k):
+        if g is not None and not (g.dtype is torch.float32 and g.device == dev and g.is_contiguous()
+                                  and g.shape == (hd,)):
+            raise ValueError("g_q and g_k must be fp32 [head_dim] on the cache's device")
+    r = _KVRotation(rp, rows, dim, ROPE_PAIRINGS[pairing], None if g_q is None else g_q.data_ptr(),
+                    None if g_k is None else g_k.data_ptr(), eps)
     n_heads, qp, qs, qop, qos = cache.n_kv, None, 0, None, 0
     if q is not None:
-        n_heads = q.shape[1]
-        qs = _kv_rows("q", q, batch, None, hd, dev)
+        qs = _kv_rows("q", q, n, None, hd, dev)
+        n_heads, qp = q.shape[1], q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        qos = _kv_rows("q_out", q_out, batch, n_heads, hd, dev)
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-    else:
-        _need(q_out is None, "q_out without q")
-    sp, ctx = _on(stream, dev)
-    with ctx:
-        _check(_lib.prox_kv_append(ctypes.byref(cache._c), ctypes.byref(batch._c), k.data_ptr(), ks, v.data_ptr(), vs,
-                                   ctypes.byref(r), n_heads, qp, qs, qop, qos, sp), "prox_kv_append")
+            q_out = torch.empty_like(q)
+        qos = qs if q_out is q else _kv_rows("q_out", q_out, n, n_heads, hd, dev)
+        qop = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    sp, here = _on(stream, dev)
+    _kv_call(_lib.prox_kv_append, "prox_kv_append", dev, here, cache._ref, batch._ref, k.data_ptr(), ks, v.data_ptr(),
+             vs, ctypes.byref(r), n_heads, qp, qs, qop, qos, sp)
     return q_out
 
 
 def kv_workspace_bytes(cache: KVCache, batch: KVBatch, n_heads: int) -> int:
-    return _lib.prox_kv_workspace_bytes(ctypes.byref(cache._c), ctypes.byref(batch._c), n_heads)
+    return _lib.prox_kv_workspace_bytes(cache._ref, batch._ref, n_heads)
 
 
 def alloc_kv_workspace(cache: KVCache, batch: KVBatch, n_heads: int):
@@ -578,23 +595,22 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, *, scale: Optional[float] = 
     1 / sqrt(head_dim), window > 0 limits a row to its last `window` positions.
     Returns out, bf16 [n_tokens][n_heads][head_dim]; rows that see nothing are
     zeros, rows outside every sequence are left as they were."""
-    dev, hd = cache.device, cache.head_dim
-    _need(batch.device == dev, "cache and batch are on different devices")
-    qs = _kv_rows("q", q, batch, None, hd, dev)
+    dev, hd, n = cache.device, cache.head_dim, batch.n_tokens
+    if batch.device != dev:
+        raise ValueError("cache and batch are on different devices")
+    qs = _kv_rows("q", q, n, None, hd, dev)
     n_heads = q.shape[1]
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    os_ = _kv_rows("out", out, batch, n_heads, hd, dev)
+        out = torch.empty_like(q)
+    os_ = _kv_rows("out", out, n, n_heads, hd, dev)
     if workspace is None:
         workspace = alloc_kv_workspace(cache, batch, n_heads)
-    _need(workspace.is_cuda and workspace.device == dev and workspace.is_contiguous(),
-          "workspace must be contiguous on the cache's device")
-    sp, ctx = _on(stream, dev)
-    with ctx:
-        _check(_lib.prox_kv_attention(ctypes.byref(cache._c), ctypes.byref(batch._c), q.data_ptr(), qs, n_heads,
-                                      hd ** -0.5 if scale is None else scale, window, out.data_ptr(), os_,
-                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(), sp),
-               "prox_kv_attention")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
+    sp, here = _on(stream, dev)
+    _kv_call(_lib.prox_kv_attention, "prox_kv_attention", dev, here, cache._ref, batch._ref, q.data_ptr(), qs, n_heads,
+             hd ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, workspace.data_ptr(),
+             workspace.nbytes, sp)
     return out
 
 
@@ -602,18 +618,22 @@ def kv_read(cache: KVCache, batch: KVBatch, *, dtype=torch.bfloat16, k_out=None,
     """The batch's tokens back from the cache: (k, v), each [n_tokens][n_kv]
     [head_dim] in bf16 or fp32, the values that the codes stand for."""
     dev = cache.device
-    _need(batch.device == dev, "cache and batch are on different devices")
-    _need(dtype in (torch.bfloat16, torch.float32), "dtype must be bfloat16 or float32")
+    if batch.device != dev:
+        raise ValueError("cache and batch are on different devices")
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError("dtype must be bfloat16 or float32")
     shape = (batch.n_tokens, cache.n_kv, cache.head_dim)
-    k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
-    for n, t in (("k_out", k_out), ("v_out", v_out)):
-        _need(t.dtype == dtype and t.device == dev and t.is_contiguous() and tuple(t.shape) == shape,
-              f"{n}: wrong dtype, shape, layout or device")
-    sp, ctx = _on(stream, dev)
-    with ctx:
-        _check(_lib.prox_kv_read(ctypes.byref(cache._c), ctypes.byref(batch._c), k_out.data_ptr(), v_out.data_ptr(),
-                                 1 if dtype == torch.float32 else 0, sp), "prox_kv_read")
+    if k_out is None and v_out is None:
+        k_out, v_out = torch.empty((2,) + shape, dtype=dtype, device=dev).unbind(0)
+    else:
+        k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
+        for t in (k_out, v_out):
+            if not (t.dtype is dtype and t.device == dev and t.is_contiguous() and t.shape == shape):
+                raise ValueError("k_out and v_out must be contiguous [n_tokens][n_kv][head_dim] of the dtype")
+    sp, here = _on(stream, dev)
+    _kv_call(_lib.prox_kv_read, "prox_kv_read", dev, here, cache._ref, batch._ref, k_out.data_ptr(), v_out.data_ptr(),
+             1 if dtype is torch.float32 else 0, sp)
     return k_out, v_out
 
 
