@@ -164,7 +164,6 @@ __device__ void append_side(const Append& A, uint8_t* image, float* red, int pag
     }
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) most = fmaxf(most, __shfl_xor(most, m));
-    __syncthreads();                             // red and image: the previous side is done with them
     if ((t & 63) == 0) red[t >> 6] = most;
     __syncthreads();
     most = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
@@ -223,16 +222,20 @@ __device__ void append_side(const Append& A, uint8_t* image, float* red, int pag
     }
 }
 
-// grid: first one block per (sequence, page that its tokens can touch, head),
-// then blocks of 256 / TPT (row, query head) pairs.
+// grid: first one block per (sequence, page that its tokens can touch, head, K
+// or V), then blocks of 256 / TPT (row, query head) pairs.  K and V of a page
+// in one block, one after the other, took 20 us for 4096 tokens of 8 heads
+// (each block one long chain of loads, a maximum and stores); as blocks of
+// their own they run side by side.
 template <int KIND, int TPT>
 __global__ void __launch_bounds__(kThreads) k_kv_append(Append A) {
     __shared__ __align__(16) uint8_t image[kKvPage * 8 * TPT];
     __shared__ float red[4];
     const int t = threadIdx.x;
     if ((int)blockIdx.x < A.kv_blocks) {
-        const int head = blockIdx.x % A.c.n_kv;
-        const int rest = blockIdx.x / A.c.n_kv;
+        const bool val = blockIdx.x & 1;
+        const int head = (blockIdx.x >> 1) % A.c.n_kv;
+        const int rest = (blockIdx.x >> 1) / A.c.n_kv;
         const int s = rest / A.pp, j = rest % A.pp;
         const KvRows R = kv_rows(A.b, s);
         if (R.rows <= 0 || R.first + R.rows <= 0) return;
@@ -244,16 +247,17 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(Append A) {
         const int page = A.b.block_table[(size_t)s * A.b.max_pages + pg];
         if (page < 0 || page >= A.c.n_pages) return;
         const int s0 = a - pg * kKvPage, s1 = b - pg * kKvPage, row0 = R.q0 + (a - R.first);
-        append_side<KIND, TPT, false>(A, image, red, page, head, s0, s1, row0, a);
-        append_side<KIND, TPT, true>(A, image, red, page, head, s0, s1, row0, a);
+        if (val) append_side<KIND, TPT, true>(A, image, red, page, head, s0, s1, row0, a);
+        else append_side<KIND, TPT, false>(A, image, red, page, head, s0, s1, row0, a);
         return;
     }
     constexpr int RPP = kThreads / TPT;
-    const int64_t id = (int64_t)((int)blockIdx.x - A.kv_blocks) * RPP + t / TPT;
+    const int64_t id0 = (int64_t)((int)blockIdx.x - A.kv_blocks) * RPP, id = id0 + t / TPT;
+    int s = kv_seq_of(A.b, (int)(id0 / A.H), t & 63);
     const int64_t row64 = id / A.H;
     if (row64 >= A.b.n_tokens) return;                       // a head's lanes leave together
-    const int row = (int)row64, h = (int)(id % A.H), c = (t % TPT) * 8, hd = A.c.head_dim;
-    const int s = kv_seq_of(A.b, row);
+    const int row = (int)row64, h = (int)(id - row64 * A.H), c = (t % TPT) * 8, hd = A.c.head_dim;
+    s = kv_seq_on(A.b, s, row);
     const KvRows R = kv_rows(A.b, s);
     const int i = row - R.q0;
     if (i < 0 || i >= R.rows) return;
@@ -272,46 +276,32 @@ struct Read {
     prox_kv_cache c;
     prox_kv_batch b;
     void *k, *v;
+    int pp;               // pages that one sequence's tokens can touch
 };
 
-// One thread: eight channels of one (row, head), K and V.
+// Four codes of each of eight channels (a dword a channel, a byte a token) ->
+// the eight codes of token e.
+__device__ __forceinline__ uint2 token_of_dwords(const uint32_t d[8], int e) {
+    const uint32_t one = (uint32_t)e | ((uint32_t)(e + 4) << 8);            // byte e of both operands
+    auto pair = [&](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, one); };
+    const uint32_t p0 = pair(d[0], d[1]), p1 = pair(d[2], d[3]), p2 = pair(d[4], d[5]), p3 = pair(d[6], d[7]);
+    return make_uint2(__builtin_amdgcn_perm(p1, p0, 0x05040100u), __builtin_amdgcn_perm(p3, p2, 0x05040100u));
+}
+
+// grid: one block per (sequence, page that its tokens can touch, head).  A
+// thread turns 16 channels of a token (K, as they are stored) or eight channels
+// of four tokens (V, bytes exchanged in registers) at a time; eight or sixteen
+// neighbouring lanes write one token's channels.  Bound by the output, two or
+// four bytes for each byte read.
 template <int KIND, bool FP32>
 __global__ void __launch_bounds__(kThreads) k_kv_read(Read A) {
-    const int hd = A.c.head_dim, hp = A.c.head_pad, n8 = hd / 8;
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t row64 = id / (A.c.n_kv * n8);
-    if (row64 >= A.b.n_tokens) return;
-    const int row = (int)row64, rest = (int)(id % (A.c.n_kv * n8)), head = rest / n8, c = rest % n8 * 8;
-    const int s = kv_seq_of(A.b, row);
+    const int hd = A.c.head_dim, hp = A.c.head_pad, t = threadIdx.x;
+    const int head = blockIdx.x % A.c.n_kv, rest = blockIdx.x / A.c.n_kv;
+    const int s = rest / A.pp, j = rest % A.pp;
     const KvRows R = kv_rows(A.b, s);
-    const int i = row - R.q0;
-    if (i < 0 || i >= R.rows) return;
-    const int pos = R.first + i;
-    int page = -1;
-    if (pos >= 0 && pos < A.b.max_pages * kKvPage) page = A.b.block_table[(size_t)s * A.b.max_pages + pos / kKvPage];
-    float k[8] = {}, v[8] = {};
-    if (page >= 0 && page < A.c.n_pages) {
-        const size_t at = (size_t)page * A.c.n_kv + head;
-        const uint8_t* kc = static_cast<const uint8_t*>(A.c.k) + at * (size_t)(kKvPage * hp);
-        const uint8_t* vc = static_cast<const uint8_t*>(A.c.v) + at * (size_t)(kKvPage * hp);
-        const float ks = A.c.k_scale[at], vs = A.c.v_scale[at];
-        const int slot = pos % kKvPage;
-        const uint2 w = *reinterpret_cast<const uint2*>(kc + kv_k_index(slot, c));
-        uint32_t x[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e >> 2] |= (uint32_t)vc[kv_v_index(slot, c + e)] << (8 * (e & 3));
-        kv_values4<KIND>(w.x, k);
-        kv_values4<KIND>(w.y, k + 4);
-        kv_values4<KIND>(x[0], v);
-        kv_values4<KIND>(x[1], v + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            k[e] *= ks;
-            v[e] *= vs;
-        }
-    }
-    const int64_t o = ((int64_t)row * A.c.n_kv + head) * hd + c;
-    auto store = [&](void* out, const float* x) {
+    if (R.rows <= 0) return;
+    auto store = [&](void* out, int row, int c, const float* x) {
+        const int64_t o = ((int64_t)row * A.c.n_kv + head) * hd + c;
         if constexpr (FP32) {
             float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
             p[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -321,8 +311,56 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(Read A) {
                 make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
         }
     };
-    store(A.k, k);
-    store(A.v, v);
+    const float zero[8] = {};
+    const int cap = A.b.max_pages * kKvPage;
+    const int lo = max(R.first, 0), hi = (int)min((int64_t)R.first + R.rows, (int64_t)cap);   // positions that exist
+    if (j == 0) {
+        // rows whose position does not exist: those before `lo`, those from `hi` on
+        const int n8 = hd / 8, before = min(R.rows, max(lo - R.first, 0)), from = min(R.rows, max(max(hi, lo) - R.first, 0));
+        const int64_t n = (int64_t)(before + R.rows - from) * n8;
+        for (int64_t e = t; e < n; e += kThreads) {
+            const int i = (int)(e / n8), row = R.q0 + (i < before ? i : from + i - before), c = (int)(e % n8) * 8;
+            store(A.k, row, c, zero);
+            store(A.v, row, c, zero);
+        }
+    }
+    const int pg = lo / kKvPage + j;
+    const int a = max(lo, pg * kKvPage), b = min(hi, (pg + 1) * kKvPage);
+    if (a >= b) return;
+    const int page = A.b.block_table[(size_t)s * A.b.max_pages + pg];
+    const bool there = page >= 0 && page < A.c.n_pages;
+    const int s0 = a - pg * kKvPage, s1 = b - pg * kKvPage, row0 = R.q0 + (a - R.first) - s0;   // slot x: row row0 + x
+    const size_t at = (size_t)(there ? page : 0) * A.c.n_kv + head;
+    const uint8_t* kc = static_cast<const uint8_t*>(A.c.k) + at * (size_t)(kKvPage * hp);
+    const uint8_t* vc = static_cast<const uint8_t*>(A.c.v) + at * (size_t)(kKvPage * hp);
+    const float ks = A.c.k_scale[at], vs = A.c.v_scale[at];
+    auto put = [&](void* out, int slot, int c, uint2 w, float scale) {
+        float x[8];
+        kv_values4<KIND>(w.x, x);
+        kv_values4<KIND>(w.y, x + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = there ? x[e] * scale : 0.f;
+        store(out, row0 + slot, c, x);
+    };
+    const int n16 = hp / 16, first = s0 / 4 * 4;
+    for (int e = t; e < (s1 - first) * n16; e += kThreads) {
+        const int slot = first + e / n16, c = e % n16 * 16;
+        if (slot < s0 || c >= hd) continue;
+        const uint4 u = *reinterpret_cast<const uint4*>(kc + kv_k_index(slot, c));
+        put(A.k, slot, c, make_uint2(u.x, u.y), ks);
+        if (c + 8 < hd) put(A.k, slot, c + 8, make_uint2(u.z, u.w), ks);
+    }
+    const int n8 = hp / 8;
+    for (int e = t; e < (s1 - first + 3) / 4 * n8; e += kThreads) {
+        const int slot = first + e / n8 * 4, c = e % n8 * 8;
+        if (c >= hd) continue;
+        uint32_t d[8];
+#pragma unroll
+        for (int f = 0; f < 8; ++f) d[f] = *reinterpret_cast<const uint32_t*>(vc + kv_v_index(slot, c + f));
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+            if (slot + f >= s0 && slot + f < s1) put(A.v, slot + f, c, token_of_dwords(d, f), vs);
+    }
 }
 
 template <int KIND>
@@ -368,7 +406,7 @@ hipError_t launch_kv_append(const prox_kv_cache& c, const prox_kv_batch& b, cons
     A.rot.eps = (double)r.eps;
     A.H = q ? n_heads : 1;
     A.pp = pages_touched(b);
-    const int64_t kvb = (int64_t)b.n_seq * A.pp * c.n_kv;
+    const int64_t kvb = (int64_t)b.n_seq * A.pp * c.n_kv * 2;
     const int rpp = kThreads / lanes_per_head(c.head_pad);
     const int64_t qb = q ? ((int64_t)b.n_tokens * n_heads + rpp - 1) / rpp : 0;
     if (kvb + qb > 0x7fffffffll) return hipErrorInvalidConfiguration;
@@ -379,8 +417,8 @@ hipError_t launch_kv_append(const prox_kv_cache& c, const prox_kv_batch& b, cons
 
 hipError_t launch_kv_read(const prox_kv_cache& c, const prox_kv_batch& b, void* k_out, void* v_out, bool fp32,
                           hipStream_t s) {
-    const Read A{c, b, k_out, v_out};
-    const int64_t blocks = ((int64_t)b.n_tokens * c.n_kv * (c.head_dim / 8) + kThreads - 1) / kThreads;
+    const Read A{c, b, k_out, v_out, pages_touched(b)};
+    const int64_t blocks = (int64_t)b.n_seq * A.pp * c.n_kv;
     if (blocks > 0x7fffffffll) return hipErrorInvalidConfiguration;
     const dim3 g((uint32_t)blocks), t(kThreads);
     if (c.kind == PROX_KV_INT8) {

@@ -95,16 +95,25 @@ __device__ __forceinline__ KvRows kv_rows(const prox_kv_batch& b, int s) {
     return r;
 }
 
-// The sequence that a row belongs to: the last s with q_start[s] <= row.
-__device__ __forceinline__ int kv_seq_of(const prox_kv_batch& b, int row) {
+// The sequence that a row belongs to, the last s with q_start[s] <= row (the
+// first one if there is none), found by a whole wave at once: row is the same
+// for its lanes.
+__device__ __forceinline__ int kv_seq_of(const prox_kv_batch& b, int row, int lane) {
     if (!b.q_start) return row;
-    int lo = 0, hi = b.n_seq;                        // q_start[lo] <= row < q_start[hi] where the starts ascend
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (b.q_start[mid] <= row) lo = mid;
-        else hi = mid;
+    int s = 0;
+    for (int base = 1; base < b.n_seq; base += 64) {
+        const int j = base + lane;
+        const uint64_t m = __ballot(j < b.n_seq && b.q_start[min(j, b.n_seq - 1)] <= row);
+        s += __builtin_popcountll(m);
+        if (m != ~0ull) break;
     }
-    return lo;
+    return s;
+}
+// The same for a row some way behind one that belongs to s.
+__device__ __forceinline__ int kv_seq_on(const prox_kv_batch& b, int s, int row) {
+    if (!b.q_start) return row;
+    while (s + 1 < b.n_seq && b.q_start[s + 1] <= row) ++s;
+    return s;
 }
 
 }  // namespace prox
