@@ -119,7 +119,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 //   else the page is put together in LDS -- what it held (requantised where the
 //   scale grew), cleared where it begins anew -- and stored whole.
 template <int KIND, int TPT, bool VAL>
-__device__ void append_side(const Append& A, uint8_t* image, float* red, int page, int head, int s0, int s1,
+__device__ void append_side(const Append& A, uint8_t* image, uint32_t* red, int page, int head, int s0, int s1,
                             int row0, int pos0) {
     constexpr int RPP = kThreads / TPT;          // slots of one pass over the threads
     constexpr int NP = kKvPage / RPP;
@@ -132,7 +132,7 @@ __device__ void append_side(const Append& A, uint8_t* image, float* red, int pag
     const float old = fresh ? 0.f : *scale;
 
     float r[NP][8];
-    float most = 0.f;
+    uint32_t bits = 0;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         if ((p + 1) * RPP <= s0 || p * RPP >= s1) continue;           // uniform
@@ -156,23 +156,66 @@ __device__ void append_side(const Append& A, uint8_t* image, float* red, int pag
         }
         if (live) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float m = fabsf(r[p][e]);
-                if (m < INFINITY) most = fmaxf(most, m);              // false for NaN too
-            }
+            for (int e = 0; e < 8; ++e) bits = max(bits, __float_as_uint(r[p][e]) << 1);    // by magnitude, NaN on top
         }
     }
+    // the largest magnitude of the block; an infinity or NaN among them (rare)
+    // is left out in a second round
+    auto over_block = [&](uint32_t v) {
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) most = fmaxf(most, __shfl_xor(most, m));
-    if ((t & 63) == 0) red[t >> 6] = most;
-    __syncthreads();
-    most = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        for (int m = 1; m < 64; m *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+        if ((t & 63) == 0) red[t >> 6] = v;
+        __syncthreads();
+        v = max(max(red[0], red[1]), max(red[2], red[3]));
+        __syncthreads();
+        return v;
+    };
+    bits = over_block(bits);
+    const bool finite = bits < 0xff000000u;
+    if (!finite) {
+        bits = 0;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            if ((p + 1) * RPP <= s0 || p * RPP >= s1) continue;
+            const int slot = p * RPP + t / TPT;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t b = __float_as_uint(r[p][e]) << 1;
+                if (slot >= s0 && slot < s1 && b < 0xff000000u) bits = max(bits, b);
+            }
+        }
+        bits = over_block(bits);
+    }
+    const float most = __uint_as_float(bits >> 1);
     const float sc = fmaxf(old, most / kv_qmax<KIND>());
     const bool grown = sc > old && old > 0.f;
     const bool whole = fresh || grown || s1 - s0 > kDirect;
     if (t == 0 && sc != old) *scale = sc;
     if (t == 0 && fresh) *scale = sc;
     const float unit = sc > 0.f ? sc : 1.f;
+    // x / unit, correctly rounded: with the rounded reciprocal i of unit, y = x i
+    // and its exact remainder x - y unit, y + i (x - y unit) is the rounded
+    // quotient (Markstein) unless the mantissa of unit is all ones or a number
+    // leaves the normal range; those pages, and those with an infinity or NaN,
+    // take the division and clamp.  The division alone takes ten instructions
+    // a value, all of the rest six.
+    const uint32_t ub = __float_as_uint(unit);
+    const bool tame = finite && sc > 0x1p-90f && sc < 0x1p90f && (ub & 0x7fffffu) != 0x7fffffu;
+    const float inv = 1.f / unit;
+    auto codes4 = [&](const float* x) {
+        float y[4];
+        if (tame) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float q = x[e] * inv;
+                y[e] = fmaf(fmaf(-q, unit, x[e]), inv, q);
+            }
+            return kv_codes4_tame<KIND>(y);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = sc > 0.f ? x[e] / unit : 0.f;
+        return kv_codes4<KIND>(y);
+    };
 
     if (whole) {
         for (int i = t; i < kKvPage * hp / 16; i += kThreads) {
@@ -200,14 +243,7 @@ __device__ void append_side(const Append& A, uint8_t* image, float* red, int pag
         if ((p + 1) * RPP <= s0 || p * RPP >= s1) continue;
         const int slot = p * RPP + t / TPT;
         if (slot < s0 || slot >= s1 || c >= hd) continue;
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = sc > 0.f ? r[p][4 * h + e] / unit : 0.f;
-            w[h] = kv_codes4<KIND>(x);
-        }
+        const uint32_t w[2] = {codes4(r[p]), codes4(r[p] + 4)};
         if constexpr (VAL) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) to[kv_v_index(slot, c + e)] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
@@ -230,7 +266,7 @@ __device__ void append_side(const Append& A, uint8_t* image, float* red, int pag
 template <int KIND, int TPT>
 __global__ void __launch_bounds__(kThreads) k_kv_append(Append A) {
     __shared__ __align__(16) uint8_t image[kKvPage * 8 * TPT];
-    __shared__ float red[4];
+    __shared__ uint32_t red[4];
     const int t = threadIdx.x;
     if ((int)blockIdx.x < A.kv_blocks) {
         const bool val = blockIdx.x & 1;

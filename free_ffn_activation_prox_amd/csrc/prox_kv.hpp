@@ -76,6 +76,23 @@ __device__ __forceinline__ T uniform_load(const T* p) {
     return *(const __attribute__((address_space(4))) T*)p;
 }
 
+// The same codes for values that are finite and at most qmax (1 + 2^-23) large:
+// nothing to clamp.  int8: adding 1.5 2^23 rounds half-even to a whole number
+// and leaves it in the low byte.
+template <int KIND>
+__device__ __forceinline__ uint32_t kv_codes4_tame(const float x[4]) {
+    if constexpr (KIND == PROX_KV_INT8) {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(x[e] + 12582912.f);
+        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
+                                     __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
+    } else {
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
+    }
+}
+
 // The rows of sequence s: rows q0 .. q0 + n - 1 (clamped to the batch), of
 // which the first `rows` are worked on; row i has position first + i.
 struct KvRows {
