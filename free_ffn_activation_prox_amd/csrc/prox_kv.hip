@@ -10,6 +10,8 @@
 // rounding that would flip it.  The work is a few operations a byte moved; what
 // bounds the call is reading q, k, v once and, for one token, the latency of
 // the launch.
+#include <algorithm>
+
 #include "prox_kv.hpp"
 
 namespace prox {
@@ -17,81 +19,111 @@ namespace prox {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;
 
 struct RotArgs {
     const float2* rot;
     int half;            // rot_dim / 2 (0: no rotation)
     int halves;          // pairing
+    int wide;            // table rows are 16-byte aligned
     double eps;
 };
 
-// Channels c .. c + 7 of one head (TPT neighbouring lanes hold the head; lanes
-// with c >= hd take part with zeros), normed by `gain` (nullable) and rotated
-// with the table row `rot`.
+// Channels c .. c + 7 of one head, held by TPT neighbouring lanes (lanes with
+// c >= hd take part with zeros): the place of a lane in a head, and the cos and
+// sin of its pairs at one position.
 template <int TPT>
-__device__ __forceinline__ void head8(const uint16_t* __restrict__ x, int c, int hd, const float* __restrict__ gain,
-                                      const float2* __restrict__ rot, const RotArgs& a, float out[8]) {
-    const bool in = c < hd;
-    const bool turn = in && c < 2 * a.half;
-    double v[8], w[8];
-    auto load = [&](int ch, double o[8]) {
-        const uint4 u = *reinterpret_cast<const uint4*>(x + ch);
-        const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+struct Head8 {
+    const RotArgs& a;
+    int c, pc, hd;       // channels; halves: those they are paired with
+    bool in, turn, lower;
+    float2 cs[8];        // halves: of the eight channels; interleaved: of the four pairs
+
+    __device__ __forceinline__ Head8(const RotArgs& r, int ch, int n) : a(r), c(ch), hd(n) {
+        in = c < hd;
+        turn = in && c < 2 * a.half;
+        lower = c < a.half;
+        pc = lower ? c + a.half : c - a.half;
+    }
+    // the table's row of position pos (a loaded pair takes 8 bytes: 16-byte loads where rows are aligned)
+    __device__ __forceinline__ void at(int pos) {
+        if (!turn) return;
+        const float2* src = a.rot + (int64_t)pos * a.half + (a.halves ? (lower ? c : pc) : c / 2);
+        if (a.wide && a.halves) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            o[2 * e] = (double)bf16_lo(d[e]);
-            o[2 * e + 1] = (double)bf16_hi(d[e]);
-        }
-    };
-    const bool lower = c < a.half;
-    const int pc = lower ? c + a.half : c - a.half;      // the other channel of each pair (halves)
+            for (int e = 0; e < 8; e += 2) two(src, e);
+        } else if (a.wide && c + 8 <= 2 * a.half) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.0;
-    if (in) load(c, v);
-    if (a.halves && turn) load(pc, w);
-    if (gain) {
-        double ss = 0.0;
+            for (int e = 0; e < 4; e += 2) two(src, e);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fma(v[e], v[e], ss);
-#pragma unroll
-        for (int m = 1; m < TPT; m *= 2) ss += __shfl_xor(ss, m);
-        const double inv = 1.0 / sqrt(ss / (double)hd + a.eps);
-        if (in) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * (double)gain[c + e];
-        }
-        if (a.halves && turn) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = w[e] * inv * (double)gain[pc + e];
+            for (int e = 0; e < 8; ++e)
+                if (a.halves || (e < 4 && c + 2 * e < 2 * a.half)) cs[e] = src[e];
         }
     }
-    if (!turn) {
+    __device__ __forceinline__ void two(const float2* src, int e) {
+        const float4 f = *reinterpret_cast<const float4*>(src + e);
+        cs[e] = make_float2(f.x, f.y);
+        cs[e + 1] = make_float2(f.z, f.w);
+    }
+    __device__ __forceinline__ void load(const uint16_t* x, uint4& own, uint4& other) const {
+        own = other = make_uint4(0, 0, 0, 0);
+        if (in) own = *reinterpret_cast<const uint4*>(x + c);
+        if (a.halves && turn) other = *reinterpret_cast<const uint4*>(x + pc);
+    }
+    // normed by `gain` (nullable) and rotated, rounded once
+    __device__ __forceinline__ void finish(const uint4& own, const uint4& other, const float* __restrict__ gain, float out[8]) const {
+        double v[8], w[8];
+        auto wide_of = [](const uint4& u, double o[8]) {
+            const uint32_t d[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) out[e] = (float)v[e];
-    } else if (a.halves) {
-        const float2* cs = rot + (lower ? c : pc);
+            for (int e = 0; e < 4; ++e) {
+                o[2 * e] = (double)bf16_lo(d[e]);
+                o[2 * e + 1] = (double)bf16_hi(d[e]);
+            }
+        };
+        wide_of(own, v);
+        wide_of(other, w);
+        if (gain) {
+            double ss = 0.0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 t = cs[e];
-            out[e] = (float)(lower ? fma(-w[e], (double)t.y, v[e] * (double)t.x)
-                                   : fma(w[e], (double)t.y, v[e] * (double)t.x));
+            for (int e = 0; e < 8; ++e) ss = fma(v[e], v[e], ss);
+#pragma unroll
+            for (int m = 1; m < TPT; m *= 2) ss += __shfl_xor(ss, m);
+            const double inv = 1.0 / sqrt(ss / (double)hd + a.eps);
+            if (in) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * (double)gain[c + e];
+            }
+            if (a.halves && turn) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = w[e] * inv * (double)gain[pc + e];
+            }
         }
-    } else {
-        const float2* cs = rot + c / 2;
+        if (!turn) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const double p = v[2 * e], q = v[2 * e + 1];
-            if (c + 2 * e < 2 * a.half) {
-                const float2 t = cs[e];
-                out[2 * e] = (float)fma(-q, (double)t.y, p * (double)t.x);
-                out[2 * e + 1] = (float)fma(p, (double)t.y, q * (double)t.x);
-            } else {
-                out[2 * e] = (float)p;
-                out[2 * e + 1] = (float)q;
+            for (int e = 0; e < 8; ++e) out[e] = (float)v[e];
+        } else if (a.halves) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double s = lower ? -(double)cs[e].y : (double)cs[e].y;
+                out[e] = (float)fma(w[e], s, v[e] * (double)cs[e].x);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const double p = v[2 * e], q = v[2 * e + 1];
+                if (c + 2 * e < 2 * a.half) {
+                    out[2 * e] = (float)fma(-q, (double)cs[e].y, p * (double)cs[e].x);
+                    out[2 * e + 1] = (float)fma(p, (double)cs[e].y, q * (double)cs[e].x);
+                } else {
+                    out[2 * e] = (float)p;
+                    out[2 * e + 1] = (float)q;
+                }
             }
         }
     }
-}
+};
 
 struct Append {
     prox_kv_cache c;
@@ -103,6 +135,7 @@ struct Append {
     RotArgs rot;
     int H, pp;            // query heads; pages that one sequence's tokens can touch
     int kv_blocks;
+    int head_blocks, per_lane;   // of q: blocks of one row; heads of one lane, at most kHeads
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -113,8 +146,116 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, r);
 }
 
+// Eight codes of each of four tokens (w) -> a dword of four tokens for each of
+// the eight channels.
+__device__ __forceinline__ void dwords_of_tokens(const uint2 w[4], uint32_t d[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t a = h ? w[0].y : w[0].x, b = h ? w[1].y : w[1].x, c = h ? w[2].y : w[2].x, e = h ? w[3].y : w[3].x;
+        const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+        const uint32_t ce0 = __builtin_amdgcn_perm(e, c, 0x05010400u), ce1 = __builtin_amdgcn_perm(e, c, 0x07030602u);
+        d[4 * h] = __builtin_amdgcn_perm(ce0, ab0, 0x05040100u);
+        d[4 * h + 1] = __builtin_amdgcn_perm(ce0, ab0, 0x07060302u);
+        d[4 * h + 2] = __builtin_amdgcn_perm(ce1, ab1, 0x05040100u);
+        d[4 * h + 3] = __builtin_amdgcn_perm(ce1, ab1, 0x07060302u);
+    }
+}
+
+// A page in LDS: 16 bytes between its kilobytes, so that the same place of
+// several kilobytes lies in different banks.
+__device__ __forceinline__ int in_image(int at) { return at + (at >> 10) * 16; }
+
+// Codes of x / unit, correctly rounded.  With the rounded reciprocal i of unit,
+// y = x i and its exact remainder x - y unit, y + i (x - y unit) is the rounded
+// quotient (Markstein) unless the mantissa of unit is all ones or a number
+// leaves the normal range; a page with such a scale, or with an infinity or
+// NaN, is not `tame` and takes the division and clamp.  The division alone
+// takes ten instructions a value, all of the rest six.
+template <int KIND>
+struct Quotient {
+    float unit, inv;
+    bool tame, zero;
+    __device__ __forceinline__ Quotient(float scale, bool finite) {
+        zero = !(scale > 0.f);
+        unit = zero ? 1.f : scale;
+        tame = finite && scale > 0x1p-90f && scale < 0x1p90f && (__float_as_uint(unit) & 0x7fffffu) != 0x7fffffu;
+        inv = 1.f / unit;
+    }
+    __device__ __forceinline__ uint32_t tame4(const float* x) const {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float q = x[e] * inv;
+            y[e] = fmaf(fmaf(-q, unit, x[e]), inv, q);
+        }
+        return kv_codes4_tame<KIND>(y);
+    }
+    __device__ __forceinline__ uint32_t codes4(const float* x) const {
+        if (tame) return tame4(x);
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = zero ? 0.f : x[e] / unit;
+        return kv_codes4<KIND>(y);
+    }
+};
+
+// Eight channels of one row of K (normed and rotated for position pos) or V;
+// a lane that holds none (`off`) takes part with zeros.
+template <int TPT, bool VAL>
+__device__ __forceinline__ void row8(const Append& A, int row, int head, int c, int pos, bool off, float r[8]) {
+    const int hd = A.c.head_dim;
+    if constexpr (VAL) {
+        const uint16_t* x = A.v + (int64_t)row * A.vs + (int64_t)head * hd;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (!off && c < hd) u = *reinterpret_cast<const uint4*>(x + c);
+        const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[2 * e] = bf16_lo(d[e]);
+            r[2 * e + 1] = bf16_hi(d[e]);
+        }
+    } else {
+        Head8<TPT> head8(A.rot, c, hd);
+        uint4 own, other;
+        head8.load(A.k + (int64_t)row * A.ks + (int64_t)head * hd, own, other);
+        head8.at(pos);
+        head8.finish(own, other, A.g_k, r);
+    }
+}
+
+// One token into a page that keeps its scale (63 of 64 single tokens, nearly):
+// every wave finds out alike, without LDS, and the first lanes store.  Returns
+// whether that was the case.
+template <int KIND, int TPT, bool VAL>
+__device__ __forceinline__ bool append_one(const Append& A, int page, int head, int slot, int row, int pos) {
+    const int t = threadIdx.x, c = (t % TPT) * 8, hd = A.c.head_dim;
+    const size_t at = (size_t)page * A.c.n_kv + head;
+    const float old = (VAL ? A.c.v_scale : A.c.k_scale)[at];
+    float r[8];
+    row8<TPT, VAL>(A, row, head, c, pos, false, r);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bits = max(bits, __float_as_uint(r[e]) << 1);
+#pragma unroll
+    for (int m = 1; m < TPT; m *= 2) bits = max(bits, (uint32_t)__shfl_xor((int)bits, m));
+    const Quotient<KIND> u(old, bits < 0xff000000u);
+    if (!u.tame || __uint_as_float(bits >> 1) / kv_qmax<KIND>() > old) return false;
+    if (t >= TPT || c >= hd) return true;
+    uint8_t* codes = static_cast<uint8_t*>(VAL ? A.c.v : A.c.k) + at * (size_t)(kKvPage * A.c.head_pad);
+    const uint32_t w[2] = {u.tame4(r), u.tame4(r + 4)};
+    if constexpr (VAL) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) codes[kv_v_index(slot, c + e)] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+    } else {
+        *reinterpret_cast<uint2*>(codes + kv_k_index(slot, c)) = make_uint2(w[0], w[1]);
+    }
+    return true;
+}
+
 // One side (K or V) of one page and head: slots s0 .. s1 - 1 come from rows
 // row0 + (slot - s0).  Block of 256 threads; every thread passes the barriers.
+// A thread holds eight channels of four slots: of K, slots 256 / TPT apart, of
+// V, neighbours, whose codes make up dwords of the page.
 //   few new slots, scale kept: the new codes are stored where they belong;
 //   else the page is put together in LDS -- what it held (requantised where the
 //   scale grew), cleared where it begins anew -- and stored whole.
@@ -122,7 +263,7 @@ template <int KIND, int TPT, bool VAL>
 __device__ void append_side(const Append& A, uint8_t* image, uint32_t* red, int page, int head, int s0, int s1,
                             int row0, int pos0) {
     constexpr int RPP = kThreads / TPT;          // slots of one pass over the threads
-    constexpr int NP = kKvPage / RPP;
+    constexpr int NP = VAL ? (TPT > 16 ? TPT / 4 : 4) : kKvPage / RPP;
     constexpr int kDirect = 8;                   // at most so many slots are stored on their own
     const int t = threadIdx.x, c = (t % TPT) * 8, hd = A.c.head_dim, hp = A.c.head_pad;
     const size_t at = (size_t)page * A.c.n_kv + head;
@@ -130,30 +271,19 @@ __device__ void append_side(const Append& A, uint8_t* image, uint32_t* red, int 
     float* scale = (VAL ? A.c.v_scale : A.c.k_scale) + at;
     const bool fresh = s0 == 0;
     const float old = fresh ? 0.f : *scale;
+    // the slot of this thread's p-th values, and whether pass p has any slot of the call
+    auto slot_of = [&](int p) { return VAL ? (p >> 2) * 4 * RPP + (t / TPT) * 4 + (p & 3) : p * RPP + t / TPT; };
+    auto idle = [&](int p) { return VAL ? (p >> 2) * 4 * RPP >= s1 || ((p >> 2) + 1) * 4 * RPP <= s0 : p * RPP >= s1 || (p + 1) * RPP <= s0; };
 
     float r[NP][8];
     uint32_t bits = 0;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        if ((p + 1) * RPP <= s0 || p * RPP >= s1) continue;           // uniform
-        const int slot = p * RPP + t / TPT;
+        if (idle(p)) continue;                                        // uniform
+        const int slot = slot_of(p);
         const bool live = slot >= s0 && slot < s1;
         const int row = row0 + (live ? slot - s0 : 0);
-        if constexpr (VAL) {
-            const uint16_t* x = A.v + (int64_t)row * A.vs + (int64_t)head * hd;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (c < hd) u = *reinterpret_cast<const uint4*>(x + c);
-            const uint32_t d[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                r[p][2 * e] = bf16_lo(d[e]);
-                r[p][2 * e + 1] = bf16_hi(d[e]);
-            }
-        } else {
-            const uint16_t* x = A.k + (int64_t)row * A.ks + (int64_t)head * hd;
-            const int pos = pos0 + (live ? slot - s0 : 0);
-            head8<TPT>(x, c, hd, A.g_k, A.rot.rot + (int64_t)pos * A.rot.half, A.rot, r[p]);
-        }
+        row8<TPT, VAL>(A, row, head, c, pos0 + (live ? slot - s0 : 0), !live, r[p]);
         if (live) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) bits = max(bits, __float_as_uint(r[p][e]) << 1);    // by magnitude, NaN on top
@@ -176,8 +306,8 @@ __device__ void append_side(const Append& A, uint8_t* image, uint32_t* red, int 
         bits = 0;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            if ((p + 1) * RPP <= s0 || p * RPP >= s1) continue;
-            const int slot = p * RPP + t / TPT;
+            if (idle(p)) continue;
+            const int slot = slot_of(p);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t b = __float_as_uint(r[p][e]) << 1;
@@ -192,80 +322,78 @@ __device__ void append_side(const Append& A, uint8_t* image, uint32_t* red, int 
     const bool whole = fresh || grown || s1 - s0 > kDirect;
     if (t == 0 && sc != old) *scale = sc;
     if (t == 0 && fresh) *scale = sc;
-    const float unit = sc > 0.f ? sc : 1.f;
-    // x / unit, correctly rounded: with the rounded reciprocal i of unit, y = x i
-    // and its exact remainder x - y unit, y + i (x - y unit) is the rounded
-    // quotient (Markstein) unless the mantissa of unit is all ones or a number
-    // leaves the normal range; those pages, and those with an infinity or NaN,
-    // take the division and clamp.  The division alone takes ten instructions
-    // a value, all of the rest six.
-    const uint32_t ub = __float_as_uint(unit);
-    const bool tame = finite && sc > 0x1p-90f && sc < 0x1p90f && (ub & 0x7fffffu) != 0x7fffffu;
-    const float inv = 1.f / unit;
-    auto codes4 = [&](const float* x) {
-        float y[4];
-        if (tame) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float q = x[e] * inv;
-                y[e] = fmaf(fmaf(-q, unit, x[e]), inv, q);
-            }
-            return kv_codes4_tame<KIND>(y);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = sc > 0.f ? x[e] / unit : 0.f;
-        return kv_codes4<KIND>(y);
-    };
+    const Quotient<KIND> u(sc, finite);
 
     if (whole) {
         for (int i = t; i < kKvPage * hp / 16; i += kThreads) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (!fresh) u = reinterpret_cast<const uint4*>(codes)[i];
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (!fresh) v = reinterpret_cast<const uint4*>(codes)[i];
             if (grown) {
-                uint32_t d[4] = {u.x, u.y, u.z, u.w};
+                uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float x[4];
                     kv_values4<KIND>(d[e], x);
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) x[f] = x[f] * old / unit;
+                    for (int f = 0; f < 4; ++f) x[f] = x[f] * old / u.unit;
                     d[e] = kv_codes4<KIND>(x);
                 }
-                u = make_uint4(d[0], d[1], d[2], d[3]);
+                v = make_uint4(d[0], d[1], d[2], d[3]);
             }
-            reinterpret_cast<uint4*>(image)[i] = u;
+            *reinterpret_cast<uint4*>(image + in_image(16 * i)) = v;
         }
         __syncthreads();
     }
-    uint8_t* to = whole ? image : codes;
+    if constexpr (VAL) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        if ((p + 1) * RPP <= s0 || p * RPP >= s1) continue;
-        const int slot = p * RPP + t / TPT;
-        if (slot < s0 || slot >= s1 || c >= hd) continue;
-        const uint32_t w[2] = {codes4(r[p]), codes4(r[p] + 4)};
-        if constexpr (VAL) {
+        for (int p = 0; p < NP; p += 4) {
+            const int slot = slot_of(p);
+            if (slot >= s1 || slot + 4 <= s0 || c >= hd) continue;
+            uint2 w[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) to[kv_v_index(slot, c + e)] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
-        } else {
-            *reinterpret_cast<uint2*>(to + kv_k_index(slot, c)) = make_uint2(w[0], w[1]);
+            for (int f = 0; f < 4; ++f) w[f] = make_uint2(u.codes4(r[p + f]), u.codes4(r[p + f] + 4));
+            uint32_t d[8];
+            dwords_of_tokens(w, d);
+            const bool all = slot >= s0 && slot + 4 <= s1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = kv_v_index(slot, c + e);
+                uint8_t* to = whole ? image + in_image(i) : codes + i;
+                if (all) {
+                    *reinterpret_cast<uint32_t*>(to) = d[e];
+                } else {
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        if (slot + f >= s0 && slot + f < s1) to[f] = (uint8_t)(d[e] >> (8 * f));
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            if (idle(p)) continue;
+            const int slot = slot_of(p);
+            if (slot < s0 || slot >= s1 || c >= hd) continue;
+            const int i = kv_k_index(slot, c);
+            *reinterpret_cast<uint2*>(whole ? image + in_image(i) : codes + i) = make_uint2(u.codes4(r[p]), u.codes4(r[p] + 4));
         }
     }
     if (whole) {
         __syncthreads();
         for (int i = t; i < kKvPage * hp / 16; i += kThreads)
-            reinterpret_cast<uint4*>(codes)[i] = reinterpret_cast<const uint4*>(image)[i];
+            reinterpret_cast<uint4*>(codes)[i] = *reinterpret_cast<const uint4*>(image + in_image(16 * i));
     }
 }
 
 // grid: first one block per (sequence, page that its tokens can touch, head, K
-// or V), then blocks of 256 / TPT (row, query head) pairs.  K and V of a page
+// or V), then blocks of one row and 256 / TPT heads for each of A.per_lane turns,
+// which share the row of the table.  K and V of a page
 // in one block, one after the other, took 20 us for 4096 tokens of 8 heads
 // (each block one long chain of loads, a maximum and stores); as blocks of
 // their own they run side by side.
 template <int KIND, int TPT>
 __global__ void __launch_bounds__(kThreads) k_kv_append(Append A) {
-    __shared__ __align__(16) uint8_t image[kKvPage * 8 * TPT];
+    __shared__ __align__(16) uint8_t image[(kKvPage + 1) * 8 * TPT];    // 16 bytes more for each kilobyte
     __shared__ uint32_t red[4];
     const int t = threadIdx.x;
     if ((int)blockIdx.x < A.kv_blocks) {
@@ -283,29 +411,40 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(Append A) {
         const int page = A.b.block_table[(size_t)s * A.b.max_pages + pg];
         if (page < 0 || page >= A.c.n_pages) return;
         const int s0 = a - pg * kKvPage, s1 = b - pg * kKvPage, row0 = R.q0 + (a - R.first);
+        if (s1 - s0 == 1 && s0 > 0) {
+            if (val ? append_one<KIND, TPT, true>(A, page, head, s0, row0, a)
+                    : append_one<KIND, TPT, false>(A, page, head, s0, row0, a)) return;
+        }
         if (val) append_side<KIND, TPT, true>(A, image, red, page, head, s0, s1, row0, a);
         else append_side<KIND, TPT, false>(A, image, red, page, head, s0, s1, row0, a);
         return;
     }
     constexpr int RPP = kThreads / TPT;
-    const int64_t id0 = (int64_t)((int)blockIdx.x - A.kv_blocks) * RPP, id = id0 + t / TPT;
-    int s = kv_seq_of(A.b, (int)(id0 / A.H), t & 63);
-    const int64_t row64 = id / A.H;
-    if (row64 >= A.b.n_tokens) return;                       // a head's lanes leave together
-    const int row = (int)row64, h = (int)(id - row64 * A.H), c = (t % TPT) * 8, hd = A.c.head_dim;
-    s = kv_seq_on(A.b, s, row);
+    const int bq = (int)blockIdx.x - A.kv_blocks, row = bq / A.head_blocks, c = (t % TPT) * 8, hd = A.c.head_dim;
+    const int h0 = (bq - row * A.head_blocks) * RPP * A.per_lane + t / TPT;
+    const int s = kv_seq_of(A.b, row, t & 63);
     const KvRows R = kv_rows(A.b, s);
     const int i = row - R.q0;
     if (i < 0 || i >= R.rows) return;
     const int pos = R.first + i;
     const bool seen = pos >= 0 && pos < A.b.max_pages * kKvPage;
-    float o[8];
-    head8<TPT>(A.q + (int64_t)row * A.qs + (int64_t)h * hd, c, hd, A.g_q,
-               A.rot.rot + (int64_t)(seen ? pos : 0) * A.rot.half, A.rot, o);
-    if (c >= hd) return;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (seen) u = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-    *reinterpret_cast<uint4*>(A.q_out + (int64_t)row * A.qos + (int64_t)h * hd + c) = u;
+    Head8<TPT> head8(A.rot, c, hd);
+    uint4 own[kHeads], other[kHeads];
+    const uint16_t* x = A.q + (int64_t)row * A.qs;
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k)
+        if (k < A.per_lane) head8.load(x + (int64_t)min(h0 + k * RPP, A.H - 1) * hd, own[k], other[k]);
+    head8.at(seen ? pos : 0);
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+        if (k >= A.per_lane) continue;
+        float o[8];
+        head8.finish(own[k], other[k], A.g_q, o);
+        if (c >= hd || h0 + k * RPP >= A.H) continue;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (seen) u = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+        *reinterpret_cast<uint4*>(A.q_out + (int64_t)row * A.qos + (int64_t)(h0 + k * RPP) * hd + c) = u;
+    }
 }
 
 struct Read {
@@ -439,12 +578,16 @@ hipError_t launch_kv_append(const prox_kv_cache& c, const prox_kv_batch& b, cons
     A.rot.rot = reinterpret_cast<const float2*>(r.rot);
     A.rot.half = r.rot ? r.rot_dim / 2 : 0;
     A.rot.halves = r.pairing == PROX_ROPE_HALVES;
+    A.rot.wide = (uintptr_t)r.rot % 16 == 0 && A.rot.half % 2 == 0;
     A.rot.eps = (double)r.eps;
     A.H = q ? n_heads : 1;
     A.pp = pages_touched(b);
     const int64_t kvb = (int64_t)b.n_seq * A.pp * c.n_kv * 2;
     const int rpp = kThreads / lanes_per_head(c.head_pad);
-    const int64_t qb = q ? ((int64_t)b.n_tokens * n_heads + rpp - 1) / rpp : 0;
+    // few rows: more blocks, one head a lane
+    A.per_lane = (int64_t)b.n_tokens * n_heads <= 4 * rpp * device_cus() ? 1 : std::min(kHeads, (n_heads + rpp - 1) / rpp);
+    A.head_blocks = (n_heads + rpp * A.per_lane - 1) / (rpp * A.per_lane);
+    const int64_t qb = q ? (int64_t)b.n_tokens * A.head_blocks : 0;
     if (kvb + qb > 0x7fffffffll) return hipErrorInvalidConfiguration;
     A.kv_blocks = (int)kvb;
     return c.kind == PROX_KV_INT8 ? append_kind<PROX_KV_INT8>(A, kvb + qb, s)

@@ -126,11 +126,4 @@ __device__ __forceinline__ int kv_seq_of(const prox_kv_batch& b, int row, int la
     }
     return s;
 }
-// The same for a row some way behind one that belongs to s.
-__device__ __forceinline__ int kv_seq_on(const prox_kv_batch& b, int s, int row) {
-    if (!b.q_start) return row;
-    while (s + 1 < b.n_seq && b.q_start[s + 1] <= row) ++s;
-    return s;
-}
-
 }  // namespace prox
