@@ -26,7 +26,7 @@ struct RotArgs {
     int half;            // rot_dim / 2 (0: no rotation)
     int halves;          // pairing
     int wide;            // table rows are 16-byte aligned
-    double eps;
+    double eps, inv_hd;  // inv_hd: 1 / head_dim
 };
 
 // Channels c .. c + 7 of one head, held by TPT neighbouring lanes (lanes with
@@ -90,7 +90,12 @@ struct Head8 {
             for (int e = 0; e < 8; ++e) ss = fma(v[e], v[e], ss);
 #pragma unroll
             for (int m = 1; m < TPT; m *= 2) ss += __shfl_xor(ss, m);
-            const double inv = 1.0 / sqrt(ss / (double)hd + a.eps);
+            // 1 / sqrt from the hardware's estimate and two Newton steps: the
+            // library's square root and division took most of a chunk's time
+            const double x = fma(ss, a.inv_hd, a.eps);
+            double inv = __builtin_amdgcn_rsq(x);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) inv = fma(0.5 * inv, fma(-x * inv, inv, 1.0), inv);
             if (in) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * (double)gain[c + e];
@@ -223,14 +228,16 @@ __device__ __forceinline__ void row8(const Append& A, int row, int head, int c, 
     }
 }
 
-// One token into a page that keeps its scale (63 of 64 single tokens, nearly):
-// every wave finds out alike, without LDS, and the first lanes store.  Returns
-// whether that was the case.
+// One token into a page that it begins or that keeps its scale (nearly every
+// single token): every wave finds out alike, without LDS, and the first lanes
+// store.  Returns whether that was the case.
 template <int KIND, int TPT, bool VAL>
 __device__ __forceinline__ bool append_one(const Append& A, int page, int head, int slot, int row, int pos) {
-    const int t = threadIdx.x, c = (t % TPT) * 8, hd = A.c.head_dim;
+    const int t = threadIdx.x, c = (t % TPT) * 8, hp = A.c.head_pad;
     const size_t at = (size_t)page * A.c.n_kv + head;
-    const float old = (VAL ? A.c.v_scale : A.c.k_scale)[at];
+    float* scale = (VAL ? A.c.v_scale : A.c.k_scale) + at;
+    const bool fresh = slot == 0;
+    const float old = fresh ? 0.f : *scale;
     float r[8];
     row8<TPT, VAL>(A, row, head, c, pos, false, r);
     uint32_t bits = 0;
@@ -238,14 +245,26 @@ __device__ __forceinline__ bool append_one(const Append& A, int page, int head, 
     for (int e = 0; e < 8; ++e) bits = max(bits, __float_as_uint(r[e]) << 1);
 #pragma unroll
     for (int m = 1; m < TPT; m *= 2) bits = max(bits, (uint32_t)__shfl_xor((int)bits, m));
-    const Quotient<KIND> u(old, bits < 0xff000000u);
-    if (!u.tame || __uint_as_float(bits >> 1) / kv_qmax<KIND>() > old) return false;
-    if (t >= TPT || c >= hd) return true;
-    uint8_t* codes = static_cast<uint8_t*>(VAL ? A.c.v : A.c.k) + at * (size_t)(kKvPage * A.c.head_pad);
+    const float need = __uint_as_float(bits >> 1) / kv_qmax<KIND>();
+    const Quotient<KIND> u(fresh ? need : old, bits < 0xff000000u);
+    if (!u.tame || (!fresh && need > old)) return false;
+    uint8_t* codes = static_cast<uint8_t*>(VAL ? A.c.v : A.c.k) + at * (size_t)(kKvPage * hp);
+    if (fresh) {
+        if (t == 0) *scale = need;
+        // the other slots' bytes; those of slot 0 lie in 16 bytes of their own (K), or first of 16 (V)
+        for (int i = t; i < kKvPage * hp / 16; i += kThreads)
+            if (VAL ? (i & 0x30) != 0 : (i & 0xcf) != 0) reinterpret_cast<uint4*>(codes)[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (t >= TPT || c >= hp) return true;                    // padding channels: zeros
     const uint32_t w[2] = {u.tame4(r), u.tame4(r + 4)};
     if constexpr (VAL) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) codes[kv_v_index(slot, c + e)] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+        for (int e = 0; e < 8; ++e) {
+            uint8_t* to = codes + kv_v_index(slot, c + e);
+            const uint32_t b = (w[e >> 2] >> (8 * (e & 3))) & 0xffu;
+            if (fresh) *reinterpret_cast<uint4*>(to) = make_uint4(b, 0, 0, 0);
+            else *to = (uint8_t)b;
+        }
     } else {
         *reinterpret_cast<uint2*>(codes + kv_k_index(slot, c)) = make_uint2(w[0], w[1]);
     }
@@ -411,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(Append A) {
         const int page = A.b.block_table[(size_t)s * A.b.max_pages + pg];
         if (page < 0 || page >= A.c.n_pages) return;
         const int s0 = a - pg * kKvPage, s1 = b - pg * kKvPage, row0 = R.q0 + (a - R.first);
-        if (s1 - s0 == 1 && s0 > 0) {
+        if (s1 - s0 == 1) {
             if (val ? append_one<KIND, TPT, true>(A, page, head, s0, row0, a)
                     : append_one<KIND, TPT, false>(A, page, head, s0, row0, a)) return;
         }
@@ -580,6 +599,7 @@ hipError_t launch_kv_append(const prox_kv_cache& c, const prox_kv_batch& b, cons
     A.rot.halves = r.pairing == PROX_ROPE_HALVES;
     A.rot.wide = (uintptr_t)r.rot % 16 == 0 && A.rot.half % 2 == 0;
     A.rot.eps = (double)r.eps;
+    A.rot.inv_hd = 1.0 / c.head_dim;
     A.H = q ? n_heads : 1;
     A.pp = pages_touched(b);
     const int64_t kvb = (int64_t)b.n_seq * A.pp * c.n_kv * 2;
