@@ -80,6 +80,8 @@ def main(argv=None):
     ap.add_argument("--decode", action="store_true",
                     help="time a decode step of a Llama-2-7B-shaped 32-layer stack (dense vs Prox FFNs) instead")
     ap.add_argument("--context", type=int, default=512, help="--decode: tokens already in the KV cache")
+    ap.add_argument("--kv-cache", default="dense", choices=["dense", "int8", "fp8"],
+                    help="--decode: the bf16 cache and torch's attention, or the paged 8-bit cache and its kernels")
     ap.add_argument("--copy-calibration", type=int, default=0, metavar="MIB",
                     help="only run a plain device copy of MIB MiB, --steps times (the reference "
                          "for scaling hardware byte counters)")
@@ -438,8 +440,9 @@ def decode_bench(args):
     --context tokens) of a random-weight Llama-2-7B-shaped decoder (d 4096,
     d_ff 11008, 32 heads), with dense bf16 FFNs (torch / hipBLASLt) and with
     Prox FFNs (int8 proxy, keep 60 %, sparsity 70 %; bf16 and int8 Stage-2
-    rows).  Attention and the rest of the block are the same torch code in
-    every variant.  Steps are timed with events on the current stream."""
+    rows).  Attention (torch over a bf16 cache, or with --kv-cache the paged
+    8-bit cache's kernels) and the rest of the block are the same in every
+    variant.  Steps are timed with events on the current stream."""
     import torch
     from free_ffn_activation_prox_amd.decode import DecodeHarness, DecoderShape, random_layers
     wl = workloads()["c2_s70"]
@@ -447,13 +450,16 @@ def decode_bench(args):
     t0 = time.time()
     layers = random_layers(sh, lambda l: gen_weights(wl.config_id, l, sh.d, sh.F), seed=0)
     k_in, k_ff = wl.k_in(), wl.k_ff()
-    variants = {"dense": DecodeHarness(sh, layers, args.context + args.steps + args.warmup + 1, ffn="dense")}
+    # room for the warm-up, the eager steps and (the paged cache, whose captured
+    # step goes on by a token) as many replays
+    kw = dict(max_ctx=args.context + 2 * args.steps + args.warmup + 2, cache=args.kv_cache)
+    if args.kv_cache == "dense":
+        kw["max_ctx"] = args.context + args.steps + args.warmup + 1
+    variants = {"dense": DecodeHarness(sh, layers, ffn="dense", **kw)}
     # the dense FFN on this library's kernels: exact mode keeping every channel
-    variants["dense_library"] = DecodeHarness(sh, layers, args.context + args.steps + args.warmup + 1, ffn="exact",
-                                              k_in=sh.d, k_ff=sh.F)
+    variants["dense_library"] = DecodeHarness(sh, layers, ffn="exact", k_in=sh.d, k_ff=sh.F, **kw)
     for name, ffn in (("prox_int8", "prox"), ("prox_int8_q8rows", "q8")):
-        variants[name] = DecodeHarness(sh, layers, args.context + args.steps + args.warmup + 1, ffn=ffn,
-                                       proxy="int8", k_in=k_in, k_ff=k_ff)
+        variants[name] = DecodeHarness(sh, layers, ffn=ffn, proxy="int8", k_in=k_in, k_ff=k_ff, **kw)
     for h in variants.values():
         h.fill_cache(args.context, seed=1)
     torch.cuda.synchronize()
@@ -496,7 +502,8 @@ def decode_bench(args):
     out = {"metric": "decode step ms (Llama-2-7B-shaped 32-layer stack, batch 1)", "unit": "ms",
            "higher_is_better": False, "steps": args.steps, "warmup": args.warmup,
            "config": {"workload": f"decode: 32 layers d=4096 d_ff=11008 heads=32 context={args.context} "
-                                  f"batch=1; Prox FFN int8 proxy keep=60% sparsity=70% (k_in={k_in} k_ff={k_ff})"},
+                                  f"batch=1; Prox FFN int8 proxy keep=60% sparsity=70% (k_in={k_in} k_ff={k_ff})",
+                      "kv_cache": args.kv_cache},
            "ms_per_step": {k: round(v, 4) for k, v in ms_graph.items()},
            "speedup_vs_dense": {k: round(ms_graph["dense"] / v, 3) for k, v in ms_graph.items() if k != "dense"},
            "speedup_vs_dense_library": {k: round(ms_graph["dense_library"] / v, 3) for k, v in ms_graph.items()
@@ -505,7 +512,7 @@ def decode_bench(args):
                         "dense_library": "FFN through this library's exact mode with every channel kept (k_ff = d_ff)",
                         "prox_int8": "Prox FFN, bf16 Stage-2 rows", "prox_int8_q8rows": "Prox FFN, int8 Stage-2 rows"},
            "timing": "ms_per_step: one step captured in a HIP graph and replayed (GPU time; every replay at the "
-                     "same cache position); eager_ms_per_step: the same step launched op by op from Python",
+                     "same cache position, at the next one with a paged cache); eager_ms_per_step: the same step launched op by op from Python",
            "eager_ms_per_step": {k: round(v, 4) for k, v in ms.items()},
            "context_pages": "1.99x end-to-end decode at 70% FFN sparsity (hardware, model and batch not stated)",
            "data": "synthetic random-init weights (attention N(0,0.02), FFN as workload c2), random KV cache",

@@ -527,3 +527,20 @@ def test_two_streams_at_once_with_their_own_workspaces():
     torch.cuda.synchronize()
     for i, (b, q, ref, ws, s) in enumerate(work):
         assert all(torch.equal(o, ref) for o in outs[i])
+
+
+def test_many_sequences():
+    # more tiles of rows than a wave sees at once; lengths from 0 on, the same pages read by two sequences
+    rng = np.random.default_rng(43)
+    lens = [int(n) for n in rng.integers(0, 150, 150)]
+    w = World("int8", 4, 2, 64, [max(n, 1) for n in lens], seed=43)
+    settle(w, lens)
+    w.table[7] = w.table[3]
+    w.ctx[7] = w.ctx[3]
+    b, start = w.batch([1] * 150, advance=False)
+    w.attend(b, start)
+    new = [int(min(n, k)) for n, k in zip(lens, rng.integers(0, 40, 150))]
+    new[7] = min(new[7], int(w.ctx[7]))
+    b, start = w.batch(new, advance=False)
+    w.attend(b, start)
+    w.attend(b, start, window=20)
