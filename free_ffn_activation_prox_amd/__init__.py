@@ -12,6 +12,7 @@ quantized proxy -> shared channel mask -> exact sparse SwiGLU).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -429,7 +430,8 @@ def _need(ok: bool, what: str) -> None:
 
 def _on(stream, device):
     """(stream pointer, whether the device is the current one) of a call on
-    tensors of `device`: the given stream, else the device's current one."""
+    tensors of `device`: the given stream (the caller's inputs must be ready on
+    it), else the device's current one."""
     if stream is None:
         return _raw_stream(device.index), _current_device() == device.index
     if stream.device != device:
@@ -452,6 +454,12 @@ def _kv_call(fn, where, device, here, *args):
             st = fn(*args)
     if st != PROX_OK:
         _check(st, where)
+
+
+def _made_on(stream):
+    """Context in which a call's own tensors are allocated: the stream that the
+    call runs on, so that their memory is that stream's."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 class KVCache:
@@ -562,7 +570,8 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, *, rot=None, q=None, q_out=N
         qs = _kv_rows("q", q, n, None, hd, dev)
         n_heads, qp = q.shape[1], q.data_ptr()
         if q_out is None:
-            q_out = torch.empty_like(q)
+            with _made_on(stream):
+                q_out = torch.empty_like(q)
         qos = qs if q_out is q else _kv_rows("q_out", q_out, n, n_heads, hd, dev)
         qop = q_out.data_ptr()
     elif q_out is not None:
@@ -600,11 +609,12 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, *, scale: Optional[float] = 
         raise ValueError("cache and batch are on different devices")
     qs = _kv_rows("q", q, n, None, hd, dev)
     n_heads = q.shape[1]
-    if out is None:
-        out = torch.empty_like(q)
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = alloc_kv_workspace(cache, batch, n_heads)
     os_ = _kv_rows("out", out, n, n_heads, hd, dev)
-    if workspace is None:
-        workspace = alloc_kv_workspace(cache, batch, n_heads)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's device")
     sp, here = _on(stream, dev)
@@ -624,10 +634,11 @@ def kv_read(cache: KVCache, batch: KVBatch, *, dtype=torch.bfloat16, k_out=None,
         raise ValueError("dtype must be bfloat16 or float32")
     shape = (batch.n_tokens, cache.n_kv, cache.head_dim)
     if k_out is None and v_out is None:
-        k_out, v_out = torch.empty((2,) + shape, dtype=dtype, device=dev).unbind(0)
+        with _made_on(stream):
+            k_out, v_out = torch.empty((2,) + shape, dtype=dtype, device=dev).unbind(0)
+    elif k_out is None or v_out is None:
+        raise ValueError("k_out and v_out must both be given or neither")
     else:
-        k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
         for t in (k_out, v_out):
             if not (t.dtype is dtype and t.device == dev and t.is_contiguous() and t.shape == shape):
                 raise ValueError("k_out and v_out must be contiguous [n_tokens][n_kv][head_dim] of the dtype")

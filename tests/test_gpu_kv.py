@@ -529,6 +529,28 @@ def test_two_streams_at_once_with_their_own_workspaces():
         assert all(torch.equal(o, ref) for o in outs[i])
 
 
+def test_given_stream_owns_what_the_call_allocates():
+    # calls on a side stream, their workspace and outputs allocated by the calls,
+    # while the current stream allocates and writes memory of the same sizes
+    w = World("int8", 8, 2, 128, [4000, 900], seed=47)
+    settle(w, [4000, 900])
+    P = w.P
+    b, start = w.batch([1, 1], advance=False)
+    q = w.rows(2, 8)
+    ref, _ = w.attend(b, start, q=q)
+    kr, vr = P.kv_read(w.c, b)
+    n = P.kv_workspace_bytes(w.c, b, 8)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for i in range(30):
+        outs.append((P.kv_attention(q, w.c, b, stream=side), *P.kv_read(w.c, b, stream=side)))
+        junk = [torch.full((n + 256,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        del junk
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) and torch.equal(k, kr) and torch.equal(v, vr) for o, k, v in outs)
+
+
 def test_many_sequences():
     # more tiles of rows than a wave sees at once; lengths from 0 on, the same pages read by two sequences
     rng = np.random.default_rng(43)
