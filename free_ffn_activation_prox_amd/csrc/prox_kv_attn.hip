@@ -121,6 +121,7 @@ struct Attend {
     uint32_t HG_inv;       // 2^17 / HG, rounded up
     int HG, VH;            // query heads of a segment; segments of one tile of tokens (key heads x head groups)
     int TQ, tiles;         // tokens of a tile; most tiles of a sequence
+    int rows_lo, rows_hi;  // least and most rows of the sequences that the launch takes
     int slot_rows;
     int seg_cost;          // units of a segment besides its pages
     int no_cut, min_part;  // pages of a segment up to which it is not cut, and least pages of a part
@@ -128,6 +129,13 @@ struct Attend {
     float scale2;          // |scale| * log2(e)
     float sign;            // that of scale
 };
+
+// The rows of sequence s, none if the launch does not take it.
+__device__ __forceinline__ KvRows rows_of(const Attend& A, int s) {
+    KvRows R = kv_rows(A.b, s);
+    if (R.rows < A.rows_lo || R.rows > A.rows_hi) R.rows = 0;
+    return R;
+}
 
 // One tile of tokens of one sequence.
 struct Tile {
@@ -170,61 +178,89 @@ __device__ __forceinline__ void blocks_of(const Attend& A, int piece, int begin,
     w1 = hi / piece;
 }
 
-// The line of all segments (below 2^31, checked on the host), seen by
-// one wave: 64 tiles at a time, tile j = sequence * A.tiles + tile of the
-// sequence, kept in registers where there are no more.
+// The line of all segments (below 2^31, checked on the host), seen by one wave.
+// It looks at 64 tiles at a time, those that there are of 64 sequences: with
+// one prompt among 255 single tokens these are 5 looks, where max_q alone would
+// allow 64 tiles for each sequence (256 looks).
 struct Line {
     const Attend& A;
-    int l, all, total;     // lane; tiles; units
-    KvRows R;              // this lane's tile of the last 64 looked at: its sequence's rows,
-    int pages, upto;       // its pages, and the units up to its end
+    int l, total, looks;   // lane; units; looks that the line takes
+    struct Look {
+        int s0, j0, base;  // first sequence; first of its chunk's tiles; units before it
+    };
+    Look from;             // at() begins here
+    KvRows Q;              // lane: sequence s0 + lane,
+    int last, tiles;       // the chunk's tiles up to its end, and all of them
+    KvRows R;              // lane: a tile's sequence,
+    int s, t, pages, upto; // its number, the tile, its pages, and the units up to its end
 
-    __device__ __forceinline__ void look(int j0, int base) {
-        const int j = j0 + l;
-        R = KvRows{0, 0, 0, 0};
-        pages = 0;
-        if (j < all) {
-            int s = j, t = 0;
-            if (A.tiles > 1) {
-                s = (int)((uint32_t)j / (uint32_t)A.tiles);
-                t = j - s * A.tiles;
-            }
-            R = kv_rows(A.b, s);
-            pages = tile_of(A, R, t).pages;
-        }
-        upto = pages > 0 ? (pages + A.seg_cost) * A.VH : 0;
+    static __device__ __forceinline__ int sum_up(int v, int l) {
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
-            const int u = __shfl_up(upto, m);
-            if (l >= m) upto += u;
+            const int u = __shfl_up(v, m);
+            if (l >= m) v += u;
         }
-        upto += base;
+        return v;
     }
-    __device__ __forceinline__ Line(const Attend& a, int lane) : A(a), l(lane), all(a.b.n_seq * a.tiles) {
-        total = 0;
-        for (int j0 = 0; j0 < all; j0 += 64) {
-            look(j0, total);
-            total = __builtin_amdgcn_readlane(upto, 63);
+    __device__ __forceinline__ void chunk(int s0) {
+        Q = s0 + l < A.b.n_seq ? rows_of(A, s0 + l) : KvRows{0, 0, 0, 0};
+        if (A.tiles > 1) {
+            last = sum_up((int)((uint32_t)(Q.rows + A.TQ - 1) / (uint32_t)A.TQ), l);
+            tiles = __builtin_amdgcn_readlane(last, 63);
+        } else {
+            tiles = 64;        // a lane's sequence is its tile
         }
     }
-    // x < total
-    __device__ __forceinline__ Place at(int x, Tile& T) {
-        int base = 0, j0 = 0;
-        if (all > 64)
-            for (;; j0 += 64) {
-                look(j0, base);
-                if (__ballot(upto > x) || j0 + 64 >= all) break;
-                base = __builtin_amdgcn_readlane(upto, 63);
+    __device__ __forceinline__ void look(const Look& k) {
+        int i = l;
+        R = Q;
+        t = 0;
+        if (A.tiles > 1) {
+            // sequence i, the number of those that end before tile j0 + lane
+            const int j = k.j0 + l;
+            i = 0;
+#pragma unroll
+            for (int m = 32; m > 0; m /= 2)
+                if (__shfl(last, i + m - 1) <= j) i += m;
+            const int before = __shfl(last, i > 0 ? i - 1 : 0);
+            t = j - (i > 0 ? before : 0);
+            R = KvRows{__shfl(Q.q0, i), __shfl(Q.n, i), __shfl(Q.rows, i), __shfl(Q.first, i)};
+            if (j >= tiles) R.rows = 0;
+        }
+        s = k.s0 + i;
+        pages = R.rows > 0 ? tile_of(A, R, t).pages : 0;
+        upto = k.base + sum_up(pages > 0 ? (pages + A.seg_cost) * A.VH : 0, l);
+    }
+    // The looks from k on, until one reaches beyond unit x.
+    __device__ __forceinline__ Look scan(Look k, int x) {
+        chunk(k.s0);
+        for (;;) {
+            while (k.j0 >= tiles) {
+                k = Look{k.s0 + 64, 0, k.base};
+                if (k.s0 >= A.b.n_seq) return k;
+                chunk(k.s0);
             }
+            look(k);
+            ++looks;
+            const int end = __builtin_amdgcn_readlane(upto, 63);
+            if (end > x) return k;
+            k.j0 += 64;
+            k.base = end;
+        }
+    }
+    __device__ __forceinline__ Line(const Attend& a, int lane) : A(a), l(lane), looks(0), from{0, 0, 0} {
+        total = scan(from, 0x7fffffff).base;
+    }
+    // x < total; keep: no later call asks for a unit of an earlier look
+    __device__ __forceinline__ Place at(int x, Tile& T, bool keep) {
+        if (looks > 1) {
+            const Look k = scan(from, x);
+            if (keep) from = k;
+        }
         const int on = __builtin_ctzll(__ballot(upto > x) | (1ull << 63));
         Place p;
-        p.s = j0 + on;
-        p.t = 0;
-        if (A.tiles > 1) {
-            const uint32_t tile = (uint32_t)p.s;
-            p.s = (int)(tile / (uint32_t)A.tiles);
-            p.t = (int)tile - p.s * A.tiles;
-        }
+        p.s = __builtin_amdgcn_readlane(s, on);
+        p.t = __builtin_amdgcn_readlane(t, on);
         p.pages = __builtin_amdgcn_readlane(pages, on);
         const int len = p.pages + A.seg_cost, first = __builtin_amdgcn_readlane(upto, on) - len * A.VH;
         p.vh = (int)((uint32_t)(x - first) / (uint32_t)len);
@@ -235,18 +271,18 @@ struct Line {
     }
 };
 
-// The segment after p.
+// The segment after p, where there is one.
 __device__ __forceinline__ void next_segment(const Attend& A, Place& p, Tile& T) {
     p.begin += p.pages + A.seg_cost;
     if (++p.vh < A.VH) return;
     p.vh = 0;
-    do {
-        if (++p.t == A.tiles) {
-            p.t = 0;
-            ++p.s;
-        }
-        T = tile_of(A, kv_rows(A.b, p.s), p.t);      // called where a segment follows
-    } while (T.pages == 0);
+    KvRows R = T.R;
+    if (++p.t * A.TQ >= R.rows) {
+        p.t = 0;
+        do R = rows_of(A, ++p.s);
+        while (R.rows <= 0);
+    }
+    T = tile_of(A, R, p.t);
     p.pages = T.pages;
 }
 
@@ -753,7 +789,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
     for (int k = 0; k < 3; ++k) {
         int64_t at = k < 2 ? ((int64_t)blockIdx.x + k) * piece : x;
         if (at < line.total) {
-            P = line.at((int)at, T);
+            P = line.at((int)at, T, k == 0);
             if (k < 2) at = cut_in(A, (int)at, P.begin, P.pages);
         } else {
             at = line.total;
@@ -989,10 +1025,11 @@ struct Split {
 constexpr int few_waves(int NP) { return NP <= 2 ? 8 : 4; }
 constexpr int kRowWaves = 8;     // waves of a block where each has rows of its own
 
-Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
+// For sequences of up to max_q tokens.
+Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int max_q) {
     Split p;
     const int rep = n_heads / c.n_kv, NP = c.head_pad / 64;
-    const int64_t most_rows = (int64_t)b.max_q * rep;
+    const int64_t most_rows = (int64_t)max_q * rep;
     p.rows = most_rows > 16;
     p.waves = p.rows ? kRowWaves : few_waves(NP);
     p.NT = p.rows && most_rows > 16 * kRowWaves && NP <= 2 ? 2 : 1;
@@ -1001,8 +1038,8 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     p.HG = (rep + groups - 1) / groups;
     p.VH = c.n_kv * groups;
     p.TQ = RT / p.HG;
-    p.tiles = (b.max_q + p.TQ - 1) / p.TQ;
-    p.slot_rows = (p.TQ < b.max_q ? p.TQ : b.max_q) * p.HG;
+    p.tiles = (max_q + p.TQ - 1) / p.TQ;
+    p.slot_rows = (p.TQ < max_q ? p.TQ : max_q) * p.HG;
     p.seg_cost = p.rows ? 3 : 1;
     p.no_cut = p.rows ? 12 : 32;
     p.min_part = p.rows ? 4 : 8;
@@ -1022,6 +1059,14 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     p.part_bytes = (size_t)p.blocks * 2 * p.slot_rows * row;
     p.bytes = p.part_at + p.part_bytes;
     return p;
+}
+
+// Tokens up to which a sequence goes into a launch of its own kind before that
+// of the longer ones, 0 where all go into one.
+int short_tokens(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
+    const int rep = n_heads / c.n_kv, few = 16 / rep;
+    const bool mixed = (int64_t)b.max_q * rep > 256 && b.n_tokens < (int64_t)b.n_seq * b.max_q;
+    return mixed && (int64_t)b.n_seq * c.n_kv >= device_cus() ? few : 0;
 }
 
 template <int KIND, int NP, int NT, bool ROWS, int kWaves>
@@ -1056,14 +1101,21 @@ hipError_t attend_kind(const Attend& A, const Split& p, hipStream_t s) {
 }  // namespace
 
 size_t kv_attention_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
-    return b.max_q > 0 ? align_up(split_of(c, b, n_heads).bytes, 256) : 256;
+    if (b.max_q <= 0) return 256;
+    const size_t all = split_of(c, b, n_heads, b.max_q).bytes;
+    const int few = short_tokens(c, b, n_heads);
+    const size_t first = few > 0 ? split_of(c, b, n_heads, few).bytes : 0;
+    return align_up(all > first ? all : first, 256);
 }
 
 hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride,
                                int n_heads, float scale, int window, uint16_t* out, int64_t out_stride,
                                void* workspace, hipStream_t s) {
-    const Split p = split_of(c, b, n_heads);
-    if (p.units > 0x7fffffffll) return hipErrorInvalidConfiguration;
+    // one launch behind the other: they share the workspace
+    const int few = short_tokens(c, b, n_heads);
+    const Split split[2] = {split_of(c, b, n_heads, few > 0 ? few : b.max_q), split_of(c, b, n_heads, b.max_q)};
+    for (const Split& p : split)
+        if (p.units > 0x7fffffffll) return hipErrorInvalidConfiguration;
     Attend A{};
     A.c = c;
     A.b = b;
@@ -1072,24 +1124,31 @@ hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, c
     A.qs = q_stride;
     A.os = out_stride;
     A.arrived = static_cast<unsigned long long*>(workspace);
-    A.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_at);
-    A.part_bytes = (uint32_t)p.part_bytes;
-    A.tag = next_call_tag();
     A.rep = n_heads / c.n_kv;
     A.window = window;
-    A.HG = p.HG;
-    A.HG_inv = (131072u + (uint32_t)p.HG - 1) / (uint32_t)p.HG;
-    A.VH = p.VH;
-    A.TQ = p.TQ;
-    A.tiles = p.tiles;
-    A.slot_rows = p.slot_rows;
-    A.seg_cost = p.seg_cost;
-    A.no_cut = p.no_cut;
-    A.min_part = p.min_part;
-    A.min_piece = p.min_piece;
     A.scale2 = fabsf(scale) * 1.4426950408889634f;
     A.sign = scale < 0.f ? -1.f : 1.f;
-    return c.kind == PROX_KV_INT8 ? attend_kind<PROX_KV_INT8>(A, p, s) : attend_kind<PROX_KV_FP8>(A, p, s);
+    for (int k = few > 0 ? 0 : 1; k < 2; ++k) {
+        const Split& p = split[k];
+        A.rows_lo = k == 0 ? 1 : few + 1;
+        A.rows_hi = k == 0 ? few : b.max_q;
+        A.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_at);
+        A.part_bytes = (uint32_t)p.part_bytes;
+        A.tag = next_call_tag();
+        A.HG = p.HG;
+        A.HG_inv = (131072u + (uint32_t)p.HG - 1) / (uint32_t)p.HG;
+        A.VH = p.VH;
+        A.TQ = p.TQ;
+        A.tiles = p.tiles;
+        A.slot_rows = p.slot_rows;
+        A.seg_cost = p.seg_cost;
+        A.no_cut = p.no_cut;
+        A.min_part = p.min_part;
+        A.min_piece = p.min_piece;
+        const hipError_t e = c.kind == PROX_KV_INT8 ? attend_kind<PROX_KV_INT8>(A, p, s) : attend_kind<PROX_KV_FP8>(A, p, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace prox

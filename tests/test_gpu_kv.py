@@ -566,3 +566,38 @@ def test_many_sequences():
     b, start = w.batch(new, advance=False)
     w.attend(b, start)
     w.attend(b, start, window=20)
+
+
+@pytest.mark.parametrize("kind,H,KV,hd", [("int8", 8, 2, 64), ("fp8", 9, 3, 128)])
+def test_long_chunks_among_many_short_sequences(kind, H, KV, hd):
+    # sequences of few tokens and longer ones get launches of their own here: 0 and 1 tokens, the last
+    # number that counts as few and the first that does not, long contexts on both sides
+    rng = np.random.default_rng(H)
+    few = 16 // (H // KV)
+    lens = [int(n) for n in rng.integers(1, 130, 140)]
+    lens[5], lens[77], lens[139] = 5000, 1500, 200
+    w = World(kind, H, KV, hd, lens, seed=H)
+    settle(w, lens)
+    new = [int(min(n, k)) for n, k in zip(lens, rng.choice([0, 1, 1, 1, 2, few, few + 1, 20], 140))]
+    new[5], new[77], new[139] = 1, 700, 130
+    b, start = w.batch(new, advance=False, pad=3)
+    w.attend(b, start)
+    w.attend(b, start, window=100)
+    # a captured call follows the lengths: only short ones, only long ones, both again
+    q = w.rows(b.n_tokens, H, 1.5)
+    out = torch.zeros_like(q)
+    ws = w.P.alloc_kv_workspace(w.c, b, H)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w.P.kv_attention(q, w.c, b, out=out, workspace=ws)
+    for keep in (lambda n: n <= few, lambda n: n > few, lambda n: True):
+        now = [n if keep(n) else 0 for n in new]
+        begin = np.concatenate([[0], np.cumsum(now)]).astype(np.int32)
+        b.q_start.copy_(torch.from_numpy(begin))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        want, tol = KO.attention(w.o, w.table, w.ctx, begin, b.max_q, f64(q), hd ** -0.5, 0)
+        got, idle = f64(out), np.isnan(want).all((1, 2))
+        assert np.array_equal(got[idle], np.full_like(got[idle], 7.0))
+        assert (np.abs(got[~idle] - want[~idle]) <= tol[~idle]).all()
