@@ -544,7 +544,8 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, *, rot=None, q=None, q_out=N
     [head_dim] gains) and the rotation of q and k by position on the way.  rot:
     cos, sin of every position and pair, complex64 [rows][rot_dim / 2] or
     fp32 [rows][rot_dim / 2][2], rows >= 64 * max_pages.  Returns q normed and
-    rotated (bf16; q_out, which may be q, or a new tensor), None without q."""
+    rotated (bf16; q_out, which may be q, or a new tensor), None without q;
+    rows outside every sequence are left as they were."""
     dev, hd, n = cache.device, cache.head_dim, batch.n_tokens
     if batch.device != dev:
         raise ValueError("cache and batch are on different devices")
@@ -626,7 +627,9 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, *, scale: Optional[float] = 
 
 def kv_read(cache: KVCache, batch: KVBatch, *, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
     """The batch's tokens back from the cache: (k, v), each [n_tokens][n_kv]
-    [head_dim] in bf16 or fp32, the values that the codes stand for."""
+    [head_dim] in bf16 or fp32, the values that the codes stand for; zeros where
+    a position or its page does not exist, and rows outside every sequence as
+    they were (a new tensor's are not initialised)."""
     dev = cache.device
     if batch.device != dev:
         raise ValueError("cache and batch are on different devices")

@@ -126,4 +126,34 @@ __device__ __forceinline__ int kv_seq_of(const prox_kv_batch& b, int row, int la
     }
     return s;
 }
+
+// Sequence and page (counted from the first that the sequence's tokens touch)
+// of the i-th such pair of the batch, found by a whole wave at once; false
+// behind the last pair.  A sequence with rows has one pair at least.
+__device__ __forceinline__ bool kv_pair_of(const prox_kv_batch& b, int i, int lane, int& s, int& j) {
+    for (int base = 0; base < b.n_seq; base += 64) {
+        int n = 0;
+        if (base + lane < b.n_seq) {
+            const KvRows R = kv_rows(b, base + lane);
+            const int64_t cap = (int64_t)b.max_pages * kKvPage, end = (int64_t)R.first + R.rows;
+            const int lo = max(R.first, 0), hi = (int)(end < cap ? end : cap);
+            if (R.rows > 0) n = hi > lo ? (hi - 1) / kKvPage - lo / kKvPage + 1 : 1;
+        }
+        int upto = n;
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const int u = __shfl_up(upto, m);
+            if (lane >= m) upto += u;
+        }
+        const uint64_t m = __ballot(upto > i);
+        if (m) {
+            const int on = __builtin_ctzll(m);
+            s = base + on;
+            j = i - (__builtin_amdgcn_readlane(upto, on) - __builtin_amdgcn_readlane(n, on));
+            return true;
+        }
+        i -= __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
 }  // namespace prox

@@ -1,5 +1,5 @@
-// C ABI of the paged 8-bit key/value cache: host-side checks, then one launch.
-// Every check runs before the launch, so an error return enqueues nothing.
+// C ABI of the paged 8-bit key/value cache: host-side checks, then the launches.
+// Every check runs before the first, so an error return enqueues nothing.
 #include "prox.h"
 #include "prox_internal.hpp"
 

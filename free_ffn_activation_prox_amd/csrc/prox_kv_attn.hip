@@ -48,7 +48,17 @@
 // near.  A segment that a cut divides leaves (maximum, sum,
 // unnormalised result) of each part in the workspace, at most two parts for
 // each block, and the block that arrives last combines them in order of
-// position, so results do not depend on timing.
+// position, so results do not depend on timing.  (A launch of its own for that
+// took 5 us of one token's call and up to 100 us of a prompt's.)
+//
+// What bounds it (medians of kernel time, query / key heads x channels; a copy
+// of 2 GiB runs at 4.9 TB/s here, a 16384^3 product in bf16 at 1380 TFLOP/s):
+//   one token, 32 / 32 x 128, 513 positions    11.7 us  the chain of table, scales, keys, values, join (4.2 MB)
+//   one token, 64 / 8 x 128, 131072 positions  63.8 us  268 MB at 4.2 TB/s: memory, read once (counters: 271 MB)
+//   64 ragged sequences, 32 / 8 x 128          52   us  224 MB at 4.3 TB/s: memory
+//   16 sequences of 1 to 6 tokens, 28 / 4 x 128, window 4096   27 us  a page's instructions, 8 waves a CU (39 MB)
+//   4096-token prompt, 32 / 8 x 128           212   us  137 GFLOP at 650 TFLOP/s, see walk_together
+//   ragged chunks, 40 / 8 x 64                242   us  127 GFLOP at 527 TFLOP/s: twice the exponentials a product
 #include "prox_kv.hpp"
 
 namespace prox {
@@ -480,8 +490,7 @@ struct Rows {
         }
     }
 
-    // The weights of a page, 2^shift times what m says, as operands; c: what
-    // the product with the constants gives.
+    // The weights of a page, 2^shift times what m says, as operands.
     __device__ __forceinline__ void weights(const f32x4_t (&w)[NT][4], const float (&fac)[NT], float shift, uint4 (&pw)[NT][2]) const {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
@@ -639,6 +648,8 @@ struct Pages {
 
 // One wave walks pages from .. upto - 1 by itself: the next page's keys are
 // loaded while this one is weighed, its values while its keys are multiplied.
+// 8 such waves keep up to 128 KB of loads in flight in a CU; bare loads of the
+// same order read 6.2 TB/s, this loop 4.2.
 template <int KIND, int NP, int NT>
 __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& A, const Place& P, const Tile& T, int from,
                                            int upto, int r0, int l) {
@@ -689,6 +700,14 @@ __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& 
 // loaded once for the block, each wave turning its share of the codes to fp16
 // operands in LDS (two pages' worth: one is filled while the other is used),
 // so a page costs the block one barrier.
+// A 4096-token prompt takes 212 us so, and 297 where each wave loads and
+// converts its own operands.  Two waves share a SIMD (229 registers); the
+// matrix unit is busy 36 % of the time and no single unit is the bound: with the
+// LDS reads, exponentials, weights or fills left out in turn the time fell by 0
+// to 20 of 224 us, with the products left out by 24.  Measured and not kept:
+// the next page's keys multiplied beside the exponentials (322 us, spills), two
+// groups of waves half a page apart (220), four waves in each of two blocks
+// (244), one tile of 16 rows a wave: 8 waves 299, 12 waves 233, 16 waves 271.
 // LDS: keys [2][4 NP x 2 operands][64] uint4, values the same.
 template <int KIND, int NP, int NT, int kWaves>
 __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds, const Attend& A, const Place& P,
@@ -1020,18 +1039,23 @@ struct Split {
     size_t part_at, part_bytes, lds, bytes;
 };
 
-// Most waves of a block where the waves share a tile: wide heads take more
-// registers than 8 waves have.
+// Most waves of a block where the waves share a tile: with heads wider than 128
+// a wave takes 300 to 371 registers, which 8 waves of a CU do not have.
 constexpr int few_waves(int NP) { return NP <= 2 ? 8 : 4; }
-constexpr int kRowWaves = 8;     // waves of a block where each has rows of its own
+// Waves of a block where each has rows of its own: see walk_together.
+constexpr int kRowWaves = 8;
 
 // For sequences of up to max_q tokens.
 Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int max_q) {
     Split p;
     const int rep = n_heads / c.n_kv, NP = c.head_pad / 64;
     const int64_t most_rows = (int64_t)max_q * rep;
+    // More than 16 rows get tiles with rows for each wave: sequences of up to 6 tokens and 7 query heads a
+    // key head take 27 us so, and 41 in tiles of 16 rows, each of which reads the pages again.
     p.rows = most_rows > 16;
     p.waves = p.rows ? kRowWaves : few_waves(NP);
+    // 32 rows a wave use each operand from LDS twice: a prompt 209 us, with 16 rows a wave 299.  Up to 16
+    // rows for each of the 8 waves there is nothing to use twice; heads wider than 128 would not fit.
     p.NT = p.rows && most_rows > 16 * kRowWaves && NP <= 2 ? 2 : 1;
     const int RT = p.rows ? 16 * p.NT * kRowWaves : 16;
     const int groups = (rep + RT - 1) / RT;
@@ -1040,6 +1064,15 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int 
     p.TQ = RT / p.HG;
     p.tiles = (max_q + p.TQ - 1) / p.TQ;
     p.slot_rows = (p.TQ < max_q ? p.TQ : max_q) * p.HG;
+    // In pages' time.  Kernel times in us of: one token at 513 positions, at 131072, 64 ragged sequences |
+    // sequences of 1 to 6 tokens, a prompt, ragged chunks (those of the head of this file).
+    //   as it is               11.6  63.8  51.6 | 26.8  213  240
+    //   seg_cost 0 | 1         11.2  63.3  65.2 | 31.1  303  244
+    //   seg_cost 2 | 6         10.9  63.7  51.7 | 27.8  211  241
+    //   no_cut 16 | 24         11.6  63.8  51.9 | 27.9  212  246
+    //   no_cut 64              11.6  63.5  54.5 |
+    //   min_piece 4            11.5  63.7  52.0 | 26.7  217  243
+    //   min_piece 16           14.0  64.1  51.2 | 34.8  216  244
     p.seg_cost = p.rows ? 3 : 1;
     p.no_cut = p.rows ? 12 : 32;
     p.min_part = p.rows ? 4 : 8;
@@ -1061,8 +1094,17 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int 
     return p;
 }
 
-// Tokens up to which a sequence goes into a launch of its own kind before that
-// of the longer ones, 0 where all go into one.
+// Tokens up to which a sequence goes into a launch of its own kind (tiles of 16
+// rows, waves that split the pages) before that of the longer ones, 0 where all
+// go into one.  In a tile for 8 waves a single token keeps one wave busy, and a
+// line of many such segments leaves the long ones too few blocks:
+//   a 4096-token prompt and 255 tokens at 1000 positions: one launch 532 us, two 309
+//   a 512-token prompt and 31 such tokens:                           66        53
+//   2 chunks of 512 and 30 tokens at 20000 positions:               654       275
+//   40 chunks of 9 to 243 tokens, none short:                       159.1     159.7
+// One launch where the host sees that all sequences are alike, where the longest
+// fits one tile, or where there cannot be a short segment for each block (a
+// prompt and 15 tokens: 200 us).
 int short_tokens(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     const int rep = n_heads / c.n_kv, few = 16 / rep;
     const bool mixed = (int64_t)b.max_q * rep > 256 && b.n_tokens < (int64_t)b.n_seq * b.max_q;
@@ -1101,11 +1143,8 @@ hipError_t attend_kind(const Attend& A, const Split& p, hipStream_t s) {
 }  // namespace
 
 size_t kv_attention_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
-    if (b.max_q <= 0) return 256;
-    const size_t all = split_of(c, b, n_heads, b.max_q).bytes;
-    const int few = short_tokens(c, b, n_heads);
-    const size_t first = few > 0 ? split_of(c, b, n_heads, few).bytes : 0;
-    return align_up(all > first ? all : first, 256);
+    // a launch for short sequences has fewer blocks and rows, so this holds it too
+    return b.max_q > 0 ? align_up(split_of(c, b, n_heads, b.max_q).bytes, 256) : 256;
 }
 
 hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride,

@@ -601,3 +601,26 @@ def test_long_chunks_among_many_short_sequences(kind, H, KV, hd):
         got, idle = f64(out), np.isnan(want).all((1, 2))
         assert np.array_equal(got[idle], np.full_like(got[idle], 7.0))
         assert (np.abs(got[~idle] - want[~idle]) <= tol[~idle]).all()
+
+
+@pytest.mark.parametrize("kind,hd", [("int8", 64), ("fp8", 128)])
+def test_append_and_read_of_a_long_chunk_among_many_short_sequences(kind, hd):
+    # more than 64 sequences, of which one has many pages: blocks find their pages in the lengths
+    lens = [1 + (7 * s) % 130 for s in range(140)]
+    w = World(kind, 4, 2, hd, [n + 40 for n in lens[:99]] + [1200] + [n + 40 for n in lens[100:]], seed=hd)
+    settle(w, lens)
+    w.append([s % 3 for s in range(99)] + [1000] + [1] * 40, norm=True, pad=2)
+    w.table[3, 0] = -1
+    w.ctx[100] = 0                                     # its row has no position
+    new = [s % 4 for s in range(99)] + [900] + [1] * 40
+    b, start = w.batch([min(n, 1000) for n in new], advance=False, pad=3)
+    ko, vo = (torch.full((b.n_tokens, 2, hd), 7.0, dtype=torch.float32, device="cuda") for _ in range(2))
+    w.P.kv_read(w.c, b, dtype=torch.float32, k_out=ko, v_out=vo)
+    kw, vw = (np.full((b.n_tokens, 2, hd), 7.0) for _ in range(2))
+    for s, row, pos in KO.rows_of(start, w.ctx, b.n_tokens, b.max_q):
+        kw[row] = vw[row] = 0
+        if pos >= 0:
+            k, v, there = KO.gather(w.o, w.table, s, pos, pos + 1)
+            if there[0]:
+                kw[row], vw[row] = k[0].astype(np.float32), v[0].astype(np.float32)
+    assert np.array_equal(f64(ko), kw) and np.array_equal(f64(vo), vw)
