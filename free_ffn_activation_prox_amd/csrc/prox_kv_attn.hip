@@ -58,6 +58,7 @@
 //   64 ragged sequences, 32 / 8 x 128          52   us  224 MB at 4.3 TB/s: memory
 //   16 sequences of 1 to 6 tokens, 28 / 4 x 128, window 4096   27 us  a page's instructions, 8 waves a CU (39 MB)
 //   4096-token prompt, 32 / 8 x 128           212   us  137 GFLOP at 650 TFLOP/s, see walk_together
+//   16384-token prompt                       2278   us  2199 GFLOP at 965 TFLOP/s: begins and joins weigh less
 //   ragged chunks, 40 / 8 x 64                242   us  127 GFLOP at 527 TFLOP/s: twice the exponentials a product
 #include "prox_kv.hpp"
 
