@@ -627,8 +627,10 @@ struct Pages {
         base = p;
         id = table[min(p + l, upto - 1)];
         id = p + l < upto && id >= 0 && id < A.c.n_pages ? id : -1;
-        ks = A.c.k_scale[where(id)];
-        vs = A.c.v_scale[where(id)];
+        // a page that is not there has scales of 0, whatever those at where(-1), another page's, hold
+        const float k0 = A.c.k_scale[where(id)], v0 = A.c.v_scale[where(id)];
+        ks = id >= 0 ? k0 : 0.f;
+        vs = id >= 0 ? v0 : 0.f;
     }
     // pages p .. p + 2 are looked at next
     __device__ __forceinline__ void follow(int p, int l) {
