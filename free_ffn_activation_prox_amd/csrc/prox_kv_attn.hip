@@ -9,10 +9,13 @@
 // Arithmetic.  Both products run on v_mfma_f32_16x16x32_f16 with fp32 sums.
 //   codes  are exact in fp16.  An int8 code c is taken as 1024 + (c + 128): the
 //          byte put under the exponent bits 0x64, half an instruction a code
-//          where a conversion takes one and a half; the 1152 too many are
-//          subtracted as a start value of the sum, -1152 sum(q) and -1152
-//          sum(p), so the fp32 sums run over values up to 1279 / 127 times
-//          larger than the codes' own.
+//          where a conversion takes one and a half.  For keys the 1152 too many
+//          are subtracted as a start value of the sum, -1152 sum(q), so a
+//          score's fp32 sum runs over values up to 1279 / 127 times larger than
+//          the codes' own.  For values they are subtracted from each pair of
+//          codes (exact in fp16, one instruction): left in sums that run over
+//          many pages they cost five bits and more, 1.6e-3 of a mean of 256
+//          pages and 1.4e-2 of one of 2048.
 //   q      (bf16, 8 bits) is scaled by a power of two to a largest value in
 //          [1, 2): exact in fp16 down to 2^-17 of the row's largest, and off
 //          by at most 2^-25 of that below.
@@ -97,13 +100,22 @@ __device__ __forceinline__ uint4 codes_f16(uint32_t lo, uint32_t hi) {
     }
 }
 
-// What a product with a column of these constants gives: -1152 times the
-// operand's sum (int8), or the sum itself.
+// The same for values: int8 without the 1152.
 template <int KIND>
-__device__ __forceinline__ uint4 constants() {
-    const uint32_t w = KIND == PROX_KV_INT8 ? 0xe480e480u : 0x3c003c00u;      // -1152 or 1, twice
-    return make_uint4(w, w, w, w);
+__device__ __forceinline__ uint4 values_f16(uint32_t lo, uint32_t hi) {
+    uint4 x = codes_f16<KIND>(lo, hi);
+    if constexpr (KIND == PROX_KV_INT8) {
+        auto less = [](uint32_t w) {
+            return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, w) - f16x2_t{(_Float16)1152.f, (_Float16)1152.f});
+        };
+        x = make_uint4(less(x.x), less(x.y), less(x.z), less(x.w));
+    }
+    return x;
 }
+
+// Operands whose product with another one gives that one's sum, or -1152 times it.
+__device__ __forceinline__ uint4 ones() { return make_uint4(0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u); }
+__device__ __forceinline__ uint4 minus_1152() { return make_uint4(0xe480e480u, 0xe480e480u, 0xe480e480u, 0xe480e480u); }
 
 // e4m3 codes with NaN taken as 0: slots that no token was written to may hold
 // any byte, and 0 x NaN would reach the sum.
@@ -348,7 +360,6 @@ template <int KIND, int NP, int NT>
 struct Rows {
     f32x4_t o[NT][4 * NP];      // lane (g, n): channels 16 d + 4 g + r of row 16 u + n, in units of s
     float m[NT], sum[NT];
-    float over[NT];             // int8: what the 1152 too many of the codes have added to every channel of o, negative
     float s;                    // unit of o
     bool live[NT];
     int key_lo[NT], key_hi[NT]; // positions that the row sees: key_lo .. key_hi - 1
@@ -410,11 +421,11 @@ struct Rows {
                                             pack_f16(bf16_lo(x.y) * down, bf16_hi(x.y) * down),
                                             pack_f16(bf16_lo(x.z) * down, bf16_hi(x.z) * down),
                                             pack_f16(bf16_lo(x.w) * down, bf16_hi(x.w) * down));
-                    if constexpr (KIND == PROX_KV_INT8) b4 = mfma16(constants<KIND>(), q[u][a][e], b4);
+                    if constexpr (KIND == PROX_KV_INT8) b4 = mfma16(minus_1152(), q[u][a][e], b4);
                 }
             bias[u] = b4[0];
             m[u] = -INFINITY;
-            sum[u] = over[u] = 0.f;
+            sum[u] = 0.f;
 #pragma unroll
             for (int d = 0; d < 4 * NP; ++d) o[u][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
@@ -484,7 +495,6 @@ struct Rows {
                 const float keep = __builtin_amdgcn_exp2f(m[u] - base);
                 m[u] = mn;
                 sum[u] *= keep;
-                over[u] *= keep * f;
 #pragma unroll
                 for (int d = 0; d < 4 * NP; ++d) o[u][d] *= keep * f;
             }
@@ -507,12 +517,6 @@ struct Rows {
             pw[u][1] = make_uint4(e[2][0], e[2][1], e[3][0], e[3][1]);
         }
     }
-    __device__ __forceinline__ f32x4_t of_constants(const uint4 (&pw)[2]) const {
-        f32x4_t c = {0.f, 0.f, 0.f, 0.f};
-        c = mfma16(constants<KIND>(), pw[0], c);
-        return mfma16(constants<KIND>(), pw[1], c);
-    }
-
     // The values of a page: vals(d, x, y) gives the two operands of channels
     // 16 d; the weights hold `ratio`.
     template <typename V>
@@ -581,12 +585,13 @@ struct Rows {
     }
     // The weights' own sums.
     __device__ __forceinline__ void weigh(const uint4 (&pw)[NT][2], float ratio) {
-        const float back = (KIND == PROX_KV_INT8 ? -1.f / 1152.f : 1.f) * __builtin_amdgcn_rcpf(ratio);
+        const float back = __builtin_amdgcn_rcpf(ratio);
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const float c = of_constants(pw[u])[0];
-            sum[u] = fmaf(c, back, sum[u]);
-            if constexpr (KIND == PROX_KV_INT8) over[u] += c;
+            f32x4_t c = {0.f, 0.f, 0.f, 0.f};
+            c = mfma16(ones(), pw[u][0], c);
+            c = mfma16(ones(), pw[u][1], c);
+            sum[u] = fmaf(c[0], back, sum[u]);
         }
     }
     // vs / s as the weights take it (a page of zeros takes none of it).
@@ -601,8 +606,7 @@ struct Rows {
         for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int d = 0; d < 4 * NP; ++d)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[u][d][r] = (o[u][d][r] + over[u]) * s;
+                o[u][d] *= s;
     }
 };
 
@@ -692,8 +696,8 @@ __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& 
         w.values(pw, ratio, [&](int d, uint4& x, uint4& y) {
             uint4 c = vf[d];
             if (clean) c = make_uint4(no_nan_fp8(c.x), no_nan_fp8(c.y), no_nan_fp8(c.z), no_nan_fp8(c.w));
-            x = codes_f16<KIND>(c.x, c.y);
-            y = codes_f16<KIND>(c.z, c.w);
+            x = values_f16<KIND>(c.x, c.y);
+            y = values_f16<KIND>(c.z, c.w);
         });
     }
     w.finish();
@@ -734,15 +738,24 @@ __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds,
             c[j] = buf_load16(r, l * 16 + ch * 1024, 0);
         }
     };
-    auto fill = [&](uint4* to, const uint4 (&c)[kOwn], bool clean) {
+    auto fill_keys = [&](uint4* to) {
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
             const int ch = wv + j * kWaves;
             if (kChunks % kWaves && ch >= kChunks) continue;
-            uint4 x = c[j];
+            to[(2 * ch) * 64] = codes_f16<KIND>(kc[j].x, kc[j].y);
+            to[(2 * ch + 1) * 64] = codes_f16<KIND>(kc[j].z, kc[j].w);
+        }
+    };
+    auto fill_values = [&](uint4* to, bool clean) {
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            const int ch = wv + j * kWaves;
+            if (kChunks % kWaves && ch >= kChunks) continue;
+            uint4 x = vc[j];
             if (clean) x = make_uint4(no_nan_fp8(x.x), no_nan_fp8(x.y), no_nan_fp8(x.z), no_nan_fp8(x.w));
-            to[(2 * ch) * 64] = codes_f16<KIND>(x.x, x.y);
-            to[(2 * ch + 1) * 64] = codes_f16<KIND>(x.z, x.w);
+            to[(2 * ch) * 64] = values_f16<KIND>(x.x, x.y);
+            to[(2 * ch + 1) * 64] = values_f16<KIND>(x.z, x.w);
         }
     };
     auto unclean = [&](int p) { return KIND == PROX_KV_FP8 && (T.pg0 + p + 1) * kKvPage > ctx; };
@@ -750,9 +763,9 @@ __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds,
     load(vc, A.c.v, pages.at(from));
     w.begin(A);
     lds_barrier();                                                  // the last segment's pages are done with
-    fill(kl, kc, false);
+    fill_keys(kl);
     load(kc, A.c.k, pages.at(from + 1));
-    fill(vl, vc, unclean(from));
+    fill_values(vl, unclean(from));
     load(vc, A.c.v, pages.at(from + 1));
     lds_barrier();
     for (int p = from; p < upto; ++p) {
@@ -772,9 +785,9 @@ __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds,
             w.values_lds(pw, ratio, vl + buf * kSize, first);
         }
         // the other half was used a turn ago
-        fill(vl + (buf ^ 1) * kSize, vc, unclean(p + 1));
+        fill_values(vl + (buf ^ 1) * kSize, unclean(p + 1));
         load(vc, A.c.v, pages.at(p + 2));
-        fill(kl + (buf ^ 1) * kSize, kc, false);
+        fill_keys(kl + (buf ^ 1) * kSize);
         load(kc, A.c.k, pages.at(p + 2));
         lds_barrier();
     }

@@ -172,10 +172,11 @@ def attention(cache: Cache, table, ctx, q_start, max_q, q, scale, window=0, n_ou
         32 products with no more than 8) of sums up to (1152 + 1279) sum(|q|)
         units of the key's scale;
       - q's channels below 2^-17 of the row's largest are off by 2^-25 of that;
-    and 2^-21 for exp2.  The sums over the keys: for int8 20 roundings a page of
-    sums up to (1152 + 1279) w_j units of the value's scale, and one rounding
-    of the running result a page, as for e4m3 (plus the products' own, 20).  The
-    bf16 result is rounded by at most 2^-8 |o|.  A weight under 2^-126 of the
+    and 2^-21 for exp2.  The sums over the keys: a page adds two matrix
+    instructions' 32 products to the running sums, with no more than 8 roundings
+    each, and takes part in at most one rescaling and one join of parts (3
+    roundings), all of sums up to sum_j w_j |v_j|: 20 a page, and 20 for the rest.
+    The bf16 result is rounded by at most 2^-8 |o|.  A weight under 2^-126 of the
     row's largest is no normal fp32 number and may be taken as 0."""
     T, H, hd = q.shape
     out = np.full((T, H, hd), np.nan)
@@ -192,8 +193,8 @@ def attention(cache: Cache, table, ctx, q_start, max_q, q, scale, window=0, n_ou
             last = min(int(ctx[s]), PAGE * table.shape[1])
             got = gather(cache, table, s, 0, max(last, 1))
             page = np.where(got[2], table[s, np.arange(max(last, 1)) // PAGE], 0)
-            vals[s] = got + (cache.ks[page].astype(np.float64), cache.vs[page].astype(np.float64))
-        K, V, there, KS, VS = vals[s]
+            vals[s] = got + (cache.ks[page].astype(np.float64),)
+        K, V, there, KS = vals[s]
         lo = max(0, pos - window + 1) if window else 0
         see = np.flatnonzero(there[lo:pos + 1]) + lo
         if see.size == 0:
@@ -206,16 +207,14 @@ def attention(cache: Cache, table, ctx, q_start, max_q, q, scale, window=0, n_ou
             w /= w.sum()
             o = w @ v
             aq = np.abs(q[row, h])
-            unit_k, unit_v = KS[see, h // rep], VS[see, h // rep]
+            unit_k = KS[see, h // rep]
             if int8:
                 eta = hd / 2 * r24 * big * unit_k * aq.sum() + 8 * r24 * (np.abs(k) @ aq)
             else:
                 eta = (hd + 8) * r24 * (np.abs(k) @ aq)
             eta = abs(scale) * (eta + 2.0 ** -25 * aq.max() * np.abs(k).sum(-1)) + 2.0 ** -21
             pages = see.size / PAGE + 2
-            sums = (pages + 20) * r24 * (w @ np.abs(v))
-            if int8:
-                sums = sums + 20 * r24 * big * (w @ unit_v)
+            sums = 20 * (pages + 1) * r24 * (w @ np.abs(v))
             out[row, h] = o
             tol[row, h] = (2.0 ** -8 * np.abs(o) + (w * (1.02 * (u + eta))) @ np.abs(v - o) + sums
                            + see.size * 2.0 ** -33 * np.abs(v - o).max(0) + 1e-37)
