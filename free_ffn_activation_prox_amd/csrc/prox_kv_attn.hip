@@ -24,14 +24,17 @@
 //          of a row's largest.  The sum that the result is divided by is that
 //          of the rounded weights (a product with a row of constants), which
 //          keeps the result a weighted mean of the stored values.
-//   sv     goes into the weights: p sv / s with s the unit of the sums, one
-//          more term of the exponent, so the values' sums stay in the matrix
+//   sv     goes into the weights: p sv / 2^e with 2^e the unit of a row's sums,
+//          one more term of the exponent, so the values' sums stay in the matrix
 //          unit's accumulators from page to page; the sum of the weights takes
-//          it out again.  s moves where sv / s leaves 2^-12 .. 1, for below that
-//          the weights would be fp16 subnormals (down by 2^80 at most at once:
-//          what values so much smaller than others add may be off by 2^-85 of
-//          the larger ones).
-// m and s move only when a score exceeds m by more than 2^6 or an sv leaves its
+//          it out again.  e moves up where p sv / 2^e leaves the weights' range,
+//          so a page that has no weight in a row moves nothing there, and down
+//          where sv / 2^e falls below 2^-12, as far as the row's sums allow:
+//          they stay below 2^100.  A page for which they do not allow it counts
+//          as 2^-12 of the unit, less than 2^-60 of the row's largest sum.
+//          m and e are whole numbers: moving them rounds nothing, and value
+//          scales of any fp32 size give the same result in their unit.
+// m and e move only when a score exceeds m by more than 2^6 or an sv leaves its
 // range, so most pages rescale nothing.
 //
 // A wave takes tiles of 16 rows that share a key head and walks their pages.
@@ -48,7 +51,7 @@
 // lengths of the sequences.  A block finds its piece from the lengths on the
 // device (the host knows bounds only, and a captured call follows the lengths).
 // A cut moves to a segment's border where the segment is short or the border
-// near.  A segment that a cut divides leaves (maximum, sum,
+// near.  A segment that a cut divides leaves (maximum, sum, unit,
 // unnormalised result) of each part in the workspace, at most two parts for
 // each block, and the block that arrives last combines them in order of
 // position, so results do not depend on timing.  (A launch of its own for that
@@ -138,7 +141,7 @@ struct Attend {
     uint16_t* out;
     int64_t qs, os;
     unsigned long long* arrived;   // [blocks]: arrivals of the cut segment that begins in a block's piece
-    float* part;                   // [blocks][2][slot_rows][head_pad + 4]: result, then maximum and sum
+    float* part;                   // [blocks][2][slot_rows][head_pad + 4]: result, then maximum, sum and unit
     uint32_t part_bytes, tag;
     int rep, window;
     uint32_t HG_inv;       // 2^17 / HG, rounded up
@@ -320,14 +323,39 @@ __device__ __forceinline__ uint2 bf16x4(f32x4_t v) {
 // 1 / the softmax sum: 0 for a row that has seen nothing; a NaN sum stays.
 __device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); }
 
-// Part (m, sum, v) joins (m0, s0, o).
-__device__ __forceinline__ void join(float& m0, float& s0, f32x4_t& o, float m, float sum, f32x4_t v) {
-    const float mn = fmaxf(m0, m), base = mn > -INFINITY ? mn : 0.f;
-    const float f = __builtin_amdgcn_exp2f(m0 - base), e = __builtin_amdgcn_exp2f(m - base);
-    m0 = mn;
-    s0 = s0 * f + sum * e;
+// A weight's rows hold up to 2^(kTop + kSlack): see "Arithmetic" above.
+constexpr float kTop = 8.f, kSlack = 6.f;
+constexpr int kLeast = -12;            // exponent of the least sv / 2^e that goes into the weights
+constexpr int kRoom = 100;             // exponent that a row's sums stay below when e moves down
+constexpr int kNoUnit = -1000;         // e of a row that has seen no value but zeros
+constexpr float kNothing = -0x1p126f;  // m of a row that has seen nothing; scores are above
+constexpr float kLarge = 0x1p20f;      // maxima from here on: see limits()
+
+// A result in its own units.
+__device__ __forceinline__ f32x4_t result(f32x4_t o, float inv, float e) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] = o[r] * f + v[r] * e;
+    for (int r = 0; r < 4; ++r) o[r] = ldexpf(o[r] * inv, (int)e);
+    return o;
+}
+
+// What a row's part is besides its results: its maximum, sum and unit.
+struct Part {
+    float m, sum, e;
+};
+__device__ __forceinline__ Part no_part() { return Part{kNothing, 0.f, (float)kNoUnit}; }
+__device__ __forceinline__ float4 packed(const Part& p) { return make_float4(p.m, p.sum, p.e, 0.f); }
+__device__ __forceinline__ Part unpacked(float4 f) { return Part{f.x, f.y, f.z}; }
+
+// Part (p, v) joins (a, o), in the larger of their units 2^(m + e).  m + e is
+// never formed: m may be so large that it would swallow e.
+__device__ __forceinline__ void join(Part& a, f32x4_t& o, const Part& p, f32x4_t v) {
+    const float mn = fmaxf(a.m, p.m), t = (p.m - a.m) + (p.e - a.e);
+    const float f = t > 0.f ? __builtin_amdgcn_exp2f(-t) : 1.f, g = t > 0.f ? 1.f : __builtin_amdgcn_exp2f(t);
+    a.e = t > 0.f ? p.e + (p.m - mn) : a.e + (a.m - mn);
+    a.sum = a.sum * __builtin_amdgcn_exp2f(a.m - mn) + p.sum * __builtin_amdgcn_exp2f(p.m - mn);
+    a.m = mn;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = o[r] * f + v[r] * g;
 }
 
 // What the rows of a segment need to be put together later.
@@ -350,17 +378,14 @@ __device__ __forceinline__ uint16_t* out_row(const Attend& A, const Seg& S, int 
     return A.out + (int64_t)(S.row0 + i) * A.os + (int64_t)(head * A.rep + hq) * A.c.head_dim;
 }
 
-// A weight's rows hold up to 2^(kTop + kSlack): see "Arithmetic" above.
-constexpr float kTop = 8.f, kSlack = 6.f;
-constexpr float kLeast = 0x1p-12f;     // least vs / s that goes into the weights
-
 // The rows r0 .. r0 + 16 NT - 1 of a segment's tile in one wave: what they see,
-// q, and the running maxima, sums and results.
+// q, and the running maxima, sums, units and results.
 template <int KIND, int NP, int NT>
 struct Rows {
-    f32x4_t o[NT][4 * NP];      // lane (g, n): channels 16 d + 4 g + r of row 16 u + n, in units of s
+    f32x4_t o[NT][4 * NP];      // lane (g, n): channels 16 d + 4 g + r of row 16 u + n, in units of 2^e
     float m[NT], sum[NT];
-    float s;                    // unit of o
+    int e[NT];
+    int unit;                   // e of every row that has seen a key, kNoUnit where they differ or an m is kLarge
     bool live[NT];
     int key_lo[NT], key_hi[NT]; // positions that the row sees: key_lo .. key_hi - 1
     uint4 q[NT][NP][2];
@@ -424,12 +449,13 @@ struct Rows {
                     if constexpr (KIND == PROX_KV_INT8) b4 = mfma16(minus_1152(), q[u][a][e], b4);
                 }
             bias[u] = b4[0];
-            m[u] = -INFINITY;
+            m[u] = kNothing;
             sum[u] = 0.f;
+            e[u] = kNoUnit;
 #pragma unroll
             for (int d = 0; d < 4 * NP; ++d) o[u][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-        s = 0.f;
+        unit = kNoUnit;
     }
 
     // The scores of one page, in units of fac: keys(a, t, x, y) gives the two
@@ -452,10 +478,12 @@ struct Rows {
         }
     }
 
-    // Masks the scores of positions base_key .. + 63 (none is seen if `gone`)
-    // and moves m and s where this page needs it.
-    __device__ __forceinline__ void limits(f32x4_t (&w)[NT][4], float (&fac)[NT], int base_key, bool gone, float ks, float vs,
-                                           int l) {
+    // Masks the scores of positions base_key .. + 63 (none is seen if `gone`),
+    // moves m and e where this page, of value scale 2^(ve + vl - kTop), needs it,
+    // and says what the weights are: 2^(w fac - base), and `back` to their sum.
+    __device__ __forceinline__ void limits(f32x4_t (&w)[NT][4], float (&fac)[NT], float (&base)[NT], float (&back)[NT],
+                                           int base_key, bool gone, float ks, int ve, float vl, int l) {
+#pragma clang fp contract(off)
         const int g = l >> 4;
         // keys that a row does not see; most pages are seen whole by every row
         bool open = !gone;
@@ -474,54 +502,110 @@ struct Rows {
                     }
             }
         }
+        const bool some = ve != kNoUnit;                // the page has values other than zeros
+        // a page without counts as one of the unit's scale: its values are read as zeros
+        const int under = some ? unit - ve : 0;
+        const bool fits = unit != kNoUnit && (uint32_t)under < (uint32_t)-kLeast;
         float top[NT];
-        bool grow = vs > s || (vs > 0.f && vs < s * kLeast);
+        bool move = false;
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            // not 0 (a page of zeros): 0 x -inf would be NaN; the scores of such a page vanish all the same
-            fac[u] = fmaxf(ks * row_scale[u], 1e-37f);
+            // not 0 (a page of zeros): 0 x -inf would be NaN; the scores of such a page vanish all the same.
+            // Not above 2^106: the largest w is below 2^19, so scores stay finite
+            fac[u] = __builtin_amdgcn_fmed3f(ks * row_scale[u], 1e-37f, 0x1p106f);
             float most = w[u][0][0];
 #pragma unroll
-            for (int e = 1; e < 16; ++e) most = fmaxf(most, w[u][e >> 2][e & 3]);
+            for (int i = 1; i < 16; ++i) most = fmaxf(most, w[u][i >> 2][i & 3]);
             top[u] = over_groups_max(most) * fac[u];
-            grow = grow || top[u] > m[u] + kSlack;
+            move = move || top[u] - m[u] > kSlack;
         }
-        if (__ballot(grow)) {
-            const float sn = vs > s || (vs > 0.f && vs < s * kLeast) ? fmaxf(vs, s * 0x1p-80f) : s, f = sn > 0.f ? s / sn : 1.f;
-            s = sn;
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                const float mn = fmaxf(m[u], top[u]), base = mn > -INFINITY ? mn : 0.f;
-                const float keep = __builtin_amdgcn_exp2f(m[u] - base);
-                m[u] = mn;
-                sum[u] *= keep;
-#pragma unroll
-                for (int d = 0; d < 4 * NP; ++d) o[u][d] *= keep * f;
-            }
-        }
-    }
-
-    // The weights of a page, 2^shift times what m says, as operands.
-    __device__ __forceinline__ void weights(const f32x4_t (&w)[NT][4], const float (&fac)[NT], float shift, uint4 (&pw)[NT][2]) const {
+        const float ratio = vl - (float)under, same = __builtin_amdgcn_exp2f(-ratio);
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const float base = (m[u] > -INFINITY ? m[u] : 0.f) - shift;
-            uint32_t e[4][2];
+            base[u] = m[u] - ratio;
+            back[u] = same;
+        }
+        if (__builtin_expect(!fits || __ballot(move) != 0, 0)) this->move(w, top, fac, base, back, some, ve, vl);
+    }
+
+    // limits() where some row's m or e moves, or the rows differ in e.
+    __device__ __forceinline__ void move(f32x4_t (&w)[NT][4], const float (&top)[NT], float (&fac)[NT], float (&base)[NT],
+                                         float (&back)[NT], bool some, int ve, float vl) {
+#pragma clang fp contract(off)
+        uint64_t large = 0;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const float mn = fmaxf(m[u], floorf(top[u])), keep = m[u] - mn;
+            int en = e[u];
+            bool down = false;
+            if (some && mn > kNothing) {
+                if (en == kNoUnit) en = unit != kNoUnit && ve <= unit && ve > unit + kLeast ? unit : ve;
+                // a page of no weight in this row does not move it far
+                else if (ve > en) en = ve - en <= 40 || (top[u] - mn) + (vl + (float)(ve - en)) > kTop + kSlack ? ve : en;
+                else down = ve <= en + kLeast;
+            }
+            if (__ballot(down)) {
+                float big = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16 * NP; ++i) big = fmaxf(big, fabsf(o[u][i >> 2][i & 3]));
+                big = over_groups_max(big);
+                const int room = kRoom - __builtin_amdgcn_frexp_expf(big) - (int)fmaxf(keep, -500.f);
+                if (down) en = big > 0.f ? max(ve, en - min(max(room, 0), 126)) : ve;
+            }
+            const float f = __builtin_amdgcn_exp2f(fminf(keep + (float)(e[u] - en), 126.f));
+            sum[u] *= __builtin_amdgcn_exp2f(keep);
+            m[u] = mn;
+            e[u] = en;
+#pragma unroll
+            for (int d = 0; d < 4 * NP; ++d) o[u][d] *= f;
+            const float ratio = some ? fmaxf(vl + (float)(ve - en), kTop + (float)kLeast) : vl;
+            base[u] = mn - ratio;
+            back[u] = __builtin_amdgcn_exp2f(-ratio);
+            // Scores of 2^20 and more are compared and subtracted as rounded products: the unrounded product
+            // would be off the maximum by more than a weight can take
+            const bool rounded = mn > kNothing && fabsf(mn) >= kLarge;
+            large |= __ballot(rounded);
+            if (rounded) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[u][i >> 2][i & 3] = w[u][i >> 2][i & 3] * fac[u] - mn;
+                fac[u] = 1.f;
+                base[u] = -ratio;
+            }
+        }
+        // every wave has a row that is there
+        int one = kNoUnit;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) one = m[u] > kNothing ? e[u] : one;
+        const uint64_t seen = __ballot(one != kNoUnit);
+        one = __builtin_amdgcn_readlane(one, seen ? __builtin_ctzll(seen) : 0);
+        bool differ = false;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) differ = differ || (m[u] > kNothing && e[u] != one);
+        unit = __ballot(differ) || large ? kNoUnit : one;
+    }
+
+    // The weights of a page as operands.
+    __device__ __forceinline__ void weights(const f32x4_t (&w)[NT][4], const float (&fac)[NT], const float (&base)[NT],
+                                            uint4 (&pw)[NT][2]) const {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            uint32_t x[4][2];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    e[t][r] = pack_f16(__builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r], fac[u], -base)),
-                                       __builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r + 1], fac[u], -base)));
-            pw[u][0] = make_uint4(e[0][0], e[0][1], e[1][0], e[1][1]);
-            pw[u][1] = make_uint4(e[2][0], e[2][1], e[3][0], e[3][1]);
+                    x[t][r] = pack_f16(__builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r], fac[u], -base[u])),
+                                       __builtin_amdgcn_exp2f(fmaf(w[u][t][2 * r + 1], fac[u], -base[u])));
+            pw[u][0] = make_uint4(x[0][0], x[0][1], x[1][0], x[1][1]);
+            pw[u][1] = make_uint4(x[2][0], x[2][1], x[3][0], x[3][1]);
         }
     }
+
     // The values of a page: vals(d, x, y) gives the two operands of channels
-    // 16 d; the weights hold `ratio`.
+    // 16 d.
     template <typename V>
-    __device__ __forceinline__ void values(const uint4 (&pw)[NT][2], float ratio, V vals) {
-        weigh(pw, ratio);
+    __device__ __forceinline__ void values(const uint4 (&pw)[NT][2], const float (&back)[NT], V vals) {
+        weigh(pw, back);
 #pragma unroll
         for (int d = 0; d < 4 * NP; ++d) {
             uint4 v0, v1;
@@ -564,7 +648,8 @@ struct Rows {
         }
     }
     // first: the first kFew operands, read before
-    __device__ __forceinline__ void values_lds(const uint4 (&pw)[NT][2], float ratio, const uint4* v, const uint4 (&first)[kFew]) {
+    __device__ __forceinline__ void values_lds(const uint4 (&pw)[NT][2], const float (&back)[NT], const uint4* v,
+                                               const uint4 (&first)[kFew]) {
         uint4 f[2][kFew];
 #pragma unroll
         for (int i = 0; i < kFew; ++i) f[0][i] = first[i];
@@ -572,7 +657,7 @@ struct Rows {
         for (int j = 0; j < 4; ++j) {                   // channels 16 NP j ..
             if (j < 3) fetch(f[(j + 1) & 1], v + (j + 1) * kFew * 64);
             __builtin_amdgcn_sched_barrier(0);
-            if (j == 0) weigh(pw, ratio);
+            if (j == 0) weigh(pw, back);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -584,36 +669,30 @@ struct Rows {
         }
     }
     // The weights' own sums.
-    __device__ __forceinline__ void weigh(const uint4 (&pw)[NT][2], float ratio) {
-        const float back = __builtin_amdgcn_rcpf(ratio);
+    __device__ __forceinline__ void weigh(const uint4 (&pw)[NT][2], const float (&back)[NT]) {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             f32x4_t c = {0.f, 0.f, 0.f, 0.f};
             c = mfma16(ones(), pw[u][0], c);
             c = mfma16(ones(), pw[u][1], c);
-            sum[u] = fmaf(c[0], back, sum[u]);
+            sum[u] = fmaf(c[0], back[u], sum[u]);
         }
     }
-    // vs / s as the weights take it (a page of zeros takes none of it).
-    __device__ __forceinline__ float ratio_of(float vs) const {
-        return vs > 0.f ? fmaxf(vs * __builtin_amdgcn_rcpf(s), kLeast) : 1.f;
-    }
-    static __device__ __forceinline__ float shift_of(float ratio) { return kTop + __builtin_amdgcn_logf(ratio); }
-
-    // The results in their own units, behind the last page.
+    // Behind the last page: o as weights of 1 make it.  (As a step of its own: without one the
+    // compiler copies o in every turn of the loop, 12 % of a prompt's time.)
     __device__ __forceinline__ void finish() {
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
-            for (int d = 0; d < 4 * NP; ++d)
-                o[u][d] *= s;
+            for (int d = 0; d < 4 * NP; ++d) o[u][d] *= __builtin_amdgcn_exp2f(-kTop);
     }
+    __device__ __forceinline__ Part part(int u) const { return Part{m[u], sum[u], (float)e[u]}; }
 };
 
 // Pages of one segment for one wave.  A page that is not there (the table
 // names none, or the segment has none) is a buffer of no bytes: its loads
 // return zeros and touch no memory, and the number of loads in flight is the
-// same in every turn of a loop.  Lane i keeps what the table and the scales
+// same in every turn of a loop.  So are the values of a page whose scale is 0.  Lane i keeps what the table and the scales
 // say of page base + i: a turn of a loop reads a lane and waits for no memory
 // (scalar loads would hold up every wait for LDS, which counts them too).
 template <int NP>
@@ -621,8 +700,8 @@ struct Pages {
     static constexpr int kBytes = kKvPage * 64 * NP;
     const Attend& A;
     const int32_t* table;
-    int head, upto, base, id;
-    float ks, vs;
+    int head, upto, base, id, ve;
+    float ks, vl;          // K's scale; V's scale 2^(ve + vl - kTop), -1 <= vl - kTop < 0 (0: ve kNoUnit)
     __device__ __forceinline__ Pages(const Attend& a, const Place& P, const Tile& T, int from, int up, int l)
         : A(a), table(a.b.block_table + (size_t)P.s * a.b.max_pages + T.pg0), head(P.vh / (a.VH / a.c.n_kv)), upto(up) {
         look(from, l);
@@ -634,22 +713,26 @@ struct Pages {
         // a page that is not there has scales of 0, whatever those at where(-1), another page's, hold
         const float k0 = A.c.k_scale[where(id)], v0 = A.c.v_scale[where(id)];
         ks = id >= 0 ? k0 : 0.f;
-        vs = id >= 0 ? v0 : 0.f;
+        const bool some = id >= 0 && v0 > 0.f;
+        ve = some ? __builtin_amdgcn_frexp_expf(v0) : kNoUnit;
+        vl = kTop + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(some ? v0 : 1.f));
     }
     // pages p .. p + 2 are looked at next
     __device__ __forceinline__ void follow(int p, int l) {
         if (p + 2 >= base + 64) look(p, l);
     }
     __device__ __forceinline__ int at(int p) const { return __builtin_amdgcn_readlane(id, p - base); }
-    __device__ __forceinline__ float k_scale(int p) const {
-        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), p - base));
+    __device__ __forceinline__ float of_page(float x, int p) const {
+        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), p - base));
     }
-    __device__ __forceinline__ float v_scale(int p) const {
-        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), p - base));
-    }
+    __device__ __forceinline__ float k_scale(int p) const { return of_page(ks, p); }
+    __device__ __forceinline__ int v_exp(int p) const { return __builtin_amdgcn_readlane(ve, p - base); }
+    __device__ __forceinline__ float v_log(int p) const { return of_page(vl, p); }
     __device__ __forceinline__ size_t where(int page) const { return (size_t)max(page, 0) * A.c.n_kv + head; }
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t codes(const void* at, int page) const {
-        return make_rsrc(static_cast<const uint8_t*>(at) + where(page) * kBytes, page >= 0 ? kBytes : 0);
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t keys(int p) const { return codes(A.c.k, at(p), at(p) >= 0); }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t values(int p) const { return codes(A.c.v, at(p), v_exp(p) != kNoUnit); }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t codes(const void* from, int page, bool there) const {
+        return make_rsrc(static_cast<const uint8_t*>(from) + where(page) * kBytes, there ? kBytes : 0);
     }
 };
 
@@ -664,36 +747,33 @@ __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& 
     const int ctx = T.R.first + T.R.n;                             // slots from here on hold no token
     w.load(A, seg_of(P, T), T.R.first + T.i0, r0, l);
     uint4 kf[4 * NP], vf[4 * NP];
-    auto load = [&](uint4 (&f)[4 * NP], const void* base, int page) {
-        const __amdgpu_buffer_rsrc_t r = pages.codes(base, page);
+    auto load = [&](uint4 (&f)[4 * NP], __amdgpu_buffer_rsrc_t r) {
 #pragma unroll
         for (int d = 0; d < 4 * NP; ++d) f[d] = buf_load16(r, l * 16, d * 1024);
     };
-    load(kf, A.c.k, pages.at(from));
+    load(kf, pages.keys(from));
     __builtin_amdgcn_sched_barrier(0);                              // q and the first keys are on their way
     w.begin(A);
     for (int p = from; p < upto; ++p) {
         pages.follow(p, l);
         const int page = pages.at(p);
-        load(vf, A.c.v, page);
+        load(vf, pages.values(p));
         __builtin_amdgcn_sched_barrier(0);                          // before the first product
         const int base_key = (T.pg0 + p) * kKvPage;
         const bool clean = KIND == PROX_KV_FP8 && base_key + kKvPage > ctx;
         f32x4_t sc[NT][4];
-        float fac[NT];
+        float fac[NT], less[NT], back[NT];
         w.scores(sc, [&](int a, int t, uint4& x, uint4& y) {
             const uint4 c = kf[a * 4 + t];
             x = codes_f16<KIND>(c.x, c.y);
             y = codes_f16<KIND>(c.z, c.w);
         });
-        load(kf, A.c.k, pages.at(p + 1));
+        load(kf, pages.keys(p + 1));
         __builtin_amdgcn_sched_barrier(0);
-        const float vs = pages.v_scale(p);
-        w.limits(sc, fac, base_key, page < 0, pages.k_scale(p), vs, l);
-        const float ratio = w.ratio_of(vs);
+        w.limits(sc, fac, less, back, base_key, page < 0, pages.k_scale(p), pages.v_exp(p), pages.v_log(p), l);
         uint4 pw[NT][2];
-        w.weights(sc, fac, w.shift_of(ratio), pw);
-        w.values(pw, ratio, [&](int d, uint4& x, uint4& y) {
+        w.weights(sc, fac, less, pw);
+        w.values(pw, back, [&](int d, uint4& x, uint4& y) {
             uint4 c = vf[d];
             if (clean) c = make_uint4(no_nan_fp8(c.x), no_nan_fp8(c.y), no_nan_fp8(c.z), no_nan_fp8(c.w));
             x = values_f16<KIND>(c.x, c.y);
@@ -730,8 +810,7 @@ __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds,
     uint4* const kl = lds + l;
     uint4* const vl = lds + 2 * kSize + l;
     uint4 kc[kOwn], vc[kOwn];
-    auto load = [&](uint4 (&c)[kOwn], const void* base, int page) {
-        const __amdgpu_buffer_rsrc_t r = pages.codes(base, page);
+    auto load = [&](uint4 (&c)[kOwn], __amdgpu_buffer_rsrc_t r) {
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
             const int ch = wv + j * kWaves;                         // past the last chunk: past the buffer, zeros
@@ -759,36 +838,35 @@ __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds,
         }
     };
     auto unclean = [&](int p) { return KIND == PROX_KV_FP8 && (T.pg0 + p + 1) * kKvPage > ctx; };
-    load(kc, A.c.k, pages.at(from));
-    load(vc, A.c.v, pages.at(from));
+    load(kc, pages.keys(from));
+    load(vc, pages.values(from));
     w.begin(A);
     lds_barrier();                                                  // the last segment's pages are done with
     fill_keys(kl);
-    load(kc, A.c.k, pages.at(from + 1));
+    load(kc, pages.keys(from + 1));
     fill_values(vl, unclean(from));
-    load(vc, A.c.v, pages.at(from + 1));
+    load(vc, pages.values(from + 1));
     lds_barrier();
     for (int p = from; p < upto; ++p) {
         const int buf = (p - from) & 1;
         pages.follow(p, l);
         if (busy) {
             f32x4_t sc[NT][4];
-            float fac[NT];
+            float fac[NT], less[NT], back[NT];
             w.scores_lds(sc, kl + buf * kSize);
             uint4 first[Rows<KIND, NP, NT>::kFew];
             w.fetch(first, vl + buf * kSize);
-            const float vs = pages.v_scale(p);
-            w.limits(sc, fac, (T.pg0 + p) * kKvPage, pages.at(p) < 0, pages.k_scale(p), vs, l);
-            const float ratio = w.ratio_of(vs);
+            w.limits(sc, fac, less, back, (T.pg0 + p) * kKvPage, pages.at(p) < 0, pages.k_scale(p), pages.v_exp(p),
+                     pages.v_log(p), l);
             uint4 pw[NT][2];
-            w.weights(sc, fac, w.shift_of(ratio), pw);
-            w.values_lds(pw, ratio, vl + buf * kSize, first);
+            w.weights(sc, fac, less, pw);
+            w.values_lds(pw, back, vl + buf * kSize, first);
         }
         // the other half was used a turn ago
         fill_values(vl + (buf ^ 1) * kSize, unclean(p + 1));
-        load(vc, A.c.v, pages.at(p + 2));
+        load(vc, pages.values(p + 2));
         fill_keys(kl + (buf ^ 1) * kSize);
-        load(kc, A.c.k, pages.at(p + 2));
+        load(kc, pages.keys(p + 2));
         lds_barrier();
     }
     w.finish();
@@ -807,7 +885,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
     __shared__ Seg seg_s[16];                     // segment of each wave's two slots, begin -1: none
     __shared__ Seg cut_s[2];                      // the segments that reach over the piece's begin and over its end
     __shared__ int done_s[2];
-    constexpr int RW = 64 * NP + 4;               // floats of a row in a slot: result, maximum, sum
+    constexpr int RW = 64 * NP + 4;               // floats of a row in a slot: result, maximum, sum, unit
     constexpr int LPR = 16 * NP;                  // lanes of a row, four channels each
     const int l = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), n = l & 15, g = l >> 4;
     const int WV = blockDim.x >> 6;
@@ -865,7 +943,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                         if (to)
 #pragma unroll
                             for (int d = 0; d < 4 * NP; ++d)
-                                if (16 * d + 4 * g < hd) *reinterpret_cast<uint2*>(to + 16 * d + 4 * g) = bf16x4(w.o[u][d] * inv);
+                                if (16 * d + 4 * g < hd) *reinterpret_cast<uint2*>(to + 16 * d + 4 * g) = bf16x4(result(w.o[u][d], inv, (float)w.e[u]));
                     } else if (!ROWS) {
                         const int slot = 2 * wv + (from == 0 ? 1 : 0);
                         if (l == 0) seg_s[slot] = seg_of(P, T);
@@ -873,7 +951,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                             float* to = lds + (slot * A.slot_rows + n) * RW;
 #pragma unroll
                             for (int d = 0; d < 4 * NP; ++d) *reinterpret_cast<f32x4_t*>(to + 16 * d + 4 * g) = w.o[u][d];
-                            if (g == 0) *reinterpret_cast<float2*>(to + 64 * NP) = make_float2(w.m[u], w.sum[u]);
+                            if (g == 0) *reinterpret_cast<float4*>(to + 64 * NP) = packed(w.part(u));
                         }
                     } else if (w.live[u]) {
                         const uint32_t at = part_at(blockIdx.x, from == 0, r);
@@ -881,10 +959,9 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                         for (int d = 0; d < 4 * NP; ++d)
                             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, w.o[u][d]), rp,
                                                                    (int)(at + 4 * (16 * d + 4 * g)), 0, kCoherent);
-                        if (g == 0) {
-                            const u32x2_t ms = {__float_as_uint(w.m[u]), __float_as_uint(w.sum[u])};
-                            __builtin_amdgcn_raw_buffer_store_b64(ms, rp, (int)(at + 256 * NP), 0, kCoherent);
-                        }
+                        if (g == 0)
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, packed(w.part(u))), rp,
+                                                                   (int)(at + 256 * NP), 0, kCoherent);
                     }
                 }
             }
@@ -913,32 +990,31 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
             const bool whole = S.begin >= b0 && S.begin + S.pages + A.seg_cost <= b1;
             for (int e = threadIdx.x; e < A.slot_rows * LPR; e += blockDim.x) {
                 const int r = e / LPR, c4 = 4 * (e % LPR);
-                float m = -INFINITY, sum = 0.f;
+                Part a = no_part();
                 f32x4_t o = {0.f, 0.f, 0.f, 0.f};
                 for (int k0 = i; k0 < j; k0 += 4) {
-                    float2 ms[4];
+                    float4 ms[4];
                     f32x4_t v[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const int k = (same >> (k0 + u)) & 1 ? k0 + u : i;
                         const float* from = lds + (k * A.slot_rows + r) * RW;
-                        ms[u] = *reinterpret_cast<const float2*>(from + 64 * NP);
+                        ms[u] = *reinterpret_cast<const float4*>(from + 64 * NP);
                         v[u] = *reinterpret_cast<const f32x4_t*>(from + c4);
                     }
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        if ((same >> (k0 + u)) & 1) join(m, sum, o, ms[u].x, ms[u].y, v[u]);
+                        if ((same >> (k0 + u)) & 1) join(a, o, unpacked(ms[u]), v[u]);
                 }
                 if (whole) {
                     uint16_t* to = out_row(A, S, r);
-                    if (to && c4 < hd) *reinterpret_cast<uint2*>(to + c4) = bf16x4(o * inverse(sum));
+                    if (to && c4 < hd) *reinterpret_cast<uint2*>(to + c4) = bf16x4(result(o, inverse(a.sum), a.e));
                 } else {
                     const uint32_t at = part_at(blockIdx.x, S.begin >= b0, r);
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), rp, (int)(at + 4 * c4), 0, kCoherent);
-                    if (c4 == 0) {
-                        const u32x2_t ms = {__float_as_uint(m), __float_as_uint(sum)};
-                        __builtin_amdgcn_raw_buffer_store_b64(ms, rp, (int)(at + 256 * NP), 0, kCoherent);
-                    }
+                    if (c4 == 0)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, packed(a)), rp,
+                                                               (int)(at + 256 * NP), 0, kCoherent);
                 }
             }
             if (!whole) {
@@ -972,29 +1048,31 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
         blocks_of(A, piece, S.begin, S.pages, w0, w1);
         const int parts = w1 - w0 + 1;
         const int lanes = A.slot_rows * LPR, bd = blockDim.x;           // (row, four channels)
-        auto load = [&](int p, int e, u32x4_t& v, u32x2_t& ms) {
+        auto load = [&](int p, int e, u32x4_t& v, u32x4_t& ms) {
             const uint32_t at = part_at(w0 + p, p == 0, e / LPR);
             v = __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 16 * (e % LPR)), 0, kCoherent);
-            ms = __builtin_amdgcn_raw_buffer_load_b64(rp, (int)(at + 256 * NP), 0, kCoherent);
+            ms = __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 256 * NP), 0, kCoherent);
         };
-        auto store = [&](int e, f32x4_t o, float sum) {
+        auto joined = [&](Part& a, f32x4_t& o, u32x4_t ms, u32x4_t v) {
+            join(a, o, unpacked(__builtin_bit_cast(float4, ms)), __builtin_bit_cast(f32x4_t, v));
+        };
+        auto store = [&](int e, f32x4_t o, const Part& a) {
             uint16_t* to = out_row(A, S, e / LPR);
-            if (to && 4 * (e % LPR) < hd) *reinterpret_cast<uint2*>(to + 4 * (e % LPR)) = bf16x4(o * inverse(sum));
+            if (to && 4 * (e % LPR) < hd)
+                *reinterpret_cast<uint2*>(to + 4 * (e % LPR)) = bf16x4(result(o, inverse(a.sum), a.e));
         };
         if (2 * lanes > bd) {
             // many rows and few parts: a thread joins four (row, four channels) at once
             for (int e0 = threadIdx.x; e0 < lanes; e0 += 4 * bd) {
-                float m[4], sum[4];
+                Part a[4];
                 f32x4_t o[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    m[u] = -INFINITY;
-                    sum[u] = 0.f;
+                    a[u] = no_part();
                     o[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
                 }
                 for (int p0 = 0; p0 < parts; p0 += 2) {
-                    u32x4_t v[2][4];
-                    u32x2_t ms[2][4];
+                    u32x4_t v[2][4], ms[2][4];
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -1003,46 +1081,41 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                     for (int q = 0; q < 2; ++q)
                         if (p0 + q < parts)
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                join(m[u], sum[u], o[u], __uint_as_float(ms[q][u].x), __uint_as_float(ms[q][u].y),
-                                     __builtin_bit_cast(f32x4_t, v[q][u]));
+                            for (int u = 0; u < 4; ++u) joined(a[u], o[u], ms[q][u], v[q][u]);
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    if (e0 + u * bd < lanes) store(e0 + u * bd, o[u], sum[u]);
+                    if (e0 + u * bd < lanes) store(e0 + u * bd, o[u], a[u]);
             }
             continue;
         }
         // few rows and many parts: groups of threads take parts in order, eight at once, then the groups are joined
         const int PG = bd / lanes, pg = (int)threadIdx.x / lanes, e = (int)threadIdx.x % lanes;
-        float m = -INFINITY, sum = 0.f;
+        Part a = no_part();
         f32x4_t o = {0.f, 0.f, 0.f, 0.f};
         if (pg < PG) {
             const int pe = (pg + 1) * parts / PG;
             for (int p0 = pg * parts / PG; p0 < pe; p0 += 8) {
-                u32x4_t v[8];
-                u32x2_t ms[8];
+                u32x4_t v[8], ms[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) load(min(p0 + u, pe - 1), e, v[u], ms[u]);
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    if (p0 + u < pe)
-                        join(m, sum, o, __uint_as_float(ms[u].x), __uint_as_float(ms[u].y), __builtin_bit_cast(f32x4_t, v[u]));
+                    if (p0 + u < pe) joined(a, o, ms[u], v[u]);
             }
         }
         __syncthreads();                                                // LDS is free
         if (pg < PG) {
             *reinterpret_cast<f32x4_t*>(lds + threadIdx.x * 8) = o;
-            *reinterpret_cast<float2*>(lds + threadIdx.x * 8 + 4) = make_float2(m, sum);
+            *reinterpret_cast<float4*>(lds + threadIdx.x * 8 + 4) = packed(a);
         }
         __syncthreads();
         if (pg == 0) {
             for (int u = 1; u < PG; ++u) {
                 const float* from = lds + (u * lanes + e) * 8;
-                const float2 ms = *reinterpret_cast<const float2*>(from + 4);
-                join(m, sum, o, ms.x, ms.y, *reinterpret_cast<const f32x4_t*>(from));
+                join(a, o, unpacked(*reinterpret_cast<const float4*>(from + 4)), *reinterpret_cast<const f32x4_t*>(from));
             }
-            store(e, o, sum);
+            store(e, o, a);
         }
     }
 }

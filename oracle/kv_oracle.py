@@ -177,7 +177,12 @@ def attention(cache: Cache, table, ctx, q_start, max_q, q, scale, window=0, n_ou
     each, and takes part in at most one rescaling and one join of parts (3
     roundings), all of sums up to sum_j w_j |v_j|: 20 a page, and 20 for the rest.
     The bf16 result is rounded by at most 2^-8 |o|.  A weight under 2^-126 of the
-    row's largest is no normal fp32 number and may be taken as 0."""
+    row's largest is no normal fp32 number and may be taken as 0.  All channels
+    of a row share a unit: where its largest sum is 2^99 units and more (weights
+    held 2^10 large at most, so 2^89 over sum_j p_j <= n in the mean), a page of
+    values too small for that unit counts as a quarter of it at most, codes up
+    to 448: an error of 2^7 against n^-1 2^89, n 2^-82 of the largest of
+    sum_j w_j |v_j| over the channels."""
     T, H, hd = q.shape
     out = np.full((T, H, hd), np.nan)
     tol = np.zeros((T, H, hd))
@@ -217,5 +222,6 @@ def attention(cache: Cache, table, ctx, q_start, max_q, q, scale, window=0, n_ou
             sums = 20 * (pages + 1) * r24 * (w @ np.abs(v))
             out[row, h] = o
             tol[row, h] = (2.0 ** -8 * np.abs(o) + (w * (1.02 * (u + eta))) @ np.abs(v - o) + sums
-                           + see.size * 2.0 ** -33 * np.abs(v - o).max(0) + 1e-37)
+                           + see.size * 2.0 ** -33 * np.abs(v - o).max(0) + 1e-37
+                           + see.size * 2.0 ** -82 * (w @ np.abs(v)).max())
     return out, tol

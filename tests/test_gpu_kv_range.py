@@ -1,10 +1,14 @@
 """Attention over the paged 8-bit cache at the ends of its range: pages that the
-table does not name, long runs of pages."""
+table does not name, long runs of pages, value scales of any size, large scores.
+
+Bounds are those of ``kv_oracle.attention`` or stated with each test; a bfloat16
+rounding is off by at most 2^-8 of the value."""
 
 import numpy as np
 import pytest
 import torch
 
+from oracle import kv_oracle as KO
 from test_gpu_kv import World, f64, settle
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +85,137 @@ def test_sums_stay_exact_over_long_runs_of_pages(kind):
         got = f64(P.kv_attention(torch.zeros(rows, 1, hd, dtype=torch.bfloat16, device="cuda"), cache, b))[:, 0]
         err = np.abs(got - want[T - rows:])
         assert np.all(err <= (2.0 ** -8 + 2.0 ** -22) * np.abs(want[T - rows:])), (rows, float(err.max()))
+
+
+# ---- value scales of any size ------------------------------------------------------
+
+def short_scales(w, shape):
+    """Scales 2^-5 (1 + m / 8): exact when moved down to 2^-149 or up."""
+    return (2.0 ** -5 * (1 + w.rng.integers(0, 8, shape) / 8)).astype(np.float32)
+
+
+LENS = [3000, 700, 130, 1]
+NEW = ([1, 1, 1, 1], [3, 1, 2, 1], [200, 90, 60, 1])
+
+
+@pytest.mark.parametrize("kind,H,KV,hd", [("int8", 4, 1, 64), ("fp8", 4, 2, 128), ("int8", 2, 1, 256)])
+def test_attention_scales_with_the_value_scales(kind, H, KV, hd):
+    # every value times 2^k: fp32 results are the same times 2^k, as far as they
+    # stay normal numbers, so their bf16 roundings are
+    w = World(kind, H, KV, hd, LENS, seed=hd + 3)
+    settle(w, LENS)
+    w.o.vs[:] = base = short_scales(w, w.o.vs.shape)
+    both(w)
+    for new in NEW:
+        b, start = w.batch(new, advance=False)
+        q = w.rows(b.n_tokens, H, 1.5)
+        ref = f64(w.attend(b, start, q=q)[0])
+        for k in (-136, -128, -120, -100, -60, 60, 100, 118):
+            w.c.v_scale.copy_(torch.from_numpy(np.ldexp(base, k)))
+            got, want = f64(w.P.kv_attention(q, w.c, b)), np.ldexp(ref, k)
+            normal = np.abs(want) >= 2.0 ** -125
+            assert np.array_equal(got[normal], want[normal]), (new, k)
+            # below: the rounding of ref, and one to a multiple of 2^-133
+            assert np.all(np.abs(got - want)[~normal] <= 2.0 ** -8 * np.abs(want[~normal]) + 2.0 ** -133), (new, k)
+        both(w)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_attention_over_appended_values_of_any_size(kind):
+    # what the append stores of values up to the largest bfloat16 and down to subnormal ones
+    for v_size, k_size in ((1e36, 2.0 ** -118), (1e38, 1.0), (3e-39, 1.0), (1e-36, 1e36)):
+        w = World(kind, 2, 1, 64, [500, 64], seed=59)
+        b, start = w.batch([500, 64])
+        k, v = w.rows(564, 1), w.rows(564, 1).clamp(-3, 3) * v_size
+        k = k * k_size
+        w.P.kv_append(w.c, b, k, v)
+        KO.append(w.o, w.table, w.ctx, start, b.max_q, f64(k), f64(v))
+        w.same_cache()
+        for new in ([1, 1], [300, 64]):
+            b, start = w.batch(new, advance=False)
+            q = w.rows(b.n_tokens, 2, 1.5 / max(k_size, 1.0))
+            out, _ = w.attend(b, start, q=q)
+            # results near the subnormal numbers, where the bound above says little
+            want, tol = KO.attention(w.o, w.table, w.ctx, start, b.max_q, f64(q), 8.0 ** -1)
+            assert np.all(np.abs(f64(out) - want) <= tol - 1e-37 + 2.0 ** -133), (v_size, new)
+
+
+PATTERNS = {
+    # exponents of the pages' value scales, repeated along the sequence
+    "two steps down": [0] * 20 + [-93, -115] * 3,
+    "three steps down and up": [0, -70, -110, -140, 60, 0, -140, 118],
+    "alternating": [0, -3, 2, -9, 0, -14],
+    "rising": list(range(-120, 118, 7)),
+    "falling": list(range(118, -120, -7)),
+    "zeros between": [0, None, -40, None, None, 40],
+}
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("pattern", PATTERNS)
+def test_attention_over_pages_of_unlike_value_scales(kind, pattern):
+    w = World(kind, 4, 1, 64, LENS, seed=61)
+    settle(w, LENS)
+    e = PATTERNS[pattern]
+    for s in range(len(LENS)):
+        for p, page in enumerate(w.table[s]):
+            if page >= 0:
+                x = e[p % len(e)]
+                w.o.vs[page] = 0 if x is None else np.ldexp(short_scales(w, 1), x)
+    both(w)
+    for new in NEW:
+        b, start = w.batch(new, advance=False)
+        w.attend(b, start)
+        w.attend(b, start, window=150)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_large_values_of_no_weight_leave_a_row_alone(kind):
+    # pages whose keys score 1000s below the others': whatever their values are, a
+    # row is what it is without them (weights under 2^-1000)
+    w = World(kind, 4, 1, 64, [3000, 400], seed=67)
+    b, start = w.batch([3000, 400])
+    k, v = w.rows(3400, 1), w.rows(3400, 1)
+    far = {0: (0, 5, 6, 45), 1: (2,)}
+    for s, pages in far.items():
+        for p in pages:
+            k[start[s] + 64 * p:start[s] + 64 * (p + 1), 0, 0] = -4000.0
+    w.P.kv_append(w.c, b, k, v)
+    KO.append(w.o, w.table, w.ctx, start, b.max_q, f64(k), f64(v))
+    w.same_cache()
+    table = w.table.copy()
+    for new in ([1, 1], [3, 2], [100, 90]):
+        b, start = w.batch(new, advance=False)
+        q = w.rows(b.n_tokens, 4)
+        q[..., 0] = 8.0
+        for s, pages in far.items():
+            w.table[s, list(pages)] = -1
+        want, tol = KO.attention(w.o, w.table, w.ctx, start, b.max_q, f64(q), 64 ** -0.5)
+        w.table[:] = table
+        for size in (1.0, 1e30, 1e-30, 0.0):
+            vs = w.o.vs.copy()
+            for s, pages in far.items():
+                vs[table[s, list(pages)]] *= np.float32(size)
+            w.c.v_scale.copy_(torch.from_numpy(vs))
+            assert np.all(np.abs(f64(w.P.kv_attention(q, w.c, b)) - want) <= tol), (new, size)
+        both(w)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_scores_past_fp32_pick_the_largest(kind):
+    # scores of +-1e50: the row is the value of its largest key
+    w = World(kind, 2, 1, 64, [60], seed=71)
+    b, start = w.batch([60])
+    k, v = w.rows(60, 1), w.rows(60, 1)
+    k[:, 0, 0] = torch.arange(-30, 30, device="cuda") * 4.0
+    k *= 1e30
+    w.P.kv_append(w.c, b, k, v)
+    KO.append(w.o, w.table, w.ctx, start, 60, f64(k), f64(v))
+    w.same_cache()
+    for n in (1, 60):
+        b, start = w.batch([n], advance=False)
+        q = torch.zeros(n, 2, 64, dtype=torch.bfloat16, device="cuda")
+        q[..., 0] = 1e20
+        out, _ = w.attend(b, start, q=q, scale=1.0)
+        q[..., 0] = 3e38
+        assert torch.equal(w.P.kv_attention(q, w.c, b, scale=4.0), out)
