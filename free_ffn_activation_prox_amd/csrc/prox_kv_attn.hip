@@ -20,8 +20,8 @@
 //          [1, 2): exact in fp16 down to 2^-17 of the row's largest, and off
 //          by at most 2^-25 of that below.
 //   p      the softmax weights are rounded to fp16 (half a step: 2^-11) and
-//          held up to 2^14, so that fp16's normal numbers reach down to 2^-22
-//          of a row's largest.  The sum that the result is divided by is that
+//          held up to 2^15.9, so that fp16's normal numbers reach down to 2^-22
+//          of a row's largest (2^-24 but for sv, see there).  The sum that the result is divided by is that
 //          of the rounded weights (a product with a row of constants), which
 //          keeps the result a weighted mean of the stored values.
 //   sv     goes into the weights: p sv / 2^e with 2^e the unit of a row's sums,
@@ -29,12 +29,14 @@
 //          unit's accumulators from page to page; the sum of the weights takes
 //          it out again.  e moves up where p sv / 2^e leaves the weights' range,
 //          so a page that has no weight in a row moves nothing there, and down
-//          where sv / 2^e falls below 2^-12, as far as the row's sums allow:
-//          they stay below 2^100.  A page for which they do not allow it counts
-//          as 2^-12 of the unit, less than 2^-60 of the row's largest sum.
+//          where sv / 2^e falls below a quarter (smaller ones would cost the
+//          small weights, and the sum with them, their bits), as far as the
+//          row's sums allow: they stay below 2^100.  A page for which they do
+//          not allow it counts as a quarter of the unit, less than 2^-50 of the
+//          row's largest sum.
 //          m and e are whole numbers: moving them rounds nothing, and value
 //          scales of any fp32 size give the same result in their unit.
-// m and e move only when a score exceeds m by more than 2^6 or an sv leaves its
+// m and e move only when a score exceeds m by more than 2^5.9 or an sv leaves its
 // range, so most pages rescale nothing.
 //
 // A wave takes tiles of 16 rows that share a key head and walks their pages.
@@ -323,9 +325,10 @@ __device__ __forceinline__ uint2 bf16x4(f32x4_t v) {
 // 1 / the softmax sum: 0 for a row that has seen nothing; a NaN sum stays.
 __device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); }
 
-// A weight's rows hold up to 2^(kTop + kSlack): see "Arithmetic" above.
-constexpr float kTop = 8.f, kSlack = 6.f;
-constexpr int kLeast = -12;            // exponent of the least sv / 2^e that goes into the weights
+// Weights hold up to 2^(kTop + kSlack), 61000 of fp16's 65504: see "Arithmetic" above.  A slack of 5 moves m
+// more often: a 4096-token prompt takes 203 us, with 5.9 198.
+constexpr float kTop = 10.f, kSlack = 5.9f;
+constexpr int kLeast = -2;             // exponent of the least sv / 2^e that goes into the weights
 constexpr int kRoom = 100;             // exponent that a row's sums stay below when e moves down
 constexpr int kNoUnit = -1000;         // e of a row that has seen no value but zeros
 constexpr float kNothing = -0x1p126f;  // m of a row that has seen nothing; scores are above

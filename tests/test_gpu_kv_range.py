@@ -1,5 +1,6 @@
 """Attention over the paged 8-bit cache at the ends of its range: pages that the
-table does not name, long runs of pages, value scales of any size, large scores.
+table does not name, long runs of pages, value scales of any size, large scores,
+small weights beside outliers.
 
 Bounds are those of ``kv_oracle.attention`` or stated with each test; a bfloat16
 rounding is off by at most 2^-8 of the value."""
@@ -219,3 +220,29 @@ def test_scores_past_fp32_pick_the_largest(kind):
         out, _ = w.attend(b, start, q=q, scale=1.0)
         q[..., 0] = 3e38
         assert torch.equal(w.P.kv_attention(q, w.c, b, scale=4.0), out)
+
+
+# ---- small weights beside an outlier -------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("outlier", [30.0, 3000.0, 1e6])
+def test_many_tiny_weights_beside_an_outlier(kind, outlier):
+    # key 0 has weight 1 and value 0, 4096 others 2^-24 each; one channel of one
+    # value in the first page is large.  The other channels' sums, some 2^-12, do
+    # not feel it beyond what the first page's codes have lost.
+    n, hd = 4097, 64
+    w = World(kind, 2, 1, hd, [n], seed=73)
+    k, v = torch.zeros(n, 1, hd, dtype=torch.bfloat16), w.rows(n, 1).cpu().abs() + 1
+    k[0, 0, 0] = 1.0
+    v[0] = 0
+    v[1, 0, 5] = outlier
+    b, start = w.batch([n])
+    w.P.kv_append(w.c, b, k.cuda(), v.cuda())
+    KO.append(w.o, w.table, w.ctx, start, n, f64(k), f64(v))
+    w.same_cache()
+    q = torch.zeros(n, 2, hd, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    for new in (1, 100):
+        b, start = w.batch([new], advance=False)
+        out, _ = w.attend(b, start, q=q[:new].clone(), scale=24.0 * float(np.log(2.0)))
+        assert float(out[-1].float().abs().min()) > 2e-4
