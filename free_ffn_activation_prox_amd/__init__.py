@@ -592,7 +592,7 @@ def alloc_kv_workspace(cache: KVCache, batch: KVBatch, n_heads: int):
     with torch.cuda.device(cache.device):
         n = kv_workspace_bytes(cache, batch, n_heads)
     if n == 0:
-        raise ValueError("invalid cache, batch or n_heads for a workspace")
+        raise ValueError("invalid cache, batch or n_heads for a workspace, or bounds too large for one call")
     raw = torch.empty(n + 256, dtype=torch.uint8, device=cache.device)
     off = (-raw.data_ptr()) % 256
     return raw[off: off + n]

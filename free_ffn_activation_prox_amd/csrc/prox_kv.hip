@@ -593,7 +593,7 @@ int lanes_per_head(int hp) { return hp <= 64 ? 8 : hp <= 128 ? 16 : 32; }
 // be idle, to find the pairs costs more than it saves: one token 4.0 -> 4.7 us,
 // 64 tokens of as many sequences 7.3 -> 9.2, read of 32768 tokens 49 -> 51.
 static int64_t page_pairs(const prox_kv_batch& b, int& pp) {
-    const int64_t n = ((int64_t)b.max_q + 2 * kKvPage - 2) / kKvPage;
+    const int64_t n = ((int64_t)std::min(b.max_q, b.n_tokens) + 2 * kKvPage - 2) / kKvPage;
     pp = (int)(n < b.max_pages ? n : b.max_pages);
     const int64_t each = (int64_t)b.n_seq * pp, found = (b.n_tokens + (2 * kKvPage - 2) * (int64_t)b.n_seq) / kKvPage;
     if (2 * found > each) return each;

@@ -139,6 +139,7 @@ extern "C" prox_status prox_kv_attention(const prox_kv_cache* c, const prox_kv_b
     if (!workspace) return fail(PROX_E_INVALID, "null workspace");
     if (!aligned(workspace, 256)) return fail(PROX_E_INVALID, "workspace must be 256-byte aligned");
     const size_t need = kv_attention_workspace(*c, *b, n_heads);
+    if (need == 0) return launched(hipErrorInvalidConfiguration, "cache attention");
     if (ws_bytes < need) return fail(PROX_E_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     return launched(launch_kv_attention(*c, *b, static_cast<const uint16_t*>(q), q_stride, n_heads, scale, window,
                                         static_cast<uint16_t*>(out), out_stride, workspace, (hipStream_t)stream),

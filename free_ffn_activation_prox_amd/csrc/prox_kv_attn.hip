@@ -68,6 +68,8 @@
 //   4096-token prompt, 32 / 8 x 128           212   us  137 GFLOP at 650 TFLOP/s, see walk_together
 //   16384-token prompt                       2278   us  2199 GFLOP at 965 TFLOP/s: begins and joins weigh less
 //   ragged chunks, 40 / 8 x 64                242   us  127 GFLOP at 527 TFLOP/s: twice the exponentials a product
+#include <algorithm>
+
 #include "prox_kv.hpp"
 
 namespace prox {
@@ -149,6 +151,7 @@ struct Attend {
     uint32_t HG_inv;       // 2^17 / HG, rounded up
     int HG, VH;            // query heads of a segment; segments of one tile of tokens (key heads x head groups)
     int TQ, tiles;         // tokens of a tile; most tiles of a sequence
+    int all_tiles;         // and of the batch: a q_start that does not rise could name more, which are left out
     int rows_lo, rows_hi;  // least and most rows of the sequences that the launch takes
     int slot_rows;
     int seg_cost;          // units of a segment besides its pages
@@ -206,7 +209,7 @@ __device__ __forceinline__ void blocks_of(const Attend& A, int piece, int begin,
     w1 = hi / piece;
 }
 
-// The line of all segments (below 2^31, checked on the host), seen by one wave.
+// The line of all segments (below 2^31: the host checks all_tiles), seen by one wave.
 // It looks at 64 tiles at a time, those that there are of 64 sequences: with
 // one prompt among 255 single tokens these are 5 looks, where max_q alone would
 // allow 64 tiles for each sequence (256 looks).
@@ -215,6 +218,7 @@ struct Line {
     int l, total, looks;   // lane; units; looks that the line takes
     struct Look {
         int s0, j0, base;  // first sequence; first of its chunk's tiles; units before it
+        int before;        // tiles before the chunk
     };
     Look from;             // at() begins here
     KvRows Q;              // lane: sequence s0 + lane,
@@ -230,11 +234,11 @@ struct Line {
         }
         return v;
     }
-    __device__ __forceinline__ void chunk(int s0) {
+    __device__ __forceinline__ void chunk(int s0, int before) {
         Q = s0 + l < A.b.n_seq ? rows_of(A, s0 + l) : KvRows{0, 0, 0, 0};
         if (A.tiles > 1) {
             last = sum_up((int)((uint32_t)(Q.rows + A.TQ - 1) / (uint32_t)A.TQ), l);
-            tiles = __builtin_amdgcn_readlane(last, 63);
+            tiles = min(__builtin_amdgcn_readlane(last, 63), A.all_tiles - before);
         } else {
             tiles = 64;        // a lane's sequence is its tile
         }
@@ -261,12 +265,12 @@ struct Line {
     }
     // The looks from k on, until one reaches beyond unit x.
     __device__ __forceinline__ Look scan(Look k, int x) {
-        chunk(k.s0);
+        chunk(k.s0, k.before);
         for (;;) {
             while (k.j0 >= tiles) {
-                k = Look{k.s0 + 64, 0, k.base};
+                k = Look{k.s0 + 64, 0, k.base, k.before + (A.tiles > 1 ? tiles : 0)};
                 if (k.s0 >= A.b.n_seq) return k;
-                chunk(k.s0);
+                chunk(k.s0, k.before);
             }
             look(k);
             ++looks;
@@ -276,7 +280,7 @@ struct Line {
             k.base = end;
         }
     }
-    __device__ __forceinline__ Line(const Attend& a, int lane) : A(a), l(lane), looks(0), from{0, 0, 0} {
+    __device__ __forceinline__ Line(const Attend& a, int lane) : A(a), l(lane), looks(0), from{0, 0, 0, 0} {
         total = scan(from, 0x7fffffff).base;
     }
     // x < total; keep: no later call asks for a unit of an earlier look
@@ -1127,7 +1131,8 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
 struct Split {
     bool rows;                   // a tile of rows for each wave
     int NT, HG, VH, TQ, tiles, slot_rows, waves, blocks, seg_cost, no_cut, min_part, min_piece;
-    int64_t units;               // bound of the line's length
+    int64_t all_tiles, units;    // bounds of the batch's tiles and of the line's length
+    bool fits;                   // the line can be walked
     size_t part_at, part_bytes, lds, bytes;
 };
 
@@ -1137,8 +1142,11 @@ constexpr int few_waves(int NP) { return NP <= 2 ? 8 : 4; }
 // Waves of a block where each has rows of its own: see walk_together.
 constexpr int kRowWaves = 8;
 
-// For sequences of up to max_q tokens.
-Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int max_q) {
+// a * b, or anything above 2^62, of numbers up to 2^62
+int64_t times(int64_t a, int64_t b) { return a > 0 && b > (1ll << 62) / a ? (1ll << 62) + 1 : a * b; }
+
+// For n_tokens rows in sequences of up to max_q tokens.
+Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int64_t n_tokens, int max_q) {
     Split p;
     const int rep = n_heads / c.n_kv, NP = c.head_pad / 64;
     const int64_t most_rows = (int64_t)max_q * rep;
@@ -1154,7 +1162,7 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int 
     p.HG = (rep + groups - 1) / groups;
     p.VH = c.n_kv * groups;
     p.TQ = RT / p.HG;
-    p.tiles = (max_q + p.TQ - 1) / p.TQ;
+    p.tiles = (max_q - 1) / p.TQ + 1;
     p.slot_rows = (p.TQ < max_q ? p.TQ : max_q) * p.HG;
     // In pages' time.  Kernel times in us of: one token at 513 positions, at 131072, 64 ragged sequences |
     // sequences of 1 to 6 tokens, a prompt, ragged chunks (those of the head of this file).
@@ -1176,8 +1184,11 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int 
         p.lds = p.waves * 2 * p.slot_rows * row;
     }
     if (p.lds < (size_t)p.waves * 64 * 32) p.lds = (size_t)p.waves * 64 * 32;     // the join of parts: 8 floats a thread
-    p.units = (int64_t)b.n_seq * p.VH * p.tiles;
-    p.units = p.units > 0x7fffffffll ? p.units : p.units * (b.max_pages + p.seg_cost);
+    // A sequence of n rows has at most (n - 1) / TQ + 1 tiles: where q_start rises, no more in all than
+    // n_tokens / TQ + n_seq, however long max_q lets one sequence be.
+    p.all_tiles = std::min((int64_t)b.n_seq * p.tiles, n_tokens / p.TQ + b.n_seq);
+    p.units = times(times(p.all_tiles, p.VH), b.max_pages + p.seg_cost);
+    p.fits = p.units <= 0x7fffffffll && p.tiles < 1 << 24;      // the device adds up 64 sequences' tiles in 32 bits
     const int64_t most = p.units / p.min_piece + 1, cap = device_cus();
     p.blocks = (int)(most < cap ? most : cap);
     p.part_at = align_up((size_t)p.blocks * sizeof(unsigned long long), 256);
@@ -1232,21 +1243,48 @@ hipError_t attend_kind(const Attend& A, const Split& p, hipStream_t s) {
     }
 }
 
+// Launches of a call: that of short sequences, if there is one, and that of the others (or all).
+struct Launches {
+    int few;
+    Split split[2];
+    Launches(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
+        few = short_tokens(c, b, n_heads);
+        split[1] = split_of(c, b, n_heads, b.n_tokens, b.max_q);
+        split[0] = few > 0 ? split_of(c, b, n_heads, b.n_tokens, few) : split[1];
+    }
+    bool fit() const { return split[0].fits && split[1].fits; }
+};
+
+// The sizes of n_seq, max_q (up to 2^28, as many tokens as a call may have) and max_pages decide, not those of
+// n_tokens: a workspace made for a batch serves others of its shape.
+size_t workspace_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, const Launches& L) {
+    const int max_q = std::min(b.max_q, 1 << 28);
+    const size_t all = split_of(c, b, n_heads, times(b.n_seq, max_q), max_q).bytes;
+    return align_up(std::max(all, std::max(L.split[0].bytes, L.split[1].bytes)), 256);
+}
+
+// No sequence has more rows than the batch.
+prox_kv_batch bounded(const prox_kv_batch& b) {
+    prox_kv_batch r = b;
+    r.max_q = std::max(std::min(b.max_q, b.n_tokens), 1);
+    return r;
+}
+
 }  // namespace
 
 size_t kv_attention_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
-    // a launch for short sequences has fewer blocks and rows, so this holds it too
-    return b.max_q > 0 ? align_up(split_of(c, b, n_heads, b.max_q).bytes, 256) : 256;
+    if (b.max_q <= 0) return 256;
+    const Launches L(c, bounded(b), n_heads);
+    return L.fit() ? workspace_of(c, b, n_heads, L) : 0;
 }
 
-hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride,
+hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& batch, const uint16_t* q, int64_t q_stride,
                                int n_heads, float scale, int window, uint16_t* out, int64_t out_stride,
                                void* workspace, hipStream_t s) {
+    const prox_kv_batch b = bounded(batch);
     // one launch behind the other: they share the workspace
-    const int few = short_tokens(c, b, n_heads);
-    const Split split[2] = {split_of(c, b, n_heads, few > 0 ? few : b.max_q), split_of(c, b, n_heads, b.max_q)};
-    for (const Split& p : split)
-        if (p.units > 0x7fffffffll) return hipErrorInvalidConfiguration;
+    const Launches L(c, b, n_heads);
+    if (!L.fit()) return hipErrorInvalidConfiguration;
     Attend A{};
     A.c = c;
     A.b = b;
@@ -1259,10 +1297,10 @@ hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, c
     A.window = window;
     A.scale2 = fabsf(scale) * 1.4426950408889634f;
     A.sign = scale < 0.f ? -1.f : 1.f;
-    for (int k = few > 0 ? 0 : 1; k < 2; ++k) {
-        const Split& p = split[k];
-        A.rows_lo = k == 0 ? 1 : few + 1;
-        A.rows_hi = k == 0 ? few : b.max_q;
+    for (int k = L.few > 0 ? 0 : 1; k < 2; ++k) {
+        const Split& p = L.split[k];
+        A.rows_lo = k == 0 ? 1 : L.few + 1;
+        A.rows_hi = k == 0 ? L.few : b.max_q;
         A.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_at);
         A.part_bytes = (uint32_t)p.part_bytes;
         A.tag = next_call_tag();
@@ -1271,6 +1309,7 @@ hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& b, c
         A.VH = p.VH;
         A.TQ = p.TQ;
         A.tiles = p.tiles;
+        A.all_tiles = (int)p.all_tiles;
         A.slot_rows = p.slot_rows;
         A.seg_cost = p.seg_cost;
         A.no_cut = p.no_cut;

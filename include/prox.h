@@ -387,7 +387,8 @@ prox_status prox_kv_append(const prox_kv_cache* c, const prox_kv_batch* b, const
                            const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, void* stream);
 
 /* Workspace bytes prox_kv_attention needs for this cache, batch and query
- * heads; 0 if the arguments are invalid. */
+ * heads (of the batch, n_seq, max_q and max_pages count); 0 if the arguments are
+ * invalid or the batch's bounds too large for one call. */
 size_t prox_kv_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, int32_t n_heads);
 
 /* Attention of the batch's tokens over the cache: for query head h of the row
@@ -402,8 +403,11 @@ size_t prox_kv_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, i
  *            workspace must not overlap in time.
  * Scores, softmax statistics and sums are fp32; a softmax weight is rounded to
  * fp16 for the product with the values, and the sum it is divided by is that
- * of the rounded weights.  The batch's bounds multiplied (n_seq, n_heads,
- * max_q / 16, max_pages) should stay below 2^31 (PROX_E_UNSUPPORTED otherwise). */
+ * of the rounded weights.  What adds less than 2^-50 of a row's largest channel
+ * to another channel may be lost.  The rows go into tiles of one sequence and
+ * key head each, n_tokens * n_heads / 64 + n_seq * max(n_kv, n_heads / 64) at
+ * most; their number times max_pages + 3 has to stay below 2^31
+ * (PROX_E_UNSUPPORTED otherwise). */
 prox_status prox_kv_attention(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
                               int32_t n_heads, float scale, int32_t window, void* out, int64_t out_stride,
                               void* workspace, size_t ws_bytes, void* stream);
