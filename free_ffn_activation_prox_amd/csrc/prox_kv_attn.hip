@@ -1188,9 +1188,10 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int6
     // n_tokens / TQ + n_seq, however long max_q lets one sequence be.
     p.all_tiles = std::min((int64_t)b.n_seq * p.tiles, n_tokens / p.TQ + b.n_seq);
     p.units = times(times(p.all_tiles, p.VH), b.max_pages + p.seg_cost);
-    p.fits = p.units <= 0x7fffffffll && p.tiles < 1 << 24;      // the device adds up 64 sequences' tiles in 32 bits
     const int64_t most = p.units / p.min_piece + 1, cap = device_cus();
     p.blocks = (int)(most < cap ? most : cap);
+    // The device counts in 32 bits: units and a piece beyond them (blocks_of()), 64 sequences' tiles.
+    p.fits = p.units + p.units / p.blocks + 64 <= 0x7fffffffll && p.tiles < 1 << 24;
     p.part_at = align_up((size_t)p.blocks * sizeof(unsigned long long), 256);
     p.part_bytes = (size_t)p.blocks * 2 * p.slot_rows * row;
     p.bytes = p.part_at + p.part_bytes;

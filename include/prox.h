@@ -406,8 +406,8 @@ size_t prox_kv_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, i
  * of the rounded weights.  What adds less than 2^-50 of a row's largest channel
  * to another channel may be lost.  The rows go into tiles of one sequence and
  * key head each, n_tokens * n_heads / 64 + n_seq * max(n_kv, n_heads / 64) at
- * most; their number times max_pages + 3 has to stay below 2^31
- * (PROX_E_UNSUPPORTED otherwise). */
+ * most; their number times max_pages + 3 has to stay below 2^31 by a block's
+ * share of it (2^31 - 2^24 on 256 CUs; PROX_E_UNSUPPORTED otherwise). */
 prox_status prox_kv_attention(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
                               int32_t n_heads, float scale, int32_t window, void* out, int64_t out_stride,
                               void* workspace, size_t ws_bytes, void* stream);

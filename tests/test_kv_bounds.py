@@ -56,3 +56,14 @@ def test_workspace_of_a_batch_serves_others_of_its_shape():
                                for n in (0, 1, n_seq, max_q, max_q + n_seq, n_seq * max_q)
                                if (n * heads // 64 + n_seq * max(8, heads // 64)) * (pages + 3) < 1 << 31}
                         assert len(got) == 1 and 0 not in got, (heads, dim, max_q, n_seq, pages, got)
+
+
+def test_line_leaves_room_for_a_piece():
+    # 64 key heads: one unit for each page and one for the segment, 64 (max_pages + 1) in all.  A block adds
+    # its piece, a 256th of the line without a GPU, to units of the line in 32 bits
+    for pages, fits in ((33554430, False), (33554431 - (1 << 16), False), (33000000, True)):
+        b = batch(n_seq=1, n_tokens=1, max_q=1, max_pages=pages)
+        c = cache(n_kv=64)
+        assert 64 * (pages + 1) < 1 << 31
+        need, st = ws(c, b, 64), attend(c=c, b=b, H=64, qs=64 * 128, os=64 * 128, n=0)
+        assert (need > 0, st) == ((True, WORKSPACE) if fits else (False, UNSUPPORTED)), pages
