@@ -431,7 +431,8 @@ def _need(ok: bool, what: str) -> None:
 def _on(stream, device):
     """(stream pointer, whether the device is the current one) of a call on
     tensors of `device`: the given stream (the caller's inputs must be ready on
-    it), else the device's current one."""
+    it; they may be let go of once the call returns), else the device's current
+    one."""
     if stream is None:
         return _raw_stream(device.index), _current_device() == device.index
     if stream.device != device:
@@ -460,6 +461,15 @@ def _made_on(stream):
     """Context in which a call's own tensors are allocated: the stream that the
     call runs on, so that their memory is that stream's."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _held_for(stream, cache, batch, *tensors):
+    """After a call on a given stream: the memory of what it reads and writes
+    stays until that stream has run it, whatever the caller lets go of."""
+    if stream is not None and stream.cuda_stream != _raw_stream(cache.device.index):
+        for t in (cache.k, cache.v, cache.k_scale, cache.v_scale, batch.ctx_len, batch.block_table, batch.q_start) + tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 class KVCache:
@@ -580,6 +590,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, *, rot=None, q=None, q_out=N
     sp, here = _on(stream, dev)
     _kv_call(_lib.prox_kv_append, "prox_kv_append", dev, here, cache._ref, batch._ref, k.data_ptr(), ks, v.data_ptr(),
              vs, ctypes.byref(r), n_heads, qp, qs, qop, qos, sp)
+    _held_for(stream, cache, batch, k, v, q, q_out, rot, g_q, g_k)
     return q_out
 
 
@@ -622,6 +633,7 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, *, scale: Optional[float] = 
     _kv_call(_lib.prox_kv_attention, "prox_kv_attention", dev, here, cache._ref, batch._ref, q.data_ptr(), qs, n_heads,
              hd ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, workspace.data_ptr(),
              workspace.nbytes, sp)
+    _held_for(stream, cache, batch, q, out, workspace)
     return out
 
 
@@ -648,6 +660,7 @@ def kv_read(cache: KVCache, batch: KVBatch, *, dtype=torch.bfloat16, k_out=None,
     sp, here = _on(stream, dev)
     _kv_call(_lib.prox_kv_read, "prox_kv_read", dev, here, cache._ref, batch._ref, k_out.data_ptr(), v_out.data_ptr(),
              1 if dtype is torch.float32 else 0, sp)
+    _held_for(stream, cache, batch, k_out, v_out)
     return k_out, v_out
 
 
