@@ -528,6 +528,7 @@ class KVBatch:
                       and t.device == ctx_len.device, f"{n}: must be int32, contiguous, of shape {shape}, on one device")
         self.n_seq, self.n_tokens = n_seq, n_seq if n_tokens is None else int(n_tokens)
         self.max_q = (1 if q_start is None else self.n_tokens) if max_q is None else int(max_q)
+        _need(max(n_seq, self.n_tokens, self.max_q, int(block_table.shape[1])) < 1 << 31, "sizes must be below 2^31")
         self.ctx_len, self.block_table, self.q_start = ctx_len, block_table, q_start
         self.device = ctx_len.device
         self._c = _KVBatch(n_seq, self.n_tokens, self.max_q, int(block_table.shape[1]), ctx_len.data_ptr(),
@@ -619,6 +620,8 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, *, scale: Optional[float] = 
     dev, hd, n = cache.device, cache.head_dim, batch.n_tokens
     if batch.device != dev:
         raise ValueError("cache and batch are on different devices")
+    if window >= 1 << 31:
+        raise ValueError("window must be below 2^31")
     qs = _kv_rows("q", q, n, None, hd, dev)
     n_heads = q.shape[1]
     with _made_on(stream):

@@ -74,3 +74,16 @@ def test_offsets_that_do_not_rise_stay_in_bounds():
     # the sequences that are worked on all say the same of a row
     assert torch.allclose(out[:n].float(), want.float(), rtol=2.0 ** -7, atol=1e-3) and bool((out[n:] == 7).all())
     assert torch.equal(P.kv_attention(q[:n], w.c, one), want)
+
+
+def test_numbers_past_32_bits_are_refused():
+    w = World("int8", 4, 2, 64, [64], seed=103)
+    P = w.P
+    b, _ = w.batch([4])
+    q = w.rows(4, 4)
+    for call in (lambda: P.KVBatch(b.ctx_len, b.block_table, b.q_start, n_tokens=4, max_q=1 << 32),
+                 lambda: P.KVBatch(b.ctx_len, b.block_table, b.q_start, n_tokens=(1 << 32) + 4),
+                 lambda: P.kv_attention(q, w.c, b, window=1 << 32), lambda: P.kv_attention(q, w.c, b, window=(1 << 32) + 2)):
+        with pytest.raises(ValueError):
+            call()
+    assert torch.equal(P.kv_attention(q, w.c, b, window=0x7fffffff), P.kv_attention(q, w.c, b))
