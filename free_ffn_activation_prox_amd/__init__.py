@@ -537,7 +537,7 @@ class KVBatch:
 
 
 def _kv_rows(name, t, n, heads, hd, device):
-    """Row stride of an activation [n][heads][hd] (heads adjacent)."""
+    """Row stride of an activation [n][heads][hd] (heads adjacent); of one row it says nothing."""
     shape, stride = t.shape, t.stride()
     if t.dtype is not torch.bfloat16 or t.device != device:
         raise ValueError(f"{name} must be bf16 on the cache's device")
@@ -545,13 +545,13 @@ def _kv_rows(name, t, n, heads, hd, device):
         raise ValueError(f"{name} must be [n_tokens][heads][head_dim]")
     if n > 0 and (stride[2] != 1 or (stride[1] != hd and shape[1] != 1)):
         raise ValueError(f"{name}: the heads of a token must be adjacent")
-    return stride[0] if n > 1 else max(stride[0], shape[1] * hd)
+    return stride[0] if n > 1 else shape[1] * hd
 
 
 def kv_append(cache: KVCache, batch: KVBatch, k, v, *, rot=None, q=None, q_out=None, g_q=None, g_k=None,
               eps: float = 1e-5, pairing: str = "interleaved", stream=None):
     """Append the batch's keys and values (bf16 [n_tokens][n_kv][head_dim], rows
-    of any stride) to the cache, with the norm of each head (g_q, g_k: fp32
+    a multiple of 8 elements apart) to the cache, with the norm of each head (g_q, g_k: fp32
     [head_dim] gains) and the rotation of q and k by position on the way.  rot:
     cos, sin of every position and pair, complex64 [rows][rot_dim / 2] or
     fp32 [rows][rot_dim / 2][2], rows >= 64 * max_pages.  Returns q normed and
@@ -612,8 +612,8 @@ def alloc_kv_workspace(cache: KVCache, batch: KVBatch, n_heads: int):
 
 def kv_attention(q, cache: KVCache, batch: KVBatch, *, scale: Optional[float] = None, window: int = 0, out=None,
                  workspace=None, stream=None):
-    """Causal attention of q (bf16 [n_tokens][n_heads][head_dim], rows of any
-    stride, as kv_append returns it) over the cache; scale defaults to
+    """Causal attention of q (bf16 [n_tokens][n_heads][head_dim], rows a multiple
+    of 8 elements apart, as kv_append returns it) over the cache; scale defaults to
     1 / sqrt(head_dim), window > 0 limits a row to its last `window` positions.
     Returns out, bf16 [n_tokens][n_heads][head_dim]; rows that see nothing are
     zeros, rows outside every sequence are left as they were."""

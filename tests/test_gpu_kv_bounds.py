@@ -87,3 +87,26 @@ def test_numbers_past_32_bits_are_refused():
         with pytest.raises(ValueError):
             call()
     assert torch.equal(P.kv_attention(q, w.c, b, window=0x7fffffff), P.kv_attention(q, w.c, b))
+
+
+def test_one_row_of_any_stride():
+    # a batch of one row: the distance to a next one says nothing
+    w = World("fp8", 4, 2, 64, [80], seed=107)
+    P = w.P
+    settle(w, [79])
+    ref, got = [], []
+    x = w.rows(1, 8)
+    codes = w.c.k.clone(), w.c.v.clone(), w.c.k_scale.clone(), w.c.v_scale.clone()
+    for out, stride in ((ref, 512), (got, 515)):
+        for t, was in zip((w.c.k, w.c.v, w.c.k_scale, w.c.v_scale), codes):
+            t.copy_(was)
+        wide = torch.zeros(2, stride, dtype=torch.bfloat16, device="cuda")
+        wide[0, :512] = x.flatten()
+        q, k, v = (wide.as_strided((1, n, 64), (stride, 64, 1), a) for a, n in ((0, 4), (256, 2), (384, 2)))
+        batch = P.KVBatch(torch.tensor([80], dtype=torch.int32, device="cuda"), torch.from_numpy(w.table).cuda())
+        out.append(P.kv_append(w.c, batch, k, v, rot=w.rot.cuda(), q=q).clone())
+        out.append(P.kv_append(w.c, batch, k, v, rot=w.rot.cuda(), q=q.clone(), q_out=q).clone())
+        into = torch.zeros(2, stride, dtype=torch.bfloat16, device="cuda").as_strided((1, 4, 64), (stride, 64, 1))
+        out.append(P.kv_attention(q, w.c, batch, out=into))
+        out += [w.c.k.clone(), w.c.v.clone()]
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
