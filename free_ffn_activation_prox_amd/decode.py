@@ -119,6 +119,8 @@ class DecodeHarness:
         """Random keys and values at positions 0..n-1 (a context of n tokens, of every sequence)."""
         g = torch.Generator(device="cpu").manual_seed(seed)
         if self.cache != "dense":
+            if n > self.max_ctx:
+                raise ValueError(f"{n} tokens do not fit the cache's {self.max_ctx} positions")
             self.lengths = [0] * self.n_seq
             self._grow(range(self.n_seq), n)
             self.ctx.fill_(n)
@@ -182,6 +184,10 @@ class DecodeHarness:
         layer (up to 4096 at a time); paged cache only."""
         if self.cache == "dense":
             raise ValueError("prefill needs the paged cache (cache='int8' or 'fp8')")
+        if not 0 <= seq < self.n_seq:
+            raise ValueError(f"sequence {seq} of {self.n_seq}")
+        if x.dim() != 2 or x.shape[1] != self.shape.d:
+            raise ValueError("x must be [tokens][d]")
         self._grow([seq], x.shape[0])
         out = []
         for p in x.split(MAX_PREFILL) if x.shape[0] else ():
@@ -195,6 +201,8 @@ class DecodeHarness:
     def step(self, x: torch.Tensor) -> torch.Tensor:
         """x fp32 [n_seq][d] -> fp32 [n_seq][d] after every layer; the cache advances."""
         if self.cache != "dense":
+            if x.shape != (self.n_seq, self.shape.d):
+                raise ValueError("x must be [n_seq][d]")
             self._grow(range(self.n_seq), 1)
             self.ctx.add_(1)
             return self._paged(x, self.one, self.kv_ws)
