@@ -360,12 +360,15 @@ def read_probe_gbs(P, torch, dev, gib=2, reps=10):
 
 
 def kernel_sources_hash():
-    """sha256 (first 16 hex digits) of the library's kernel sources and header."""
+    """sha256 (first 16 hex digits) of the sources of the FFN forward's kernels: what
+    the committed profiles were taken on.  The cache's kernels (prox_kv*) are not
+    among them, nor is the header, which declares the interface of both."""
     files = sorted(glob.glob(os.path.join(ROOT, "free_ffn_activation_prox_amd", "csrc", "*.hip")) +
                    glob.glob(os.path.join(ROOT, "free_ffn_activation_prox_amd", "csrc", "*.hpp")))
-    files.append(os.path.join(ROOT, "include", "prox.h"))
     h = hashlib.sha256()
     for f in files:
+        if os.path.basename(f).startswith("prox_kv"):
+            continue
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
