@@ -1,8 +1,8 @@
 // Device helpers of the paged 8-bit key/value cache: where a value lies in a
 // page, what a code stands for, and which tokens a batch names.
 //
-// Page layout.  The products of attention run on v_mfma_f32_16x16x32_bf16 with
-// the cache as the A operand (lane l: row l % 16, eight values of the reduced
+// Page layout.  The products of attention run on v_mfma_f32_16x16x32_f16 (codes
+// widened to fp16) with the cache as the A operand (lane l: row l % 16, eight values of the reduced
 // dimension at 8 (l / 16)).  Scores reduce over channels, K rows are tokens;
 // outputs reduce over tokens, V rows are channels.  A page stores each
 // kilobyte that one wave loads (16 bytes a lane, two operands) contiguously:
@@ -66,14 +66,6 @@ __device__ __forceinline__ uint32_t kv_codes4(const float x[4]) {
         int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
     }
-}
-
-// A load at an address that is the same for the whole wave, from memory that no
-// kernel of this call writes: through the constant address space it is a scalar
-// load, which vector loads in flight do not have to come back for.
-template <typename T>
-__device__ __forceinline__ T uniform_load(const T* p) {
-    return *(const __attribute__((address_space(4))) T*)p;
 }
 
 // The same codes for values that are finite and at most qmax (1 + 2^-23) large:
