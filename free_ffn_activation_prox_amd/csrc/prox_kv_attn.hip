@@ -514,7 +514,7 @@ struct Rows {
         const int under = some ? unit - ve : 0;
         const bool fits = unit != kNoUnit && (uint32_t)under < (uint32_t)-kLeast;
         float top[NT];
-        bool move = false;
+        bool large = false;
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             // not 0 (a page of zeros): 0 x -inf would be NaN; the scores of such a page vanish all the same.
@@ -524,7 +524,7 @@ struct Rows {
 #pragma unroll
             for (int i = 1; i < 16; ++i) most = fmaxf(most, w[u][i >> 2][i & 3]);
             top[u] = over_groups_max(most) * fac[u];
-            move = move || top[u] - m[u] > kSlack;
+            large = large || top[u] >= kLarge;
         }
         const float ratio = vl - (float)under, same = __builtin_amdgcn_exp2f(-ratio);
 #pragma unroll
@@ -532,7 +532,23 @@ struct Rows {
             base[u] = m[u] - ratio;
             back[u] = same;
         }
-        if (__builtin_expect(!fits || __ballot(move) != 0, 0)) this->move(w, top, fac, base, back, some, ve, vl);
+        if (__builtin_expect(!fits || __ballot(large) != 0, 0)) move(w, top, fac, base, back, some, ve, vl);
+        // most moves are of m alone; there is none left behind move()
+        bool grow = false;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) grow = grow || top[u] - m[u] > kSlack;
+        if (__ballot(grow)) {
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const float mn = fmaxf(m[u], floorf(top[u])), f = __builtin_amdgcn_exp2f(m[u] - mn);
+                m[u] = mn;
+                e[u] = mn > kNothing ? unit : e[u];
+                sum[u] *= f;
+                base[u] = mn - ratio;
+#pragma unroll
+                for (int d = 0; d < 4 * NP; ++d) o[u][d] *= f;
+            }
+        }
     }
 
     // limits() where some row's m or e moves, or the rows differ in e.
