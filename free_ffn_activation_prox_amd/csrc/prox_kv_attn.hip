@@ -335,6 +335,7 @@ constexpr float kTop = 10.f, kSlack = 5.9f;
 constexpr int kLeast = -2;             // exponent of the least sv / 2^e that goes into the weights
 constexpr int kRoom = 100;             // exponent that a row's sums stay below when e moves down
 constexpr int kNoUnit = -1000;         // e of a row that has seen no value but zeros
+constexpr int kNoPage = -1001;         // unit before the first page with others
 constexpr float kNothing = -0x1p126f;  // m of a row that has seen nothing; scores are above
 constexpr float kLarge = 0x1p20f;      // maxima from here on: see limits()
 
@@ -392,7 +393,7 @@ struct Rows {
     f32x4_t o[NT][4 * NP];      // lane (g, n): channels 16 d + 4 g + r of row 16 u + n, in units of 2^e
     float m[NT], sum[NT];
     int e[NT];
-    int unit;                   // e of every row that has seen a key, kNoUnit where they differ or an m is kLarge
+    int unit;                   // e of every row; kNoUnit where they differ or an m is kLarge
     bool live[NT];
     int key_lo[NT], key_hi[NT]; // positions that the row sees: key_lo .. key_hi - 1
     uint4 q[NT][NP][2];
@@ -462,7 +463,7 @@ struct Rows {
 #pragma unroll
             for (int d = 0; d < 4 * NP; ++d) o[u][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-        unit = kNoUnit;
+        unit = kNoPage;
     }
 
     // The scores of one page, in units of fac: keys(a, t, x, y) gives the two
@@ -510,6 +511,11 @@ struct Rows {
             }
         }
         const bool some = ve != kNoUnit;                // the page has values other than zeros
+        if (some && unit == kNoPage) {
+            unit = ve;
+#pragma unroll
+            for (int u = 0; u < NT; ++u) e[u] = ve;
+        }
         // a page without counts as one of the unit's scale: its values are read as zeros
         const int under = some ? unit - ve : 0;
         const bool fits = unit != kNoUnit && (uint32_t)under < (uint32_t)-kLeast;
@@ -532,28 +538,31 @@ struct Rows {
             base[u] = m[u] - ratio;
             back[u] = same;
         }
-        if (__builtin_expect(!fits || __ballot(large) != 0, 0)) move(w, top, fac, base, back, some, ve, vl);
+        float f[NT];                                    // what o is multiplied by: in one place only
+#pragma unroll
+        for (int u = 0; u < NT; ++u) f[u] = 1.f;
+        if (__builtin_expect(!fits || __ballot(large) != 0, 0)) move(w, top, fac, base, back, f, some, ve, vl);
         // most moves are of m alone; there is none left behind move()
         bool grow = false;
 #pragma unroll
-        for (int u = 0; u < NT; ++u) grow = grow || top[u] - m[u] > kSlack;
+        for (int u = 0; u < NT; ++u) grow = grow || f[u] != 1.f || top[u] - m[u] > kSlack;
         if (__ballot(grow)) {
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
-                const float mn = fmaxf(m[u], floorf(top[u])), f = __builtin_amdgcn_exp2f(m[u] - mn);
+                const float mn = fmaxf(m[u], floorf(top[u])), keep = __builtin_amdgcn_exp2f(m[u] - mn);
+                base[u] = mn > m[u] ? mn - ratio : base[u];
                 m[u] = mn;
-                e[u] = mn > kNothing ? unit : e[u];
-                sum[u] *= f;
-                base[u] = mn - ratio;
+                sum[u] *= keep;
+                f[u] *= keep;
 #pragma unroll
-                for (int d = 0; d < 4 * NP; ++d) o[u][d] *= f;
+                for (int d = 0; d < 4 * NP; ++d) o[u][d] *= f[u];
             }
         }
     }
 
     // limits() where some row's m or e moves, or the rows differ in e.
     __device__ __forceinline__ void move(f32x4_t (&w)[NT][4], const float (&top)[NT], float (&fac)[NT], float (&base)[NT],
-                                         float (&back)[NT], bool some, int ve, float vl) {
+                                         float (&back)[NT], float (&f)[NT], bool some, int ve, float vl) {
 #pragma clang fp contract(off)
         uint64_t large = 0;
 #pragma unroll
@@ -575,12 +584,10 @@ struct Rows {
                 const int room = kRoom - __builtin_amdgcn_frexp_expf(big) - (int)fmaxf(keep, -500.f);
                 if (down) en = big > 0.f ? max(ve, en - min(max(room, 0), 126)) : ve;
             }
-            const float f = __builtin_amdgcn_exp2f(fminf(keep + (float)(e[u] - en), 126.f));
+            f[u] = __builtin_amdgcn_exp2f(fminf(keep + (float)(e[u] - en), 126.f));
             sum[u] *= __builtin_amdgcn_exp2f(keep);
             m[u] = mn;
             e[u] = en;
-#pragma unroll
-            for (int d = 0; d < 4 * NP; ++d) o[u][d] *= f;
             const float ratio = some ? fmaxf(vl + (float)(ve - en), kTop + (float)kLeast) : vl;
             base[u] = mn - ratio;
             back[u] = __builtin_amdgcn_exp2f(-ratio);
@@ -604,7 +611,12 @@ struct Rows {
         bool differ = false;
 #pragma unroll
         for (int u = 0; u < NT; ++u) differ = differ || (m[u] > kNothing && e[u] != one);
-        unit = __ballot(differ) || large ? kNoUnit : one;
+        unit = kNoUnit;
+        if (__ballot(differ) == 0 && large == 0) {
+            unit = one;
+#pragma unroll
+            for (int u = 0; u < NT; ++u) e[u] = one;            // o of a row that has seen nothing is 0
+        }
     }
 
     // The weights of a page as operands.
