@@ -11,8 +11,9 @@
 // bounds the call is reading q, k, v once and, for one token, the latency of
 // the launch.  Kernel times, with 32 query and 8 key heads of 128 channels:
 //   one token 4.0 us (latency); 64 sequences of one 7.3 us (10 MB: latency, each
-//   page's scale and codes read before they are written); 4096 tokens 22.7 us
-//   (117 MB, 5.2 TB/s); read-back of 32768 tokens 49 us (201 MB, 4.1 TB/s).
+//   page's scale and codes read before they are written); 4096 tokens 23.6 us
+//   (117 MB, 5.0 TB/s); read-back of 32768 tokens 50 us (201 MB, 4.0 TB/s), as
+//   fp32 105 us (336 MB, 3.2 TB/s).
 #include <algorithm>
 
 #include "prox_kv.hpp"

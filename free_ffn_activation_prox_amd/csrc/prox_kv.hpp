@@ -2,10 +2,11 @@
 // page, what a code stands for, and which tokens a batch names.
 //
 // Page layout.  The products of attention run on v_mfma_f32_16x16x32_f16 (codes
-// widened to fp16) with the cache as the A operand (lane l: row l % 16, eight values of the reduced
-// dimension at 8 (l / 16)).  Scores reduce over channels, K rows are tokens;
-// outputs reduce over tokens, V rows are channels.  A page stores each
-// kilobyte that one wave loads (16 bytes a lane, two operands) contiguously:
+// widened to fp16) with the cache as the A operand (lane l: row l % 16, eight
+// values of the reduced dimension at 8 (l / 16)).  Scores reduce over channels,
+// K rows are tokens; outputs reduce over tokens, V rows are channels.  A page
+// stores each kilobyte that one wave loads (16 bytes a lane, two operands)
+// contiguously:
 //   K block (64 channels a, 16 tokens b): lane (c = l / 16, d = l % 16) holds
 //     channels 64 a + 16 c .. + 15 of token 16 b + d
 //   V block (16 channels a): lane (b, c) holds tokens 16 d + 4 b + e, d, e < 4,

@@ -59,15 +59,16 @@
 // position, so results do not depend on timing.  (A launch of its own for that
 // took 5 us of one token's call and up to 100 us of a prompt's.)
 //
-// What bounds it (medians of kernel time, query / key heads x channels; a copy
-// of 2 GiB runs at 4.9 TB/s here, a 16384^3 product in bf16 at 1380 TFLOP/s):
-//   one token, 32 / 32 x 128, 513 positions    11.7 us  the chain of table, scales, keys, values, join (4.2 MB)
-//   one token, 64 / 8 x 128, 131072 positions  63.8 us  268 MB at 4.2 TB/s: memory, read once (counters: 271 MB)
-//   64 ragged sequences, 32 / 8 x 128          52   us  224 MB at 4.3 TB/s: memory
-//   16 sequences of 1 to 6 tokens, 28 / 4 x 128, window 4096   27 us  a page's instructions, 8 waves a CU (39 MB)
-//   4096-token prompt, 32 / 8 x 128           212   us  137 GFLOP at 650 TFLOP/s, see walk_together
-//   16384-token prompt                       2278   us  2199 GFLOP at 965 TFLOP/s: begins and joins weigh less
-//   ragged chunks, 40 / 8 x 64                242   us  127 GFLOP at 527 TFLOP/s: twice the exponentials a product
+// What bounds it (medians of kernel time under a profiler and, in brackets, of calls
+// back to back; query / key heads x channels; a copy of 2 GiB runs at 4.9 TB/s
+// here, a 16384^3 product in bf16 at 1380 TFLOP/s):
+//   one token, 32 / 32 x 128, 513 positions    12.7 us  latency; its parts are not measured (4.2 MB)
+//   one token, 64 / 8 x 128, 131072 positions  64.6 us  268 MB at 4.2 TB/s: memory, read once (counters: 271 MB)
+//   64 ragged sequences, 32 / 8 x 128          52.5 us  224 MB at 4.3 TB/s: memory
+//   16 sequences of 1 to 6 tokens, 28 / 4 x 128, window 4096   27.5 us  5 to 7 of a block's 8 waves have no rows (39 MB)
+//   4096-token prompt, 32 / 8 x 128           236 (203) us  137 GFLOP at 680 TFLOP/s, see walk_together
+//   16384-token prompt                       2550 (2470) us  2199 GFLOP at 890 TFLOP/s: begins and joins weigh less
+//   ragged chunks, 40 / 8 x 64                252 (219) us  127 GFLOP at 580 TFLOP/s: twice the exponentials a product
 #include <algorithm>
 
 #include "prox_kv.hpp"
@@ -822,14 +823,16 @@ __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& 
 // loaded once for the block, each wave turning its share of the codes to fp16
 // operands in LDS (two pages' worth: one is filled while the other is used),
 // so a page costs the block one barrier.
-// A 4096-token prompt takes 212 us so, and 297 where each wave loads and
-// converts its own operands.  Two waves share a SIMD (229 registers); the
-// matrix unit is busy 36 % of the time and no single unit is the bound: with the
-// LDS reads, exponentials, weights or fills left out in turn the time fell by 0
-// to 20 of 224 us, with the products left out by 24.  Measured and not kept:
-// the next page's keys multiplied beside the exponentials (322 us, spills), two
-// groups of waves half a page apart (220), four waves in each of two blocks
-// (244), one tile of 16 rows a wave: 8 waves 299, 12 waves 233, 16 waves 271.
+// Two waves share a SIMD (248 registers).  Measured on a form of this loop that
+// took 212 us for a 4096-token prompt (one unit of the sums for a whole wave;
+// units of the rows' own cost some 5 %): 297 where each wave loads and converts
+// its own operands; the matrix unit is busy 36 % of the time and no single unit
+// is the bound: with the LDS reads, exponentials, weights or fills left out in
+// turn the time fell by 0 to 20 of 224 us, with the products left out by 24.
+// Not kept: the next page's keys multiplied beside the exponentials (322 us,
+// spills), two groups of waves half a page apart (220), four waves in each of
+// two blocks (244), one tile of 16 rows a wave: 8 waves 299, 12 waves 233, 16
+// waves 271.
 // LDS: keys [2][4 NP x 2 operands][64] uint4, values the same.
 template <int KIND, int NP, int NT, int kWaves>
 __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds, const Attend& A, const Place& P,
@@ -1179,7 +1182,8 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int6
     const int rep = n_heads / c.n_kv, NP = c.head_pad / 64;
     const int64_t most_rows = (int64_t)max_q * rep;
     // More than 16 rows get tiles with rows for each wave: sequences of up to 6 tokens and 7 query heads a
-    // key head take 27 us so, and 41 in tiles of 16 rows, each of which reads the pages again.
+    // key head take 27 us so, and 41 in tiles of 16 rows, each of which reads the pages again.  (Up to 128 rows
+    // leave most of the 8 waves without any: 64 single tokens with 32 query heads on one key head take 47 us.)
     p.rows = most_rows > 16;
     p.waves = p.rows ? kRowWaves : few_waves(NP);
     // 32 rows a wave use each operand from LDS twice: a prompt 209 us, with 16 rows a wave 299.  Up to 16
@@ -1193,7 +1197,8 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int6
     p.tiles = (max_q - 1) / p.TQ + 1;
     p.slot_rows = (p.TQ < max_q ? p.TQ : max_q) * p.HG;
     // In pages' time.  Kernel times in us of: one token at 513 positions, at 131072, 64 ragged sequences |
-    // sequences of 1 to 6 tokens, a prompt, ragged chunks (those of the head of this file).
+    // sequences of 1 to 6 tokens, a prompt, ragged chunks (those of the head of this file, on the form that
+    // walk_together names).
     //   as it is               11.6  63.8  51.6 | 26.8  213  240
     //   seg_cost 0 | 1         11.2  63.3  65.2 | 31.1  303  244
     //   seg_cost 2 | 6         10.9  63.7  51.7 | 27.8  211  241
@@ -1230,13 +1235,16 @@ Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int6
 // rows, waves that split the pages) before that of the longer ones, 0 where all
 // go into one.  In a tile for 8 waves a single token keeps one wave busy, and a
 // line of many such segments leaves the long ones too few blocks:
-//   a 4096-token prompt and 255 tokens at 1000 positions: one launch 532 us, two 309
-//   a 512-token prompt and 31 such tokens:                           66        53
-//   2 chunks of 512 and 30 tokens at 20000 positions:               654       275
+//   a 4096-token prompt and 255 tokens at 1000 positions: one launch 532 us, two 318
+//   a 512-token prompt and 31 such tokens:                           66        56
+//   2 chunks of 512 and 30 tokens at 20000 positions:               654       280
 //   40 chunks of 9 to 243 tokens, none short:                       159.1     159.7
 // One launch where the host sees that all sequences are alike, where the longest
-// fits one tile, or where there cannot be a short segment for each block (a
-// prompt and 15 tokens: 200 us).
+// fits one tile, or where there cannot be a short segment for each block: a
+// prompt and 15 tokens take 209 us so.  That last rule counts segments, not their
+// pages: 2 chunks and 29 tokens at 20000 positions, one segment too few for each
+// block, still take 655 us in one launch; with 4 key heads, 2 chunks and 30
+// tokens 346 where 62 tokens in two launches take 283.
 int short_tokens(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     const int rep = n_heads / c.n_kv, few = 16 / rep;
     const bool mixed = (int64_t)b.max_q * rep > 256 && b.n_tokens < (int64_t)b.n_seq * b.max_q;
