@@ -531,7 +531,7 @@ struct Rows {
 #pragma unroll
             for (int i = 1; i < 16; ++i) most = fmaxf(most, w[u][i >> 2][i & 3]);
             top[u] = over_groups_max(most) * fac[u];
-            large = large || top[u] >= kLarge;
+            large = large || (fabsf(top[u]) >= kLarge && top[u] != -INFINITY);
         }
         const float ratio = vl - (float)under, same = __builtin_amdgcn_exp2f(-ratio);
 #pragma unroll
@@ -543,7 +543,7 @@ struct Rows {
 #pragma unroll
         for (int u = 0; u < NT; ++u) f[u] = 1.f;
         if (__builtin_expect(!fits || __ballot(large) != 0, 0)) move(w, top, fac, base, back, f, some, ve, vl);
-        // most moves are of m alone; there is none left behind move()
+        // most moves are of m alone, and there is none left behind move()
         bool grow = false;
 #pragma unroll
         for (int u = 0; u < NT; ++u) grow = grow || f[u] != 1.f || top[u] - m[u] > kSlack;

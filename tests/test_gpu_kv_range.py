@@ -246,3 +246,26 @@ def test_many_tiny_weights_beside_an_outlier(kind, outlier):
         b, start = w.batch([new], advance=False)
         out, _ = w.attend(b, start, q=q[:new].clone(), scale=24.0 * float(np.log(2.0)))
         assert float(out[-1].float().abs().min()) > 2e-4
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_scores_far_from_zero(kind, sign):
+    # the best key of the first pages scores +-2^x, every other one is lower by half of
+    # that and more: the row is its value; then a page of scores around zero
+    w = World(kind, 2, 1, 64, [400], seed=79)
+    b, start = w.batch([400])
+    k, v = w.rows(400, 1), w.rows(400, 1)
+    steps = torch.arange(400, device="cuda") % 50
+    k[:, 0, 0] = -(steps + 1.0) if sign < 0 else 60.0 - steps
+    k[320:384, 0, 0] = 0                      # page 5
+    w.P.kv_append(w.c, b, k, v)
+    KO.append(w.o, w.table, w.ctx, start, 400, f64(k), f64(v))
+    w.same_cache()
+    for n in (1, 60, 390):
+        b, start = w.batch([n], advance=False)
+        q = torch.zeros(n, 2, 64, dtype=torch.bfloat16, device="cuda")
+        q[..., 0] = 1.0
+        for x in (12, 18, 20, 22, 25, 30, 60, 100):
+            w.attend(b, start, q=q, scale=2.0 ** x)
+            w.attend(b, start, q=q, scale=2.0 ** x, window=200)
