@@ -62,13 +62,13 @@
 // What bounds it (medians of kernel time under a profiler and, in brackets, of calls
 // back to back; query / key heads x channels; a copy of 2 GiB runs at 4.9 TB/s
 // here, a 16384^3 product in bf16 at 1380 TFLOP/s):
-//   one token, 32 / 32 x 128, 513 positions    12.7 us  latency; its parts are not measured (4.2 MB)
-//   one token, 64 / 8 x 128, 131072 positions  64.6 us  268 MB at 4.2 TB/s: memory, read once (counters: 271 MB)
-//   64 ragged sequences, 32 / 8 x 128          52.5 us  224 MB at 4.3 TB/s: memory
-//   16 sequences of 1 to 6 tokens, 28 / 4 x 128, window 4096   27.5 us  5 to 7 of a block's 8 waves have no rows (39 MB)
-//   4096-token prompt, 32 / 8 x 128           236 (203) us  137 GFLOP at 680 TFLOP/s, see walk_together
-//   16384-token prompt                       2550 (2470) us  2199 GFLOP at 890 TFLOP/s: begins and joins weigh less
-//   ragged chunks, 40 / 8 x 64                252 (219) us  127 GFLOP at 580 TFLOP/s: twice the exponentials a product
+//   one token, 32 / 32 x 128, 513 positions    12.5 us  latency; its parts are not measured (4.2 MB)
+//   one token, 64 / 8 x 128, 131072 positions  65.4 us  268 MB at 4.1 TB/s: memory, read once (counters: 271 MB)
+//   64 ragged sequences, 32 / 8 x 128          52.6 us  224 MB at 4.3 TB/s: memory
+//   16 sequences of 1 to 6 tokens, 28 / 4 x 128, window 4096   27.3 us  5 to 7 of a block's 8 waves have no rows (39 MB)
+//   4096-token prompt, 32 / 8 x 128           242 (204) us  137 GFLOP at 674 TFLOP/s, see walk_together
+//   16384-token prompt                       2530 (2460) us  2199 GFLOP at 890 TFLOP/s: begins and joins weigh less
+//   ragged chunks, 40 / 8 x 64                270 (226) us  127 GFLOP at 565 TFLOP/s: twice the exponentials a product
 #include <algorithm>
 
 #include "prox_kv.hpp"

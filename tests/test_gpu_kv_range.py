@@ -269,3 +269,20 @@ def test_scores_far_from_zero(kind, sign):
         for x in (12, 18, 20, 22, 25, 30, 60, 100):
             w.attend(b, start, q=q, scale=2.0 ** x)
             w.attend(b, start, q=q, scale=2.0 ** x, window=200)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_keys_of_zeros_weigh_alike_under_any_query(kind):
+    # a key scale of 0 beside a query whose own scale is past fp32
+    w = World(kind, 2, 1, 64, [150], seed=109)
+    b, start = w.batch([150])
+    k, v = w.rows(150, 1) * 0, w.rows(150, 1)
+    w.P.kv_append(w.c, b, k, v)
+    KO.append(w.o, w.table, w.ctx, start, 150, f64(k), f64(v))
+    w.same_cache()
+    assert not w.c.k_scale[torch.from_numpy(w.table[0]).long().cuda()].any()
+    for n in (1, 150):
+        b, start = w.batch([n], advance=False)
+        for size in (1.0, 3e38):
+            for scale in (4.0, -1e30, 0.0):
+                w.attend(b, start, q=torch.full((n, 2, 64), size, dtype=torch.bfloat16, device="cuda"), scale=scale)
