@@ -78,6 +78,11 @@ class _KVRotation(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class _KVPool(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("n_seq", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("refs", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+
+
 N_PHASES = 3
 PHASES = ("stage1", "stage2", "reduce_y")
 
@@ -113,6 +118,10 @@ def _load() -> ctypes.CDLL:
         "prox_kv_attention": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, ctypes.c_float,
                                     I32, P, I64, P, SZ, P]),
         "prox_kv_read": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, P, I32, P]),
+        "prox_kv_pages_workspace_bytes": (SZ, [ctypes.POINTER(_KVPool)]),
+        "prox_kv_pages": (I32, [ctypes.POINTER(_KVPool), P, P, P, P, I32, P, P, P, SZ, P]),
+        "prox_kv_page_bounds": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, P]),
+        "prox_kv_select": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, P, I32, I32, I32, P, P]),
         "prox_status_str": (ctypes.c_char_p, [I32]),
         "prox_last_error": (ctypes.c_char_p, []),
     }
@@ -467,9 +476,13 @@ def _held_for(stream, cache, batch, *tensors):
     """After a call on a given stream: the memory of what it reads and writes
     stays until that stream has run it, whatever the caller lets go of."""
     if stream is not None and stream.cuda_stream != _raw_stream(cache.device.index):
-        for t in (cache.k, cache.v, cache.k_scale, cache.v_scale, batch.ctx_len, batch.block_table, batch.q_start) + tensors:
-            if t is not None:
-                t.record_stream(stream)
+        _hold(stream, cache.k, cache.v, cache.k_scale, cache.v_scale, batch.ctx_len, batch.block_table, batch.q_start, *tensors)
+
+
+def _hold(stream, *tensors):
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 class KVCache:
@@ -667,7 +680,124 @@ def kv_read(cache: KVCache, batch: KVBatch, *, dtype=torch.bfloat16, k_out=None,
     return k_out, v_out
 
 
-__all__ = ["KVCache", "KVBatch", "KV_KINDS", "KV_PAGE", "kv_head_pad", "kv_append", "kv_attention", "kv_read",
+class KVPool:
+    """Pages of a cache and the sequences that hold them, kept on the device
+    (``include/prox.h``): refs int32 [n_pages] (sequences that hold a page),
+    ctx_len int32 [n_seq] and block_table int32 [n_seq][max_pages], the last two as
+    KVBatch takes them.  ``KVPool.alloc`` makes an empty one; kv_pages moves it."""
+
+    def __init__(self, refs, ctx_len, block_table):
+        _need(refs.dim() == 1 and ctx_len.dim() == 1 and block_table.dim() == 2
+              and block_table.shape[0] == ctx_len.shape[0], "refs must be [n_pages], ctx_len [n_seq], block_table [n_seq][max_pages]")
+        for n, t in (("refs", refs), ("ctx_len", ctx_len), ("block_table", block_table)):
+            _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.device == refs.device,
+                  f"{n}: must be int32, contiguous, on one device")
+        self.refs, self.ctx_len, self.block_table, self.device = refs, ctx_len, block_table, refs.device
+        self.n_pages, self.n_seq, self.max_pages = int(refs.shape[0]), int(ctx_len.shape[0]), int(block_table.shape[1])
+        _need(max(self.n_pages, self.n_seq, self.max_pages) < 1 << 31, "sizes must be below 2^31")
+        self._c = _KVPool(self.n_pages, self.n_seq, self.max_pages, refs.data_ptr(), ctx_len.data_ptr(),
+                          block_table.data_ptr())
+        self._ref = ctypes.byref(self._c)
+        n = _lib.prox_kv_pages_workspace_bytes(self._ref)
+        if n == 0:
+            raise ValueError(f"invalid pool: {_lib.prox_last_error().decode()}")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    @classmethod
+    def alloc(cls, n_pages: int, n_seq: int, max_pages: int, device="cuda") -> "KVPool":
+        return cls(torch.zeros(n_pages, dtype=torch.int32, device=device), torch.zeros(n_seq, dtype=torch.int32, device=device),
+                   torch.full((n_seq, max_pages), -1, dtype=torch.int32, device=device))
+
+
+def _ints(name, t, shape, device):
+    if t is not None and not (t.dtype is torch.int32 and t.device == device and t.is_contiguous() and t.shape == shape):
+        raise ValueError(f"{name} must be int32, contiguous, of shape {tuple(shape)}, on the pool's device")
+    return None if t is None else t.data_ptr()
+
+
+def kv_pages(pool: KVPool, want, n_rows: int, *, parent=None, shared=None, q_start=None, slots=None, status=None,
+             stream=None):
+    """Take the pool's sequences to want (int32 [n_seq]) tokens: pages are taken
+    and given back, pool.ctx_len and pool.block_table follow.  A sequence without
+    tokens whose parent[s] is not -1 begins with that sequence's first shared[s]
+    pages, which both then hold.  Returns (q_start [n_seq + 1], slots [n_rows],
+    status [2]), int32: the new tokens' rows for a KVBatch of n_rows tokens, each
+    row's place 64 * page + slot (-1 behind the last), and how many sequences were
+    refused (they keep their tokens) and how many pages are free."""
+    dev, n = pool.device, (pool.n_seq,)
+    if not 0 <= n_rows < 1 << 31:
+        raise ValueError("n_rows must be at least 0 and below 2^31")
+    wp, pp, sp_ = _ints("want", want, n, dev), _ints("parent", parent, n, dev), _ints("shared", shared, n, dev)
+    with _made_on(stream):
+        if q_start is None:
+            q_start = torch.empty(pool.n_seq + 1, dtype=torch.int32, device=dev)
+        if slots is None:
+            slots = torch.empty(n_rows, dtype=torch.int32, device=dev)
+        if status is None:
+            status = torch.empty(2, dtype=torch.int32, device=dev)
+    qp, lp, tp = (_ints("q_start", q_start, (pool.n_seq + 1,), dev), _ints("slots", slots, (n_rows,), dev),
+                  _ints("status", status, (2,), dev))
+    sp, here = _on(stream, dev)
+    _kv_call(_lib.prox_kv_pages, "prox_kv_pages", dev, here, pool._ref, wp, pp, sp_, qp, n_rows, lp, tp,
+             pool.workspace.data_ptr(), pool.workspace.nbytes, sp)
+    if stream is not None and stream.cuda_stream != _raw_stream(dev.index):
+        _hold(stream, pool.refs, pool.ctx_len, pool.block_table, pool.workspace, want, parent, shared, q_start, slots, status)
+    return q_start, slots, status
+
+
+def alloc_kv_bounds(cache: KVCache):
+    """Bounds of the keys of the cache's pages, int8 [n_pages][n_kv][2][head_pad], all 0."""
+    return torch.zeros(cache.n_pages, cache.n_kv, 2, cache.head_pad, dtype=torch.int8, device=cache.device)
+
+
+def _bounds_ptr(cache, bounds):
+    if not (bounds.dtype is torch.int8 and bounds.device == cache.device and bounds.is_contiguous()
+            and bounds.shape == (cache.n_pages, cache.n_kv, 2, cache.head_pad)):
+        raise ValueError("bounds must be contiguous int8 [n_pages][n_kv][2][head_pad] on the cache's device")
+    return bounds.data_ptr()
+
+
+def kv_page_bounds(cache: KVCache, batch: KVBatch, bounds, *, stream=None):
+    """Set the bounds (least and largest code of every channel) of the pages that
+    the batch's tokens lie in, behind kv_append with the same batch or over whole
+    sequences.  Returns bounds."""
+    dev = cache.device
+    if batch.device != dev:
+        raise ValueError("cache and batch are on different devices")
+    bp = _bounds_ptr(cache, bounds)
+    sp, here = _on(stream, dev)
+    _kv_call(_lib.prox_kv_page_bounds, "prox_kv_page_bounds", dev, here, cache._ref, batch._ref, bp, sp)
+    _held_for(stream, cache, batch, bounds)
+    return bounds
+
+
+def kv_select(q, cache: KVCache, batch: KVBatch, bounds, n_keep: int, *, first: int = 1, last: int = 1, pages=None,
+              stream=None):
+    """For every row of q (as kv_attention takes it) and key head the n_keep pages
+    of its sequence whose keys can give the largest scores, by their bounds; the
+    first `first` and last `last` pages that the row sees are always among them.
+    Returns pages, int32 [n_tokens][n_kv][n_keep], ascending, then -1; rows outside
+    every sequence are left as they were."""
+    dev, hd, n = cache.device, cache.head_dim, batch.n_tokens
+    if batch.device != dev:
+        raise ValueError("cache and batch are on different devices")
+    if max(n_keep, first, last) >= 1 << 31 or min(n_keep, first, last) < -1 << 31:
+        raise ValueError("n_keep, first and last must fit 32 bits")
+    qs = _kv_rows("q", q, n, None, hd, dev)
+    bp = _bounds_ptr(cache, bounds)
+    if pages is None:
+        with _made_on(stream):
+            pages = torch.empty(n, cache.n_kv, max(n_keep, 0), dtype=torch.int32, device=dev)
+    pp = _ints("pages", pages, (n, cache.n_kv, n_keep), dev)
+    sp, here = _on(stream, dev)
+    _kv_call(_lib.prox_kv_select, "prox_kv_select", dev, here, cache._ref, batch._ref, q.data_ptr(), qs, q.shape[1], bp,
+             n_keep, first, last, pp, sp)
+    _held_for(stream, cache, batch, q, bounds, pages)
+    return pages
+
+
+__all__ = ["KVPool", "kv_pages", "alloc_kv_bounds", "kv_page_bounds", "kv_select",
+           "KVCache", "KVBatch", "KV_KINDS", "KV_PAGE", "kv_head_pad", "kv_append", "kv_attention", "kv_read",
            "kv_workspace_bytes", "alloc_kv_workspace",
            "QWeights", "build_qweights", "qweights_bytes", "quality", "timeline_forward", "read_probe", "noalloc_scratch_bytes", "ffn_forward_noalloc", "Weights", "Proxy", "ProxError", "abi_version", "library_sha256", "proxy_bytes", "workspace_bytes",
            "build_proxy", "alloc_workspace", "ffn_forward", "LIB_PATH", "KINDS", "N_PHASES", "PHASES"]

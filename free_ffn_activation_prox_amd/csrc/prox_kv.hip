@@ -134,14 +134,6 @@ struct Head8 {
     }
 };
 
-// Sequence s and page j of it for pair i of the grid (see page_pairs).
-__device__ __forceinline__ bool pair_of(const prox_kv_batch& b, int pp, int i, int lane, int& s, int& j) {
-    if (pp == 0) return kv_pair_of(b, i, lane, s, j);
-    s = i / pp;
-    j = i % pp;
-    return true;
-}
-
 struct Append {
     prox_kv_cache c;
     prox_kv_batch b;
@@ -583,24 +575,6 @@ hipError_t append_kind(const Append& A, int64_t blocks, hipStream_t s) {
 int lanes_per_head(int hp) { return hp <= 64 ? 8 : hp <= 128 ? 16 : 32; }
 
 }  // namespace
-
-// Blocks for the pages that a batch's tokens can touch.  Each sequence gets as
-// many as max_q neighbouring positions can touch (pp, the first of them anywhere
-// in a page), or, where that would leave half of the blocks without work, pp is
-// 0 and the blocks find their pairs of sequence and page in the lengths: there
-// are (n + 126) / 64 at most for n tokens, so (n_tokens + 126 n_seq) / 64 in all.
-// A 4096-token prompt beside 255 single tokens of 8 key heads: append 216 us
-// with pp blocks a sequence, 55 us so; read 82 and 16 us.  Where few blocks would
-// be idle, to find the pairs costs more than it saves: one token 4.0 -> 4.7 us,
-// 64 tokens of as many sequences 7.3 -> 9.2, read of 32768 tokens 49 -> 51.
-static int64_t page_pairs(const prox_kv_batch& b, int& pp) {
-    const int64_t n = ((int64_t)std::min(b.max_q, b.n_tokens) + 2 * kKvPage - 2) / kKvPage;
-    pp = (int)(n < b.max_pages ? n : b.max_pages);
-    const int64_t each = (int64_t)b.n_seq * pp, found = (b.n_tokens + (2 * kKvPage - 2) * (int64_t)b.n_seq) / kKvPage;
-    if (2 * found > each) return each;
-    pp = 0;
-    return found;
-}
 
 hipError_t launch_kv_append(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* k, int64_t k_stride,
                             const uint16_t* v, int64_t v_stride, const prox_kv_rotation& r, int n_heads,

@@ -2,6 +2,7 @@
 // Every check runs before the first, so an error return enqueues nothing.
 #include "prox.h"
 #include "prox_internal.hpp"
+#include "prox_kv.hpp"
 
 using namespace prox;
 
@@ -155,4 +156,73 @@ extern "C" prox_status prox_kv_read(const prox_kv_cache* c, const prox_kv_batch*
     if (!k_out || !v_out) return fail(PROX_E_INVALID, "null k_out or v_out");
     if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(PROX_E_INVALID, "outputs must be 16-byte aligned");
     return launched(launch_kv_read(*c, *b, k_out, v_out, out_fp32 != 0, (hipStream_t)stream), "cache read");
+}
+
+static prox_status check_pool(const prox_kv_pool* p) {
+    if (!p) return fail(PROX_E_INVALID, "null pool");
+    if (p->n_pages < 1 || p->n_seq < 1 || p->max_pages < 1)
+        return fail(PROX_E_INVALID, "n_pages, n_seq and max_pages must be >= 1");
+    if (p->n_pages > PROX_KV_MAX_POOL || p->n_seq > PROX_KV_MAX_POOL)
+        return fail(PROX_E_UNSUPPORTED, "more than PROX_KV_MAX_POOL pages or sequences");
+    if (p->max_pages > 0x7fffffff / PROX_KV_PAGE) return fail(PROX_E_UNSUPPORTED, "64 * max_pages above 2^31 - 1");
+    if (!p->refs || !p->ctx_len || !p->block_table) return fail(PROX_E_INVALID, "null pool array");
+    if (!aligned(p->refs, 4) || !aligned(p->ctx_len, 4) || !aligned(p->block_table, 4))
+        return fail(PROX_E_INVALID, "misaligned pool array");
+    return PROX_OK;
+}
+
+extern "C" size_t prox_kv_pages_workspace_bytes(const prox_kv_pool* p) {
+    clear_error();
+    return check_pool(p) == PROX_OK ? kv_pages_workspace(*p) : 0;
+}
+
+extern "C" prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want, const int32_t* parent,
+                                     const int32_t* shared, int32_t* q_start, int32_t n_rows, int32_t* slots,
+                                     int32_t* status, void* workspace, size_t ws_bytes, void* stream) {
+    clear_error();
+    PROX_CHECK(check_pool(p));
+    if (!want || !q_start || !status) return fail(PROX_E_INVALID, "null want, q_start or status");
+    if ((!parent) != (!shared)) return fail(PROX_E_INVALID, "parent and shared must both be given or both be null");
+    if (n_rows < 0) return fail(PROX_E_INVALID, "n_rows must be >= 0");
+    if (n_rows > 0 && !slots) return fail(PROX_E_INVALID, "null slots");
+    if (!aligned(want, 4) || !aligned(parent, 4) || !aligned(shared, 4) || !aligned(q_start, 4) || !aligned(slots, 4) ||
+        !aligned(status, 4))
+        return fail(PROX_E_INVALID, "misaligned array");
+    if (!workspace) return fail(PROX_E_INVALID, "null workspace");
+    if (!aligned(workspace, 4)) return fail(PROX_E_INVALID, "workspace must be 4-byte aligned");
+    const size_t need = kv_pages_workspace(*p);
+    if (ws_bytes < need) return fail(PROX_E_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    return launched(launch_kv_pages(*p, want, parent, shared, q_start, n_rows, slots, status, workspace, (hipStream_t)stream),
+                    "page tables");
+}
+
+extern "C" prox_status prox_kv_page_bounds(const prox_kv_cache* c, const prox_kv_batch* b, void* bounds, void* stream) {
+    clear_error();
+    PROX_CHECK(check_cache(c));
+    PROX_CHECK(check_batch(b));
+    if (b->n_tokens == 0 || b->max_q == 0) return PROX_OK;
+    if (!bounds) return fail(PROX_E_INVALID, "null bounds");
+    if (!aligned(bounds, 16)) return fail(PROX_E_INVALID, "bounds must be 16-byte aligned");
+    return launched(launch_kv_bounds(*c, *b, static_cast<int8_t*>(bounds), (hipStream_t)stream), "page bounds");
+}
+
+extern "C" prox_status prox_kv_select(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
+                                      int32_t n_heads, const void* bounds, int32_t n_keep, int32_t first, int32_t last,
+                                      int32_t* pages, void* stream) {
+    clear_error();
+    PROX_CHECK(check_cache(c));
+    PROX_CHECK(check_batch(b));
+    PROX_CHECK(check_heads(c, n_heads));
+    if (n_keep < 1) return fail(PROX_E_INVALID, "n_keep must be >= 1");
+    if (n_keep > 1 << 20) return fail(PROX_E_UNSUPPORTED, "n_keep above 2^20");
+    if (first < 0 || last < 1 || first > n_keep || last > n_keep - first)
+        return fail(PROX_E_INVALID, "first >= 0, last >= 1 and first + last <= n_keep are needed");
+    if (b->max_pages > PROX_KV_MAX_SELECT_PAGES) return fail(PROX_E_UNSUPPORTED, "max_pages above PROX_KV_MAX_SELECT_PAGES");
+    if (b->n_tokens == 0 || b->max_q == 0) return PROX_OK;
+    if (!bounds || !pages) return fail(PROX_E_INVALID, "null bounds or pages");
+    if (!aligned(bounds, 16) || !aligned(pages, 4)) return fail(PROX_E_INVALID, "misaligned bounds or pages");
+    PROX_CHECK(check_rows("q", q, q_stride, (int64_t)n_heads * c->head_dim));
+    return launched(launch_kv_select(*c, *b, static_cast<const uint16_t*>(q), q_stride, n_heads,
+                                     static_cast<const int8_t*>(bounds), n_keep, first, last, pages, (hipStream_t)stream),
+                    "page selection");
 }

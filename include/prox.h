@@ -418,6 +418,78 @@ prox_status prox_kv_attention(const prox_kv_cache* c, const prox_kv_batch* b, co
 prox_status prox_kv_read(const prox_kv_cache* c, const prox_kv_batch* b, void* k_out, void* v_out, int32_t out_fp32,
                          void* stream);
 
+/* ---- Page tables on the device -------------------------------------------------
+ * A pool of pages and the sequences that hold them (host struct; the caller owns
+ * the device arrays).  ctx_len and block_table are those of a prox_kv_batch.  A
+ * new pool: refs and ctx_len 0, block_table -1. */
+#define PROX_KV_MAX_POOL (1 << 24)   /* most pages, and most sequences, of a pool */
+typedef struct {
+    int32_t n_pages;
+    int32_t n_seq;
+    int32_t max_pages;       /* entries of one table row; 64 * max_pages < 2^31 */
+    int32_t* refs;           /* [n_pages]: sequences that hold the page; 0: free */
+    int32_t* ctx_len;        /* [n_seq]: tokens of each sequence */
+    int32_t* block_table;    /* [n_seq][max_pages]: its pages in order, then -1 */
+} prox_kv_pool;
+
+/* Workspace bytes of prox_kv_pages; 0 if the pool is invalid. */
+size_t prox_kv_pages_workspace_bytes(const prox_kv_pool* p);
+
+/* Take every sequence s to want[s] tokens (device; below 0 counts as 0):
+ *   1  a sequence of 0 tokens whose parent[s] names one begins with that one's
+ *      first min(shared[s], ctx_len[parent[s]] / 64) pages (whole pages, by its
+ *      length before the call), which both then hold;
+ *   2  pages that a sequence needs no more are given back (one that ends, or
+ *      drops tokens); a page that nobody holds is free at once;
+ *   3  pages that it needs more are the free ones of lowest number, in order of
+ *      the sequences.  A sequence keeps the length of step 1 and gets nothing if
+ *      the free pages do not last up to it, if want[s] exceeds the table, or if it
+ *      would go on in a page that another sequence holds too (cut back into
+ *      shared pages): it is refused, the call goes on with the others.
+ * Out (device), for the next prox_kv_batch:
+ *   ctx_len, block_table, refs   the state after the call
+ *   q_start [n_seq + 1]  the rows of the new tokens (0 for those that did not grow)
+ *   slots   [n_rows]     64 * page + slot of each such row, -1 for rows behind the
+ *                        last (rows that n_rows leaves no room for are dropped)
+ *   status  [2]          sequences refused; free pages left
+ * parent and shared [n_seq] are both given or both null.  workspace: device, 4-byte
+ * aligned, scratch.  Calls on one pool must not overlap in time. */
+prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want, const int32_t* parent, const int32_t* shared,
+                          int32_t* q_start, int32_t n_rows, int32_t* slots, int32_t* status, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/* ---- Sparse attention: pages selected by bounds of their keys ------------------
+ * Bounds of the keys of a cache's pages, int8 [n_pages][n_kv][2][head_pad]: of each
+ * channel the least and the largest code of the page's tokens (e4m3 values v as
+ * floor(127 v / 448) and ceil(127 v / 448); NaN as 0).  prox_kv_page_bounds sets
+ * those of every page that the batch's tokens lie in, from all tokens of the page
+ * up to the sequence's last one; it is called behind prox_kv_append (which may
+ * round a page's codes again) with the same batch, or once over whole sequences.
+ * bounds: device, 16-byte aligned. */
+prox_status prox_kv_page_bounds(const prox_kv_cache* c, const prox_kv_batch* b, void* bounds, void* stream);
+
+/* For every row of the batch and key head the n_keep pages of its sequence, of
+ * those that it sees (0 .. position / 64), whose keys can give the largest score:
+ *   unit_h = fl32(max|q_h| / 127) over finite channels, q8 = clamp(round-half-even(
+ *   fl32(q / unit_h)), -127, 127) (infinities +-127, NaN 0; unit 0: zeros),
+ *   dot_h = sum_d (min(q8_d, 0) lo_d + max(q8_d, 0) hi_d), a whole number: the
+ *   most that q8 . k can be for keys within the bounds,
+ *   key = fl32(max_h fl32(dot_h unit_h) k_scale) over the query heads h of the head;
+ * larger keys first, equal ones by the lower page, NaN last.  The first `first` and
+ * the last `last` of them (last >= 1: the row's own page) are kept in any case;
+ * pages that the table does not name are not.  Meant for attention with a scale
+ * above 0.
+ *   q      as for prox_kv_attention
+ *   pages  device int32 [n_tokens][n_kv][n_keep]: numbers within the sequence,
+ *          ascending, then -1; all -1 for a row whose position does not exist.
+ *          Rows outside every sequence are not touched.
+ * 1 <= n_keep <= 2^20; first + last <= n_keep; max_pages up to
+ * PROX_KV_MAX_SELECT_PAGES (PROX_E_UNSUPPORTED above). */
+#define PROX_KV_MAX_SELECT_PAGES 32768
+prox_status prox_kv_select(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
+                           int32_t n_heads, const void* bounds, int32_t n_keep, int32_t first, int32_t last,
+                           int32_t* pages, void* stream);
+
 /* ---- Measurement helper (not part of the forward) ---------------------------
  * Read-stream probe: reads the first bytes / 16 * 16 bytes of the device
  * buffer `buf` (16-byte aligned) with `blocks` blocks of 512 threads, each

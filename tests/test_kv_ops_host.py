@@ -1,0 +1,113 @@
+"""The operators around the paged cache without a GPU: refusals of the C ABI
+(before anything is enqueued), the Python handles' checks, and pins of their oracle."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import free_ffn_activation_prox_amd as P
+from free_ffn_activation_prox_amd import _KVPool, _lib
+from oracle import kv_oracle as KO
+from oracle import kv_ops_oracle as OO
+from test_kv_host import FAKE, INVALID, MISMATCH, UNSUPPORTED, WORKSPACE, batch, cache
+
+
+def pool(**over):
+    p = _KVPool(100, 4, 8, FAKE, FAKE, FAKE)
+    for k, v in over.items():
+        setattr(p, k, v)
+    return p
+
+
+def pages(p=None, want=FAKE, parent=None, shared=None, qs=FAKE, rows=10, slots=FAKE, status=FAKE, ws=FAKE, n=1 << 40):
+    return _lib.prox_kv_pages(ctypes.byref(p or pool()), want, parent, shared, qs, rows, slots, status, ws, n, None)
+
+
+def bounds(c=None, b=None, out=FAKE):
+    return _lib.prox_kv_page_bounds(ctypes.byref(c or cache()), ctypes.byref(b or batch()), out, None)
+
+
+def select(c=None, b=None, q=FAKE, qs=512, H=4, bnd=FAKE, keep=4, first=1, last=1, out=FAKE):
+    return _lib.prox_kv_select(ctypes.byref(c or cache()), ctypes.byref(b or batch()), q, qs, H, bnd, keep, first, last,
+                               out, None)
+
+
+def test_pool_refusals():
+    for over, want in ((dict(n_pages=0), INVALID), (dict(n_seq=0), INVALID), (dict(max_pages=0), INVALID),
+                       (dict(n_pages=(1 << 24) + 1), UNSUPPORTED), (dict(n_seq=(1 << 24) + 1), UNSUPPORTED),
+                       (dict(max_pages=1 << 26), UNSUPPORTED), (dict(refs=0), INVALID), (dict(ctx_len=0), INVALID),
+                       (dict(block_table=0), INVALID), (dict(refs=FAKE + 2), INVALID), (dict(ctx_len=FAKE + 1), INVALID)):
+        assert pages(p=pool(**over)) == want, over
+        assert _lib.prox_kv_pages_workspace_bytes(ctypes.byref(pool(**over))) == 0
+    for over in (dict(want=0), dict(qs=0), dict(status=0), dict(slots=0), dict(ws=0), dict(parent=FAKE), dict(shared=FAKE),
+                 dict(rows=-1), dict(want=FAKE + 2), dict(ws=FAKE + 2), dict(slots=FAKE + 1)):
+        assert pages(**over) == INVALID, over
+    need = _lib.prox_kv_pages_workspace_bytes(ctypes.byref(pool()))
+    assert need > 0 and pages(n=need - 1) == WORKSPACE
+
+
+@pytest.mark.parametrize("call", [bounds, select])
+def test_cache_and_batch_refusals(call):
+    for over, want in ((dict(kind=0), INVALID), (dict(n_pages=0), INVALID), (dict(n_kv=1025), UNSUPPORTED),
+                       (dict(head_dim=132), INVALID), (dict(head_pad=64), MISMATCH), (dict(k=0), INVALID)):
+        assert call(c=cache(**over)) == want, over
+    for over, want in ((dict(n_seq=0), INVALID), (dict(n_tokens=-1), INVALID), (dict(max_pages=0), INVALID),
+                       (dict(max_pages=1 << 26), UNSUPPORTED), (dict(ctx_len=0), INVALID), (dict(q_start=0), INVALID)):
+        assert call(b=batch(**over)) == want, over
+    for b in (batch(n_tokens=0), batch(max_q=0)):
+        assert call(b=b) == 0
+
+
+def test_bounds_and_select_refusals():
+    assert bounds(out=0) == INVALID and bounds(out=FAKE + 8) == INVALID
+    assert select(q=0) == INVALID and select(bnd=0) == INVALID and select(out=0) == INVALID
+    assert select(bnd=FAKE + 8) == INVALID and select(out=FAKE + 2) == INVALID
+    assert select(H=5) == INVALID and select(H=1026) == UNSUPPORTED and select(qs=511) == INVALID
+    assert select(keep=0, first=0) == INVALID and select(keep=(1 << 20) + 1) == UNSUPPORTED
+    assert select(first=-1) == INVALID and select(last=0) == INVALID and select(keep=4, first=3, last=2) == INVALID
+    assert select(first=0x7fffffff, last=0x7fffffff) == INVALID
+    assert select(b=batch(max_pages=32769)) == UNSUPPORTED
+
+
+def test_python_handles_refuse_host_tensors_and_shapes():
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        P.KVPool(torch.zeros(9, dtype=torch.int32), i, torch.zeros(3, 4, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        P.KVPool(torch.zeros(9, dtype=torch.int32), i, torch.zeros(2, 4, dtype=torch.int32))
+
+
+def test_oracle_pool_conserves_pages():
+    r = np.random.default_rng(1)
+    o = OO.Pool(60, 7, 12)
+    for _ in range(60):
+        want = np.where(r.random(7) < 0.2, 0, np.maximum(o.ctx + r.integers(-90, 120, 7), 0))
+        q_start, slots, status = o.move(want, 2000, r.integers(-1, 7, 7), r.integers(0, 5, 7))
+        # each page's count is how often the tables name it; the rest of a row is -1
+        names = o.table[o.table >= 0]
+        assert np.array_equal(np.bincount(names, minlength=60), o.refs)
+        assert np.array_equal((o.table >= 0).sum(1), -(-o.ctx // 64))
+        assert status[1] == (o.refs == 0).sum()
+        used = slots[:q_start[-1]]
+        assert (used >= 0).all() and np.unique(used).size == used.size and (slots[q_start[-1]:] == -1).all()
+        assert (o.refs[used // 64] == 1).all()                       # nothing new goes into a shared page
+
+
+def test_oracle_bounds_hold_for_every_query():
+    r = np.random.default_rng(2)
+    for kind in ("int8", "fp8"):
+        c = KO.Cache(kind, 3, 2, 24)
+        c.k = r.integers(0, 256, c.k.shape).astype(np.uint8)
+        table = np.array([[2, 0]], np.int32)
+        b = np.zeros((3, 2, 2, c.hp), np.int8)
+        OO.bounds(c, table, [100], None, 1, 1, b)                     # one token: the page that it lies in
+        assert not b[1].any() and not b[2].any()
+        OO.bounds(c, table, [100], np.array([0, 100]), 100, 100, b)
+        tok = np.nan_to_num(KO.decode(kind, c.tokens("k")), nan=0.0) * (1.0 if kind == "int8" else 127 / 448)
+        for pg, held in ((2, 64), (0, 36)):
+            for _ in range(20):
+                q = r.standard_normal((2, c.hp))
+                top = np.maximum(q * b[pg, :, 0], q * b[pg, :, 1]).sum(-1)
+                assert ((tok[pg, :, :held] * q[:, None]).sum(-1).max(-1) <= top + 1e-9).all()
