@@ -122,6 +122,9 @@ def _load() -> ctypes.CDLL:
         "prox_kv_pages": (I32, [ctypes.POINTER(_KVPool), P, P, P, P, I32, P, P, P, SZ, P]),
         "prox_kv_page_bounds": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, P]),
         "prox_kv_select": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, P, I32, I32, I32, P, P]),
+        "prox_kv_selected_workspace_bytes": (SZ, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), I32, I32]),
+        "prox_kv_attention_selected": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, P, I32,
+                                             ctypes.c_float, P, I64, P, SZ, P]),
         "prox_status_str": (ctypes.c_char_p, [I32]),
         "prox_last_error": (ctypes.c_char_p, []),
     }
@@ -796,7 +799,53 @@ def kv_select(q, cache: KVCache, batch: KVBatch, bounds, n_keep: int, *, first: 
     return pages
 
 
-__all__ = ["KVPool", "kv_pages", "alloc_kv_bounds", "kv_page_bounds", "kv_select",
+def _alloc_scratch(cache, n):
+    """n bytes of scratch on the cache's device, 256-byte aligned."""
+    if n == 0:
+        raise ValueError(f"no workspace for this call: {_lib.prox_last_error().decode() or 'its bounds are too large'}")
+    raw = torch.empty(n + 256, dtype=torch.uint8, device=cache.device)
+    off = (-raw.data_ptr()) % 256
+    return raw[off: off + n]
+
+
+def alloc_kv_selected_workspace(cache: KVCache, batch: KVBatch, n_heads: int, n_keep: int):
+    """Workspace of kv_attention_selected for batches of n_tokens rows."""
+    with torch.cuda.device(cache.device):
+        n = _lib.prox_kv_selected_workspace_bytes(cache._ref, batch._ref, n_heads, n_keep)
+    return _alloc_scratch(cache, n)
+
+
+def kv_attention_selected(q, cache: KVCache, batch: KVBatch, pages, *, scale: Optional[float] = None, out=None,
+                          workspace=None, stream=None):
+    """kv_attention over the pages that kv_select lists (pages int32 [n_tokens][n_kv]
+    [n_keep]): a row sees the positions up to its own of the pages listed for it
+    and the key head.  Returns out; rows that see nothing are zeros, rows outside
+    every sequence are left as they were."""
+    dev, hd, n = cache.device, cache.head_dim, batch.n_tokens
+    if batch.device != dev:
+        raise ValueError("cache and batch are on different devices")
+    qs = _kv_rows("q", q, n, None, hd, dev)
+    n_heads = q.shape[1]
+    if pages.dim() != 3 or pages.shape[2] >= 1 << 31:
+        raise ValueError("pages must be [n_tokens][n_kv][n_keep]")
+    pp, keep = _ints("pages", pages, (n, cache.n_kv, pages.shape[2]), dev), pages.shape[2]
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = alloc_kv_selected_workspace(cache, batch, n_heads, keep)
+    os_ = _kv_rows("out", out, n, n_heads, hd, dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
+    sp, here = _on(stream, dev)
+    _kv_call(_lib.prox_kv_attention_selected, "prox_kv_attention_selected", dev, here, cache._ref, batch._ref, q.data_ptr(),
+             qs, n_heads, pp, keep, hd ** -0.5 if scale is None else scale, out.data_ptr(), os_, workspace.data_ptr(),
+             workspace.nbytes, sp)
+    _held_for(stream, cache, batch, q, out, workspace, pages)
+    return out
+
+
+__all__ = ["alloc_kv_selected_workspace", "kv_attention_selected", "KVPool", "kv_pages", "alloc_kv_bounds", "kv_page_bounds", "kv_select",
            "KVCache", "KVBatch", "KV_KINDS", "KV_PAGE", "kv_head_pad", "kv_append", "kv_attention", "kv_read",
            "kv_workspace_bytes", "alloc_kv_workspace",
            "QWeights", "build_qweights", "qweights_bytes", "quality", "timeline_forward", "read_probe", "noalloc_scratch_bytes", "ffn_forward_noalloc", "Weights", "Proxy", "ProxError", "abi_version", "library_sha256", "proxy_bytes", "workspace_bytes",

@@ -185,5 +185,9 @@ hipError_t launch_kv_pages(const prox_kv_pool& p, const int32_t* want, const int
 hipError_t launch_kv_bounds(const prox_kv_cache& c, const prox_kv_batch& b, int8_t* bounds, hipStream_t s);
 hipError_t launch_kv_select(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride, int n_heads,
                             const int8_t* bounds, int keep, int first, int last, int32_t* pages, hipStream_t s);
+size_t kv_selected_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int keep);
+hipError_t launch_kv_selected(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride, int n_heads,
+                              const int32_t* pages, int keep, float scale, uint16_t* out, int64_t out_stride,
+                              void* workspace, hipStream_t s);
 
 }  // namespace prox

@@ -196,6 +196,12 @@ extern "C" prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want,
                     "page tables");
 }
 
+static prox_status check_keep(int32_t n_keep) {
+    if (n_keep < 1) return fail(PROX_E_INVALID, "n_keep must be >= 1");
+    if (n_keep > 1 << 20) return fail(PROX_E_UNSUPPORTED, "n_keep above 2^20");
+    return PROX_OK;
+}
+
 extern "C" prox_status prox_kv_page_bounds(const prox_kv_cache* c, const prox_kv_batch* b, void* bounds, void* stream) {
     clear_error();
     PROX_CHECK(check_cache(c));
@@ -213,8 +219,7 @@ extern "C" prox_status prox_kv_select(const prox_kv_cache* c, const prox_kv_batc
     PROX_CHECK(check_cache(c));
     PROX_CHECK(check_batch(b));
     PROX_CHECK(check_heads(c, n_heads));
-    if (n_keep < 1) return fail(PROX_E_INVALID, "n_keep must be >= 1");
-    if (n_keep > 1 << 20) return fail(PROX_E_UNSUPPORTED, "n_keep above 2^20");
+    PROX_CHECK(check_keep(n_keep));
     if (first < 0 || last < 1 || first > n_keep || last > n_keep - first)
         return fail(PROX_E_INVALID, "first >= 0, last >= 1 and first + last <= n_keep are needed");
     if (b->max_pages > PROX_KV_MAX_SELECT_PAGES) return fail(PROX_E_UNSUPPORTED, "max_pages above PROX_KV_MAX_SELECT_PAGES");
@@ -225,4 +230,40 @@ extern "C" prox_status prox_kv_select(const prox_kv_cache* c, const prox_kv_batc
     return launched(launch_kv_select(*c, *b, static_cast<const uint16_t*>(q), q_stride, n_heads,
                                      static_cast<const int8_t*>(bounds), n_keep, first, last, pages, (hipStream_t)stream),
                     "page selection");
+}
+
+extern "C" size_t prox_kv_selected_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, int32_t n_heads,
+                                                   int32_t n_keep) {
+    clear_error();
+    if (check_cache(c) != PROX_OK || check_batch(b) != PROX_OK || check_heads(c, n_heads) != PROX_OK ||
+        check_keep(n_keep) != PROX_OK)
+        return 0;
+    return kv_selected_workspace(*c, *b, n_heads, n_keep);
+}
+
+extern "C" prox_status prox_kv_attention_selected(const prox_kv_cache* c, const prox_kv_batch* b, const void* q,
+                                                  int64_t q_stride, int32_t n_heads, const int32_t* pages, int32_t n_keep,
+                                                  float scale, void* out, int64_t out_stride, void* workspace,
+                                                  size_t ws_bytes, void* stream) {
+    clear_error();
+    PROX_CHECK(check_cache(c));
+    PROX_CHECK(check_batch(b));
+    PROX_CHECK(check_heads(c, n_heads));
+    PROX_CHECK(check_keep(n_keep));
+    if (!(scale > -3.0e38f && scale < 3.0e38f)) return fail(PROX_E_INVALID, "scale must be finite");
+    if (b->n_tokens == 0 || b->max_q == 0) return PROX_OK;
+    const int64_t width = (int64_t)n_heads * c->head_dim;
+    PROX_CHECK(check_rows("q", q, q_stride, width));
+    PROX_CHECK(check_rows("out", out, out_stride, width));
+    if (q == out) return fail(PROX_E_INVALID, "out must not be q");
+    if (!pages) return fail(PROX_E_INVALID, "null pages");
+    if (!aligned(pages, 4)) return fail(PROX_E_INVALID, "misaligned pages");
+    if (!workspace) return fail(PROX_E_INVALID, "null workspace");
+    if (!aligned(workspace, 256)) return fail(PROX_E_INVALID, "workspace must be 256-byte aligned");
+    const size_t need = kv_selected_workspace(*c, *b, n_heads, n_keep);
+    if (need == 0) return launched(hipErrorInvalidConfiguration, "attention over selected pages");
+    if (ws_bytes < need) return fail(PROX_E_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    return launched(launch_kv_selected(*c, *b, static_cast<const uint16_t*>(q), q_stride, n_heads, pages, n_keep, scale,
+                                       static_cast<uint16_t*>(out), out_stride, workspace, (hipStream_t)stream),
+                    "attention over selected pages");
 }

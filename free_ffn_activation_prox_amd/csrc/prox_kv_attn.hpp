@@ -739,12 +739,14 @@ struct Pages {
     static constexpr int kBytes = kKvPage * 64 * NP;
     const Attend& A;
     const int32_t* table;
-    int head, upto, base, id, ve;
+    int head, upto, pg0, base, id, ve;
     float ks, vl;          // K's scale; V's scale 2^(ve + vl - kTop), -1 <= vl - kTop < 0 (0: ve kNoUnit)
     __device__ __forceinline__ Pages(const Attend& a, const Place& P, const Tile& T, int from, int up, int l)
-        : A(a), table(a.b.block_table + (size_t)P.s * a.b.max_pages + T.pg0), head(P.vh / (a.VH / a.c.n_kv)), upto(up) {
+        : A(a), table(a.b.block_table + (size_t)P.s * a.b.max_pages + T.pg0), head(P.vh / (a.VH / a.c.n_kv)), upto(up),
+          pg0(T.pg0) {
         look(from, l);
     }
+    __device__ __forceinline__ int base_key(int p) const { return (pg0 + p) * kKvPage; }
     __device__ __forceinline__ void look(int p, int l) {
         base = p;
         id = table[min(p + l, upto - 1)];
@@ -778,13 +780,10 @@ struct Pages {
 // One wave walks pages from .. upto - 1 by itself: the next page's keys are
 // loaded while this one is weighed, its values while its keys are multiplied.
 // 8 such waves keep up to 128 KB of loads in flight in a CU; bare loads of the
-// same order read 6.2 TB/s, this loop 4.2.
-template <int KIND, int NP, int NT>
-__device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& A, const Place& P, const Tile& T, int from,
-                                           int upto, int r0, int l) {
-    Pages<NP> pages(A, P, T, from, upto, l);
-    const int ctx = T.R.first + T.R.n;                             // slots from here on hold no token
-    w.load(A, seg_of(P, T), T.R.first + T.i0, r0, l);
+// same order read 6.2 TB/s, this loop 4.2.  w's rows are on their way; slots of
+// positions from ctx on hold no token.
+template <int KIND, int NP, int NT, typename P>
+__device__ __forceinline__ void walk_pages(Rows<KIND, NP, NT>& w, P& pages, const Attend& A, int ctx, int from, int upto, int l) {
     uint4 kf[4 * NP], vf[4 * NP];
     auto load = [&](uint4 (&f)[4 * NP], __amdgpu_buffer_rsrc_t r) {
 #pragma unroll
@@ -798,7 +797,7 @@ __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& 
         const int page = pages.at(p);
         load(vf, pages.values(p));
         __builtin_amdgcn_sched_barrier(0);                          // before the first product
-        const int base_key = (T.pg0 + p) * kKvPage;
+        const int base_key = pages.base_key(p);
         const bool clean = KIND == PROX_KV_FP8 && base_key + kKvPage > ctx;
         f32x4_t sc[NT][4];
         float fac[NT], less[NT], back[NT];
@@ -820,6 +819,14 @@ __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& 
         });
     }
     w.finish();
+}
+
+template <int KIND, int NP, int NT>
+__device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& A, const Place& P, const Tile& T, int from,
+                                           int upto, int r0, int l) {
+    Pages<NP> pages(A, P, T, from, upto, l);
+    w.load(A, seg_of(P, T), T.R.first + T.i0, r0, l);
+    walk_pages<KIND, NP, NT>(w, pages, A, T.R.first + T.R.n, from, upto, l);
 }
 
 // The waves of a block walk the same pages, each for its own rows.  A page is

@@ -490,6 +490,24 @@ prox_status prox_kv_select(const prox_kv_cache* c, const prox_kv_batch* b, const
                            int32_t n_heads, const void* bounds, int32_t n_keep, int32_t first, int32_t last,
                            int32_t* pages, void* stream);
 
+/* Workspace bytes of prox_kv_attention_selected for a batch of n_tokens rows; 0 if
+ * the arguments are invalid or more than one call can take. */
+size_t prox_kv_selected_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, int32_t n_heads, int32_t n_keep);
+
+/* prox_kv_attention over the pages that prox_kv_select lists (or any other list of
+ * that form), without a window: a row sees the positions up to its own of the
+ * pages that its list for the key head names.  A list ends before the first entry
+ * that is not above the one before it (so at -1), or is above position / 64; a page
+ * that the table does not name is not seen; a row that sees nothing is written as
+ * zeros.  With every page listed the result is that
+ * of prox_kv_attention, within its rounding.
+ *   pages  device int32 [n_tokens][n_kv][n_keep], 1 <= n_keep <= 2^20
+ * The other arguments as prox_kv_attention's; the workspace is
+ * prox_kv_selected_workspace_bytes(). */
+prox_status prox_kv_attention_selected(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
+                                       int32_t n_heads, const int32_t* pages, int32_t n_keep, float scale, void* out,
+                                       int64_t out_stride, void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- Measurement helper (not part of the forward) ---------------------------
  * Read-stream probe: reads the first bytes / 16 * 16 bytes of the device
  * buffer `buf` (16-byte aligned) with `blocks` blocks of 512 threads, each

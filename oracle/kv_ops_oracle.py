@@ -131,18 +131,20 @@ class _Part:
 
 
 def attention_selected(cache, table, ctx, q_start, max_q, q, pages, scale):
-    """(out, tol) as kv_oracle.attention, of rows that see the listed pages alone: an
-    entry counts where it is above the one before it, names a page of the row's
-    sequence and is not behind the row's own."""
+    """(out, tol) as kv_oracle.attention, of rows that see the listed pages alone: a
+    list ends before the first entry that is not above the one before it, or is
+    behind the row's own page."""
     T, H, hd = q.shape
     rep = H // cache.n_kv
     out, tol = np.full((T, H, hd), np.nan), np.zeros((T, H, hd))
     for s, row, pos in KO.rows_of(q_start, ctx, T, max_q):
         for g in range(cache.n_kv):
             heads = slice(g * rep, (g + 1) * rep)
-            lst = pages[row, g]
-            ok = [int(p) for i, p in enumerate(lst)
-                  if p >= 0 and (i == 0 or p > lst[i - 1]) and pos >= 0 and p <= pos // PAGE and pos < PAGE * table.shape[1]]
+            ok = []
+            for p in pages[row, g] if 0 <= pos < PAGE * table.shape[1] else ():
+                if not (ok[-1] if ok else -1) < p <= pos // PAGE:
+                    break
+                ok.append(int(p))
             if not ok:
                 out[row, heads] = 0
                 continue

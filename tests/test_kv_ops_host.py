@@ -34,6 +34,11 @@ def select(c=None, b=None, q=FAKE, qs=512, H=4, bnd=FAKE, keep=4, first=1, last=
                                out, None)
 
 
+def selected(c=None, b=None, q=FAKE, qs=512, H=4, lst=FAKE, keep=4, scale=0.1, out=2 * FAKE, os=512, ws=FAKE, n=1 << 40):
+    return _lib.prox_kv_attention_selected(ctypes.byref(c or cache()), ctypes.byref(b or batch()), q, qs, H, lst, keep,
+                                           scale, out, os, ws, n, None)
+
+
 def test_pool_refusals():
     for over, want in ((dict(n_pages=0), INVALID), (dict(n_seq=0), INVALID), (dict(max_pages=0), INVALID),
                        (dict(n_pages=(1 << 24) + 1), UNSUPPORTED), (dict(n_seq=(1 << 24) + 1), UNSUPPORTED),
@@ -48,7 +53,7 @@ def test_pool_refusals():
     assert need > 0 and pages(n=need - 1) == WORKSPACE
 
 
-@pytest.mark.parametrize("call", [bounds, select])
+@pytest.mark.parametrize("call", [bounds, select, selected])
 def test_cache_and_batch_refusals(call):
     for over, want in ((dict(kind=0), INVALID), (dict(n_pages=0), INVALID), (dict(n_kv=1025), UNSUPPORTED),
                        (dict(head_dim=132), INVALID), (dict(head_pad=64), MISMATCH), (dict(k=0), INVALID)):
@@ -69,6 +74,24 @@ def test_bounds_and_select_refusals():
     assert select(first=-1) == INVALID and select(last=0) == INVALID and select(keep=4, first=3, last=2) == INVALID
     assert select(first=0x7fffffff, last=0x7fffffff) == INVALID
     assert select(b=batch(max_pages=32769)) == UNSUPPORTED
+
+
+def test_selected_refusals():
+    assert selected(q=0) == INVALID and selected(out=0) == INVALID and selected(out=FAKE) == INVALID
+    assert selected(H=5) == INVALID and selected(H=1026) == UNSUPPORTED
+    assert selected(qs=511) == INVALID and selected(os=500) == INVALID
+    assert selected(lst=0) == INVALID and selected(lst=FAKE + 2) == INVALID
+    assert selected(keep=0) == INVALID and selected(keep=(1 << 20) + 1) == UNSUPPORTED
+    assert selected(scale=float("inf")) == INVALID and selected(scale=float("nan")) == INVALID
+    assert selected(ws=0) == INVALID and selected(ws=FAKE + 16) == INVALID
+    for keep in (1, 64, 5000):
+        b = batch()
+        need = _lib.prox_kv_selected_workspace_bytes(ctypes.byref(cache()), ctypes.byref(b), 4, keep)
+        assert need > 0 and selected(keep=keep, n=need - 1) == WORKSPACE
+    big = batch(n_tokens=1 << 28, max_q=1 << 28)
+    c = cache(n_kv=64)
+    assert _lib.prox_kv_selected_workspace_bytes(ctypes.byref(c), ctypes.byref(big), 64, 4) == 0
+    assert selected(c=c, b=big, H=64, qs=64 * 128, os=64 * 128) == UNSUPPORTED
 
 
 def test_python_handles_refuse_host_tensors_and_shapes():
