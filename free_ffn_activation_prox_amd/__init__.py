@@ -125,6 +125,9 @@ def _load() -> ctypes.CDLL:
         "prox_kv_selected_workspace_bytes": (SZ, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), I32, I32]),
         "prox_kv_attention_selected": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, P, I32,
                                              ctypes.c_float, P, I64, P, SZ, P]),
+        "prox_kv_shared_workspace_bytes": (SZ, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), I32, I32]),
+        "prox_kv_attention_shared": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I32, P, P, I64, I32,
+                                           ctypes.c_float, P, I64, P, SZ, P]),
         "prox_status_str": (ctypes.c_char_p, [I32]),
         "prox_last_error": (ctypes.c_char_p, []),
     }
@@ -845,7 +848,48 @@ def kv_attention_selected(q, cache: KVCache, batch: KVBatch, pages, *, scale: Op
     return out
 
 
-__all__ = ["alloc_kv_selected_workspace", "kv_attention_selected", "KVPool", "kv_pages", "alloc_kv_bounds", "kv_page_bounds", "kv_select",
+def alloc_kv_shared_workspace(cache: KVCache, batch: KVBatch, n_heads: int, n_groups: int = 1):
+    """Workspace of kv_attention_shared for batches of this shape (n_seq, n_tokens, max_q, max_pages)."""
+    with torch.cuda.device(cache.device):
+        n = _lib.prox_kv_shared_workspace_bytes(cache._ref, batch._ref, n_heads, n_groups)
+    return _alloc_scratch(cache, n)
+
+
+def kv_attention_shared(q, cache: KVCache, batch: KVBatch, shared, *, group_start=None, scale: Optional[float] = None,
+                        out=None, workspace=None, stream=None):
+    """kv_attention for sequences that share their first pages, which are then read
+    once for all rows of a group.  Group g is the sequences group_start[g] ..
+    group_start[g + 1] - 1 (int32 [n_groups + 1]; None: one group of all); the
+    first shared[g] (int32 [n_groups]) pages of its sequences are those of its first
+    one.  A sequence whose first row lies before the end of these pages counts as
+    sharing none.  Returns out; rows that see nothing are zeros, rows outside every
+    sequence are left as they were."""
+    dev, hd, n = cache.device, cache.head_dim, batch.n_tokens
+    if batch.device != dev:
+        raise ValueError("cache and batch are on different devices")
+    qs = _kv_rows("q", q, n, None, hd, dev)
+    n_heads = q.shape[1]
+    if shared.dim() != 1 or shared.shape[0] > batch.n_seq:
+        raise ValueError("shared must be [n_groups], at most a group for each sequence")
+    groups = int(shared.shape[0])
+    gp, hp = _ints("group_start", group_start, (groups + 1,), dev), _ints("shared", shared, (groups,), dev)
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = alloc_kv_shared_workspace(cache, batch, n_heads, groups)
+    os_ = _kv_rows("out", out, n, n_heads, hd, dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
+    sp, here = _on(stream, dev)
+    _kv_call(_lib.prox_kv_attention_shared, "prox_kv_attention_shared", dev, here, cache._ref, batch._ref, gp, groups, hp,
+             q.data_ptr(), qs, n_heads, hd ** -0.5 if scale is None else scale, out.data_ptr(), os_, workspace.data_ptr(),
+             workspace.nbytes, sp)
+    _held_for(stream, cache, batch, q, out, workspace, shared, group_start)
+    return out
+
+
+__all__ = ["alloc_kv_shared_workspace", "kv_attention_shared", "alloc_kv_selected_workspace", "kv_attention_selected", "KVPool", "kv_pages", "alloc_kv_bounds", "kv_page_bounds", "kv_select",
            "KVCache", "KVBatch", "KV_KINDS", "KV_PAGE", "kv_head_pad", "kv_append", "kv_attention", "kv_read",
            "kv_workspace_bytes", "alloc_kv_workspace",
            "QWeights", "build_qweights", "qweights_bytes", "quality", "timeline_forward", "read_probe", "noalloc_scratch_bytes", "ffn_forward_noalloc", "Weights", "Proxy", "ProxError", "abi_version", "library_sha256", "proxy_bytes", "workspace_bytes",

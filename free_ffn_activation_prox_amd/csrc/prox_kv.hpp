@@ -189,5 +189,9 @@ size_t kv_selected_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int
 hipError_t launch_kv_selected(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride, int n_heads,
                               const int32_t* pages, int keep, float scale, uint16_t* out, int64_t out_stride,
                               void* workspace, hipStream_t s);
+size_t kv_shared_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int n_groups);
+hipError_t launch_kv_shared(const prox_kv_cache& c, const prox_kv_batch& b, const int32_t* group_start, int n_groups,
+                            const int32_t* shared, const uint16_t* q, int64_t q_stride, int n_heads, float scale,
+                            uint16_t* out, int64_t out_stride, void* workspace, hipStream_t s);
 
 }  // namespace prox

@@ -267,3 +267,46 @@ extern "C" prox_status prox_kv_attention_selected(const prox_kv_cache* c, const 
                                        static_cast<uint16_t*>(out), out_stride, workspace, (hipStream_t)stream),
                     "attention over selected pages");
 }
+
+static prox_status check_groups(const prox_kv_batch* b, int32_t n_groups) {
+    if (n_groups < 1 || n_groups > b->n_seq) return fail(PROX_E_INVALID, "n_groups must be 1 .. n_seq");
+    return PROX_OK;
+}
+
+extern "C" size_t prox_kv_shared_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, int32_t n_heads,
+                                                 int32_t n_groups) {
+    clear_error();
+    if (check_cache(c) != PROX_OK || check_batch(b) != PROX_OK || check_heads(c, n_heads) != PROX_OK ||
+        check_groups(b, n_groups) != PROX_OK)
+        return 0;
+    return kv_shared_workspace(*c, *b, n_heads, n_groups);
+}
+
+extern "C" prox_status prox_kv_attention_shared(const prox_kv_cache* c, const prox_kv_batch* b, const int32_t* group_start,
+                                                int32_t n_groups, const int32_t* shared, const void* q, int64_t q_stride,
+                                                int32_t n_heads, float scale, void* out, int64_t out_stride,
+                                                void* workspace, size_t ws_bytes, void* stream) {
+    clear_error();
+    PROX_CHECK(check_cache(c));
+    PROX_CHECK(check_batch(b));
+    PROX_CHECK(check_heads(c, n_heads));
+    PROX_CHECK(check_groups(b, n_groups));
+    if (!group_start && n_groups != 1) return fail(PROX_E_INVALID, "without group_start there is one group");
+    if (!shared) return fail(PROX_E_INVALID, "null shared");
+    if (!aligned(group_start, 4) || !aligned(shared, 4)) return fail(PROX_E_INVALID, "misaligned group_start or shared");
+    if (!(scale > -3.0e38f && scale < 3.0e38f)) return fail(PROX_E_INVALID, "scale must be finite");
+    if (b->n_tokens == 0 || b->max_q == 0) return PROX_OK;
+    const int64_t width = (int64_t)n_heads * c->head_dim;
+    PROX_CHECK(check_rows("q", q, q_stride, width));
+    PROX_CHECK(check_rows("out", out, out_stride, width));
+    if (q == out) return fail(PROX_E_INVALID, "out must not be q");
+    if (!workspace) return fail(PROX_E_INVALID, "null workspace");
+    if (!aligned(workspace, 256)) return fail(PROX_E_INVALID, "workspace must be 256-byte aligned");
+    const size_t need = kv_shared_workspace(*c, *b, n_heads, n_groups);
+    if (need == 0) return launched(hipErrorInvalidConfiguration, "attention with a shared prefix");
+    if (ws_bytes < need) return fail(PROX_E_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    return launched(launch_kv_shared(*c, *b, group_start, n_groups, shared, static_cast<const uint16_t*>(q), q_stride,
+                                     n_heads, scale, static_cast<uint16_t*>(out), out_stride, workspace,
+                                     (hipStream_t)stream),
+                    "attention with a shared prefix");
+}

@@ -17,35 +17,14 @@ hipError_t launch_kv_attention(const prox_kv_cache& c, const prox_kv_batch& batc
     const Launches L(c, b, n_heads);
     if (!L.fit()) return hipErrorInvalidConfiguration;
     Attend A{};
-    A.c = c;
-    A.b = b;
-    A.q = q;
-    A.out = out;
-    A.qs = q_stride;
-    A.os = out_stride;
+    set_call(A, c, b, q, q_stride, n_heads, scale, window, out, out_stride);
     A.arrived = static_cast<unsigned long long*>(workspace);
-    A.rep = n_heads / c.n_kv;
-    A.window = window;
-    A.scale2 = fabsf(scale) * 1.4426950408889634f;
-    A.sign = scale < 0.f ? -1.f : 1.f;
     for (int k = L.few > 0 ? 0 : 1; k < 2; ++k) {
         const Split& p = L.split[k];
         A.rows_lo = k == 0 ? 1 : L.few + 1;
         A.rows_hi = k == 0 ? L.few : b.max_q;
         A.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_at);
-        A.part_bytes = (uint32_t)p.part_bytes;
-        A.tag = next_call_tag();
-        A.HG = p.HG;
-        A.HG_inv = (131072u + (uint32_t)p.HG - 1) / (uint32_t)p.HG;
-        A.VH = p.VH;
-        A.TQ = p.TQ;
-        A.tiles = p.tiles;
-        A.all_tiles = (int)p.all_tiles;
-        A.slot_rows = p.slot_rows;
-        A.seg_cost = p.seg_cost;
-        A.no_cut = p.no_cut;
-        A.min_part = p.min_part;
-        A.min_piece = p.min_piece;
+        set_split(A, p);
         const hipError_t e = c.kind == PROX_KV_INT8 ? attend_kind<PROX_KV_INT8>(A, p, s) : attend_kind<PROX_KV_FP8>(A, p, s);
         if (e != hipSuccess) return e;
     }

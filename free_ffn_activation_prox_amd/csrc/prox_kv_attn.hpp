@@ -143,6 +143,8 @@ __device__ __forceinline__ float over_groups_max(float v) {
 }
 
 struct Attend {
+    typedef KvRows Row;
+    typedef uint16_t* Out;
     prox_kv_cache c;
     prox_kv_batch b;
     const uint16_t* q;
@@ -165,6 +167,10 @@ struct Attend {
     float sign;            // that of scale
 };
 
+// What follows up to `Place` is that of a call over the sequences' own pages.  A
+// call of another kind has a type of its own derived from Attend, with its own
+// Row and Out, and overloads of what its needs differ in: these and out_row(), put().
+//
 // The rows of sequence s, none if the launch does not take it.
 __device__ __forceinline__ KvRows rows_of(const Attend& A, int s) {
     KvRows R = kv_rows(A.b, s);
@@ -172,12 +178,28 @@ __device__ __forceinline__ KvRows rows_of(const Attend& A, int s) {
     return R;
 }
 
+// Work that a launch does besides, before the attention.
+__device__ __forceinline__ void prologue(const Attend&, int, int) {}
+
+__device__ __forceinline__ KvRows no_rows(const Attend&) { return KvRows{0, 0, 0, 0}; }
+// A lane's rows from lane i; those of lane `on`, the same for the whole wave.
+__device__ __forceinline__ KvRows shuffled(const KvRows& R, int i) {
+    return KvRows{__shfl(R.q0, i), __shfl(R.n, i), __shfl(R.rows, i), __shfl(R.first, i)};
+}
+__device__ __forceinline__ KvRows of_lane(const KvRows& R, int on) {
+    return KvRows{__builtin_amdgcn_readlane(R.q0, on), __builtin_amdgcn_readlane(R.n, on),
+                  __builtin_amdgcn_readlane(R.rows, on), __builtin_amdgcn_readlane(R.first, on)};
+}
+
 // One tile of tokens of one sequence.
-struct Tile {
-    KvRows R;
+template <typename Row>
+struct TileOf {
+    Row R;
     int i0, n;             // tokens i0 .. i0 + n - 1 of the sequence's rows
     int pg0, pages;        // pages that some row sees: pg0 .. pg0 + pages - 1; at least one (0: no such tile)
 };
+
+typedef TileOf<KvRows> Tile;
 
 __device__ __forceinline__ Tile tile_of(const Attend& A, const KvRows& R, int t) {
     Tile x;
@@ -192,6 +214,12 @@ __device__ __forceinline__ Tile tile_of(const Attend& A, const KvRows& R, int t)
     x.pages = x.n <= 0 ? 0 : some ? (hi - 1) / kKvPage + 1 - x.pg0 : 1;
     return x;
 }
+
+// The table's row of (the launch's) sequence s; the slots of positions from
+// ctx_of() on hold no token; whether rows see only what their position allows.
+__device__ __forceinline__ const int32_t* table_of(const Attend& A, int s) { return A.b.block_table + (size_t)s * A.b.max_pages; }
+__device__ __forceinline__ int ctx_of(const Attend&, const Tile& T) { return T.R.first + T.R.n; }
+__device__ __forceinline__ constexpr bool masked(const Attend&) { return true; }
 
 // A segment: key head and head group vh of tile t of sequence s, and the unit
 // of the line that it begins at.
@@ -217,17 +245,20 @@ __device__ __forceinline__ void blocks_of(const Attend& A, int piece, int begin,
 // It looks at 64 tiles at a time, those that there are of 64 sequences: with
 // one prompt among 255 single tokens these are 5 looks, where max_q alone would
 // allow 64 tiles for each sequence (256 looks).
+template <typename AT>
 struct Line {
-    const Attend& A;
+    typedef typename AT::Row Row;
+    typedef TileOf<Row> Tile;
+    const AT& A;
     int l, total, looks;   // lane; units; looks that the line takes
     struct Look {
         int s0, j0, base;  // first sequence; first of its chunk's tiles; units before it
         int before;        // tiles before the chunk
     };
     Look from;             // at() begins here
-    KvRows Q;              // lane: sequence s0 + lane,
+    Row Q;                 // lane: sequence s0 + lane,
     int last, tiles;       // the chunk's tiles up to its end, and all of them
-    KvRows R;              // lane: a tile's sequence,
+    Row R;                 // lane: a tile's sequence,
     int s, t, pages, upto; // its number, the tile, its pages, and the units up to its end
 
     static __device__ __forceinline__ int sum_up(int v, int l) {
@@ -239,7 +270,7 @@ struct Line {
         return v;
     }
     __device__ __forceinline__ void chunk(int s0, int before) {
-        Q = s0 + l < A.b.n_seq ? rows_of(A, s0 + l) : KvRows{0, 0, 0, 0};
+        Q = s0 + l < A.b.n_seq ? rows_of(A, s0 + l) : no_rows(A);
         if (A.tiles > 1) {
             last = sum_up((int)((uint32_t)(Q.rows + A.TQ - 1) / (uint32_t)A.TQ), l);
             tiles = min(__builtin_amdgcn_readlane(last, 63), A.all_tiles - before);
@@ -260,7 +291,7 @@ struct Line {
                 if (__shfl(last, i + m - 1) <= j) i += m;
             const int before = __shfl(last, i > 0 ? i - 1 : 0);
             t = j - (i > 0 ? before : 0);
-            R = KvRows{__shfl(Q.q0, i), __shfl(Q.n, i), __shfl(Q.rows, i), __shfl(Q.first, i)};
+            R = shuffled(Q, i);
             if (j >= tiles) R.rows = 0;
         }
         s = k.s0 + i;
@@ -284,7 +315,7 @@ struct Line {
             k.base = end;
         }
     }
-    __device__ __forceinline__ Line(const Attend& a, int lane) : A(a), l(lane), looks(0), from{0, 0, 0, 0} {
+    __device__ __forceinline__ Line(const AT& a, int lane) : A(a), l(lane), looks(0), from{0, 0, 0, 0} {
         total = scan(from, 0x7fffffff).base;
     }
     // x < total; keep: no later call asks for a unit of an earlier look
@@ -301,18 +332,18 @@ struct Line {
         const int len = p.pages + A.seg_cost, first = __builtin_amdgcn_readlane(upto, on) - len * A.VH;
         p.vh = (int)((uint32_t)(x - first) / (uint32_t)len);
         p.begin = first + p.vh * len;
-        T = tile_of(A, KvRows{__builtin_amdgcn_readlane(R.q0, on), __builtin_amdgcn_readlane(R.n, on),
-                              __builtin_amdgcn_readlane(R.rows, on), __builtin_amdgcn_readlane(R.first, on)}, p.t);
+        T = tile_of(A, of_lane(R, on), p.t);
         return p;
     }
 };
 
 // The segment after p, where there is one.
-__device__ __forceinline__ void next_segment(const Attend& A, Place& p, Tile& T) {
+template <typename AT, typename Tile>
+__device__ __forceinline__ void next_segment(const AT& A, Place& p, Tile& T) {
     p.begin += p.pages + A.seg_cost;
     if (++p.vh < A.VH) return;
     p.vh = 0;
-    KvRows R = T.R;
+    auto R = T.R;
     if (++p.t * A.TQ >= R.rows) {
         p.t = 0;
         do R = rows_of(A, ++p.s);
@@ -375,6 +406,7 @@ struct Seg {
     int begin, pages;      // units of the line
     int vh, row0, n;       // key head and head group; rows of the batch row0 .. row0 + n - 1
 };
+template <typename Tile>
 __device__ __forceinline__ Seg seg_of(const Place& P, const Tile& T) {
     return Seg{P.begin, P.pages, P.vh, T.R.q0 + T.i0, T.n};
 }
@@ -388,6 +420,11 @@ __device__ __forceinline__ uint16_t* out_row(const Attend& A, const Seg& S, int 
     const int i = token_of(A, r), hq = grp * A.HG + r - i * A.HG;
     if (i >= S.n || hq >= A.rep) return nullptr;
     return A.out + (int64_t)(S.row0 + i) * A.os + (int64_t)(head * A.rep + hq) * A.c.head_dim;
+}
+
+// Four channels of a row's result go there, from c4 on: o unnormalised, a what goes with it, inv the inverse of its sum.
+__device__ __forceinline__ void put(const Attend& A, uint16_t* to, int c4, f32x4_t o, const Part& a, float inv) {
+    if (c4 < A.c.head_dim) *reinterpret_cast<uint2*>(to + c4) = bf16x4(result(o, inv, a.e));
 }
 
 // The rows r0 .. r0 + 16 NT - 1 of a segment's tile in one wave: what they see,
@@ -404,7 +441,8 @@ struct Rows {
     float row_scale[NT], bias[NT];
 
     // Where the rows are, and their q on its way.
-    __device__ __forceinline__ void load(const Attend& A, const Seg& S, int pos0, int r0, int l) {
+    template <typename AT>
+    __device__ __forceinline__ void load(const AT& A, const Seg& S, int pos0, int r0, int l) {
         const int n = l & 15, g = l >> 4, hd = A.c.head_dim, cap = A.b.max_pages * kKvPage;
         const int groups = A.VH / A.c.n_kv, head = S.vh / groups, grp = S.vh - head * groups;
 #pragma unroll
@@ -414,7 +452,7 @@ struct Rows {
             const int pos = pos0 + i;
             const bool sees = live[u] && pos >= 0 && pos < cap;
             key_lo[u] = sees && A.window > 0 ? pos - A.window + 1 : 0;
-            key_hi[u] = sees ? pos + 1 : (live[u] ? 0 : 0x7fffffff);    // a row that is not there is not masked
+            key_hi[u] = !masked(A) ? 0x7fffffff : sees ? pos + 1 : (live[u] ? 0 : 0x7fffffff);    // a row that is not there is not masked
             const uint16_t* src = A.q + (int64_t)(S.row0 + (live[u] ? i : 0)) * A.qs +
                                   (int64_t)(head * A.rep + (live[u] ? hq : 0)) * hd;
 #pragma unroll
@@ -734,15 +772,16 @@ struct Rows {
 // same in every turn of a loop.  So are the values of a page whose scale is 0.  Lane i keeps what the table and the scales
 // say of page base + i: a turn of a loop reads a lane and waits for no memory
 // (scalar loads would hold up every wait for LDS, which counts them too).
-template <int NP>
+template <int NP, typename AT>
 struct Pages {
     static constexpr int kBytes = kKvPage * 64 * NP;
-    const Attend& A;
+    const AT& A;
     const int32_t* table;
     int head, upto, pg0, base, id, ve;
     float ks, vl;          // K's scale; V's scale 2^(ve + vl - kTop), -1 <= vl - kTop < 0 (0: ve kNoUnit)
-    __device__ __forceinline__ Pages(const Attend& a, const Place& P, const Tile& T, int from, int up, int l)
-        : A(a), table(a.b.block_table + (size_t)P.s * a.b.max_pages + T.pg0), head(P.vh / (a.VH / a.c.n_kv)), upto(up),
+    template <typename Tile>
+    __device__ __forceinline__ Pages(const AT& a, const Place& P, const Tile& T, int from, int up, int l)
+        : A(a), table(table_of(a, P.s) + T.pg0), head(P.vh / (a.VH / a.c.n_kv)), upto(up),
           pg0(T.pg0) {
         look(from, l);
     }
@@ -821,12 +860,12 @@ __device__ __forceinline__ void walk_pages(Rows<KIND, NP, NT>& w, P& pages, cons
     w.finish();
 }
 
-template <int KIND, int NP, int NT>
-__device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& A, const Place& P, const Tile& T, int from,
+template <int KIND, int NP, int NT, typename AT, typename Tile>
+__device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const AT& A, const Place& P, const Tile& T, int from,
                                            int upto, int r0, int l) {
-    Pages<NP> pages(A, P, T, from, upto, l);
+    Pages<NP, AT> pages(A, P, T, from, upto, l);
     w.load(A, seg_of(P, T), T.R.first + T.i0, r0, l);
-    walk_pages<KIND, NP, NT>(w, pages, A, T.R.first + T.R.n, from, upto, l);
+    walk_pages<KIND, NP, NT>(w, pages, A, ctx_of(A, T), from, upto, l);
 }
 
 // The waves of a block walk the same pages, each for its own rows.  A page is
@@ -844,14 +883,14 @@ __device__ __forceinline__ void walk_alone(Rows<KIND, NP, NT>& w, const Attend& 
 // two blocks (244), one tile of 16 rows a wave: 8 waves 299, 12 waves 233, 16
 // waves 271.
 // LDS: keys [2][4 NP x 2 operands][64] uint4, values the same.
-template <int KIND, int NP, int NT, int kWaves>
-__device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds, const Attend& A, const Place& P,
+template <int KIND, int NP, int NT, int kWaves, typename AT, typename Tile>
+__device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds, const AT& A, const Place& P,
                                               const Tile& T, int from, int upto, int wv, int l) {
     constexpr int kChunks = 4 * NP;                                 // kilobytes of codes of K, and of V
     constexpr int kOwn = (kChunks + kWaves - 1) / kWaves;           // a wave's: chunks wv, wv + kWaves, ...
     constexpr int kSize = kChunks * 128;                            // uint4 of a page's operands
-    Pages<NP> pages(A, P, T, from, upto, l);
-    const int ctx = T.R.first + T.R.n;
+    Pages<NP, AT> pages(A, P, T, from, upto, l);
+    const int ctx = ctx_of(A, T);
     const int r0 = 16 * NT * wv;
     const bool busy = r0 < T.n * A.HG;                              // a wave without rows only fills
     w.load(A, seg_of(P, T), T.R.first + T.i0, r0, l);
@@ -927,8 +966,8 @@ __device__ __forceinline__ void walk_together(Rows<KIND, NP, NT>& w, uint4* lds,
 //     LDS: [waves][2][slot_rows][64 NP + 4] floats
 //   ROWS true: a tile of 16 NT rows for each wave; the waves walk the same pages.
 // Rows of cut segments go to the workspace.
-template <int KIND, int NP, int NT, bool ROWS, int kWaves>
-__global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Attend A) {
+template <int KIND, int NP, int NT, bool ROWS, int kWaves, typename AT>
+__global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(AT A) {
     extern __shared__ __align__(16) float lds[];
     __shared__ Seg seg_s[16];                     // segment of each wave's two slots, begin -1: none
     __shared__ Seg cut_s[2];                      // the segments that reach over the piece's begin and over its end
@@ -937,15 +976,15 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
     constexpr int LPR = 16 * NP;                  // lanes of a row, four channels each
     const int l = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), n = l & 15, g = l >> 4;
     const int WV = blockDim.x >> 6;
-    const int hd = A.c.head_dim;
-    Line line(A, l);
+    prologue(A, wv, l);
+    Line<AT> line(A, l);
     const int piece = (int)max((uint32_t)line.total / gridDim.x + 1, (uint32_t)A.min_piece);
     if ((int64_t)blockIdx.x * piece >= line.total) return;
     // where the piece begins and ends, and the place of this wave's first unit:
     // one turn each of a loop that stays a loop (code that runs once is fetched once)
     int b0 = 0, b1 = 0, x = 0, end = 0;
     Place P;
-    Tile T;
+    TileOf<typename AT::Row> T;
 #pragma nounroll
     for (int k = 0; k < 3; ++k) {
         int64_t at = k < 2 ? ((int64_t)blockIdx.x + k) * piece : x;
@@ -986,12 +1025,11 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                 for (int u = 0; u < NT; ++u) {
                     const int r = r0 + 16 * u + n;
                     if (from == 0 && upto == P.pages) {
-                        uint16_t* to = w.live[u] ? out_row(A, seg_of(P, T), r) : nullptr;
+                        const typename AT::Out to = w.live[u] ? out_row(A, seg_of(P, T), r) : typename AT::Out();
                         const float inv = inverse(w.sum[u]);
                         if (to)
 #pragma unroll
-                            for (int d = 0; d < 4 * NP; ++d)
-                                if (16 * d + 4 * g < hd) *reinterpret_cast<uint2*>(to + 16 * d + 4 * g) = bf16x4(result(w.o[u][d], inv, (float)w.e[u]));
+                            for (int d = 0; d < 4 * NP; ++d) put(A, to, 16 * d + 4 * g, w.o[u][d], w.part(u), inv);
                     } else if (!ROWS) {
                         const int slot = 2 * wv + (from == 0 ? 1 : 0);
                         if (l == 0) seg_s[slot] = seg_of(P, T);
@@ -1055,8 +1093,8 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
                         if ((same >> (k0 + u)) & 1) join(a, o, unpacked(ms[u]), v[u]);
                 }
                 if (whole) {
-                    uint16_t* to = out_row(A, S, r);
-                    if (to && c4 < hd) *reinterpret_cast<uint2*>(to + c4) = bf16x4(result(o, inverse(a.sum), a.e));
+                    const typename AT::Out to = out_row(A, S, r);
+                    if (to) put(A, to, c4, o, a, inverse(a.sum));
                 } else {
                     const uint32_t at = part_at(blockIdx.x, S.begin >= b0, r);
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), rp, (int)(at + 4 * c4), 0, kCoherent);
@@ -1105,9 +1143,8 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(Atte
             join(a, o, unpacked(__builtin_bit_cast(float4, ms)), __builtin_bit_cast(f32x4_t, v));
         };
         auto store = [&](int e, f32x4_t o, const Part& a) {
-            uint16_t* to = out_row(A, S, e / LPR);
-            if (to && 4 * (e % LPR) < hd)
-                *reinterpret_cast<uint2*>(to + 4 * (e % LPR)) = bf16x4(result(o, inverse(a.sum), a.e));
+            const typename AT::Out to = out_row(A, S, e / LPR);
+            if (to) put(A, to, 4 * (e % LPR), o, a, inverse(a.sum));
         };
         if (2 * lanes > bd) {
             // many rows and few parts: a thread joins four (row, four channels) at once
@@ -1187,7 +1224,7 @@ constexpr int kRowWaves = 8;
 int64_t times(int64_t a, int64_t b) { return a > 0 && b > (1ll << 62) / a ? (1ll << 62) + 1 : a * b; }
 
 // For n_tokens rows in sequences of up to max_q tokens.
-Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int64_t n_tokens, int max_q) {
+[[maybe_unused]] Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int64_t n_tokens, int max_q) {
     Split p;
     const int rep = n_heads / c.n_kv, NP = c.head_pad / 64;
     const int64_t most_rows = (int64_t)max_q * rep;
@@ -1261,27 +1298,27 @@ int short_tokens(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
     return mixed && (int64_t)b.n_seq * c.n_kv >= device_cus() ? few : 0;
 }
 
-template <int KIND, int NP, int NT, bool ROWS, int kWaves>
-hipError_t attend_launch(const Attend& A, const Split& p, hipStream_t s) {
+template <int KIND, int NP, int NT, bool ROWS, int kWaves, typename AT>
+hipError_t attend_launch(const AT& A, const Split& p, hipStream_t s) {
     if (p.lds > 48 * 1024) {
-        const hipError_t e = hipFuncSetAttribute((const void*)k_kv_attend<KIND, NP, NT, ROWS, kWaves>,
+        const hipError_t e = hipFuncSetAttribute((const void*)k_kv_attend<KIND, NP, NT, ROWS, kWaves, AT>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((k_kv_attend<KIND, NP, NT, ROWS, kWaves>), dim3((uint32_t)p.blocks), dim3(64 * p.waves), p.lds, s, A);
+    hipLaunchKernelGGL((k_kv_attend<KIND, NP, NT, ROWS, kWaves, AT>), dim3((uint32_t)p.blocks), dim3(64 * p.waves), p.lds, s, A);
     return hipGetLastError();
 }
 
-template <int KIND, int NP>
-hipError_t attend_np(const Attend& A, const Split& p, hipStream_t s) {
+template <int KIND, int NP, typename AT>
+hipError_t attend_np(const AT& A, const Split& p, hipStream_t s) {
     if (!p.rows) return attend_launch<KIND, NP, 1, false, few_waves(NP)>(A, p, s);
     if constexpr (NP <= 2)
         if (p.NT == 2) return attend_launch<KIND, NP, 2, true, kRowWaves>(A, p, s);
     return attend_launch<KIND, NP, 1, true, kRowWaves>(A, p, s);
 }
 
-template <int KIND>
-hipError_t attend_kind(const Attend& A, const Split& p, hipStream_t s) {
+template <int KIND, typename AT>
+hipError_t attend_kind(const AT& A, const Split& p, hipStream_t s) {
     switch (A.c.head_pad / 64) {
         case 1: return attend_np<KIND, 1>(A, p, s);
         case 2: return attend_np<KIND, 2>(A, p, s);
@@ -1315,6 +1352,36 @@ prox_kv_batch bounded(const prox_kv_batch& b) {
     prox_kv_batch r = b;
     r.max_q = std::max(std::min(b.max_q, b.n_tokens), 1);
     return r;
+}
+
+// What a call and what its split give the kernel.
+void set_call(Attend& A, const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride, int n_heads,
+              float scale, int window, uint16_t* out, int64_t out_stride) {
+    A.c = c;
+    A.b = b;
+    A.q = q;
+    A.out = out;
+    A.qs = q_stride;
+    A.os = out_stride;
+    A.rep = n_heads / c.n_kv;
+    A.window = window;
+    A.scale2 = fabsf(scale) * 1.4426950408889634f;
+    A.sign = scale < 0.f ? -1.f : 1.f;
+}
+void set_split(Attend& A, const Split& p) {
+    A.part_bytes = (uint32_t)p.part_bytes;
+    A.tag = next_call_tag();
+    A.HG = p.HG;
+    A.HG_inv = (131072u + (uint32_t)p.HG - 1) / (uint32_t)p.HG;
+    A.VH = p.VH;
+    A.TQ = p.TQ;
+    A.tiles = p.tiles;
+    A.all_tiles = (int)p.all_tiles;
+    A.slot_rows = p.slot_rows;
+    A.seg_cost = p.seg_cost;
+    A.no_cut = p.no_cut;
+    A.min_part = p.min_part;
+    A.min_piece = p.min_piece;
 }
 
 }  // namespace

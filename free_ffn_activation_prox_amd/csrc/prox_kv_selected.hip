@@ -236,21 +236,13 @@ hipError_t launch_kv_selected(const prox_kv_cache& c, const prox_kv_batch& b, co
     if (!p.fits) return hipErrorInvalidConfiguration;
     Selected S{};
     Attend& A = S.A;
-    A.c = c;
-    A.b = b;
-    A.q = q;
-    A.out = out;
-    A.qs = q_stride;
-    A.os = out_stride;
+    set_call(A, c, b, q, q_stride, n_heads, scale, 0, out, out_stride);
     A.arrived = static_cast<unsigned long long*>(workspace);
     A.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_at);
     A.part_bytes = (uint32_t)p.part_bytes;
     A.tag = next_call_tag();
-    A.rep = n_heads / c.n_kv;
     A.HG = p.HG;
     A.VH = p.VH;
-    A.scale2 = fabsf(scale) * 1.4426950408889634f;
-    A.sign = scale < 0.f ? -1.f : 1.f;
     S.pages = pages;
     S.keep = keep;
     S.parts = p.parts;

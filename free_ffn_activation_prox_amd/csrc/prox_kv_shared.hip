@@ -1,0 +1,221 @@
+// Attention over the paged key/value cache for sequences that share a prefix.
+//
+// A softmax over two sets of positions is put together from the two sets' own
+// maxima, sums and results.  So a call is two launches of the attention's kernel:
+//   1  the rows of all sequences of a group, as those of one sequence, over the
+//      group's shared pages, without a mask; what comes out is each row's
+//      maximum, sum, unit and unnormalised result, in fp32, in the workspace;
+//   2  the rows of each sequence over its other pages, causal; a row's part of 1
+//      joins before it is normalised and rounded.
+// A page of a prefix is read once for up to 256 rows (32 of each of 8 waves)
+// instead of once for each sequence.  A sequence whose first row lies inside the
+// prefix takes no part in it: launch 2 goes over all of its pages.
+#include "prox_kv_attn.hpp"
+
+namespace prox {
+
+namespace {
+
+struct GroupArgs {
+    const int32_t *group_start, *shared;
+    int n_groups, n_seq;
+    int n_heads;
+    float* row_part;           // [n_tokens][n_heads][head_pad + 4]
+    int32_t* skip;             // [n_seq]: pages of a sequence that are taken from its group
+    int32_t* joins;            // [n_tokens]: whether the row takes its part of the prefix
+};
+
+__device__ __forceinline__ int group_at(const GroupArgs& G, int g) {
+    return G.group_start ? min(max(G.group_start[g], 0), G.n_seq) : (g == 0 ? 0 : G.n_seq);
+}
+__device__ __forceinline__ int shared_pages(const GroupArgs& G, const prox_kv_batch& b, int g) {
+    return min(max(G.shared[g], 0), b.max_pages);
+}
+__device__ __forceinline__ size_t row_part_at(const Attend& A, const GroupArgs& G, int row, int head) {
+    return ((size_t)row * G.n_heads + head) * (size_t)(A.c.head_pad + 4);
+}
+
+// Row of the batch and query head of row r of a segment; row -1 for one that the segment does not have.
+struct RowHead {
+    int row, head;
+};
+__device__ __forceinline__ RowHead row_head(const Attend& A, const Seg& S, int r) {
+    const int groups = A.VH / A.c.n_kv, head = S.vh / groups, grp = S.vh - head * groups;
+    const int i = token_of(A, r), hq = grp * A.HG + r - i * A.HG;
+    return RowHead{i >= S.n || hq >= A.rep ? -1 : S.row0 + i, head * A.rep + hq};
+}
+
+// ---- launch 1: "sequence" s is group s, A.b.n_seq their number; a group's Row has
+// the number of its shared pages as `first`.
+struct AttendPrefix : Attend {
+    typedef float* Out;
+    GroupArgs G;
+};
+
+// Which sequences and rows take part, for launch 2.
+__device__ __forceinline__ void prologue(const AttendPrefix& A, int wv, int l) {
+    const GroupArgs& G = A.G;
+    for (int s = blockIdx.x * (int)(blockDim.x >> 6) + wv; s < G.n_seq; s += gridDim.x * (int)(blockDim.x >> 6)) {
+        int g = 0;
+        if (G.group_start) {
+            int upto = 0;                                        // groups that begin at s or before
+            for (int base = 0; base < G.n_groups; base += 64)
+                upto += __popcll(__ballot(base + l < G.n_groups && G.group_start[min(base + l, G.n_groups - 1)] <= s));
+            g = max(upto - 1, 0);
+        }
+        const KvRows R = kv_rows(A.b, s);
+        int pages = s >= group_at(G, g) && s < group_at(G, g + 1) ? shared_pages(G, A.b, g) : 0;
+        if (R.first < pages * kKvPage) pages = 0;
+        if (l == 0) G.skip[s] = pages;
+        const int cap = A.b.max_pages * kKvPage;
+        for (int i = l; i < R.n; i += 64) G.joins[R.q0 + i] = pages > 0 && R.first + i < cap;
+    }
+}
+__device__ __forceinline__ KvRows rows_of(const AttendPrefix& A, int g) {
+    const int s0 = group_at(A.G, g), s1 = max(group_at(A.G, g + 1), s0);
+    KvRows R;
+    R.q0 = A.b.q_start ? min(max(A.b.q_start[s0], 0), A.b.n_tokens) : s0;
+    R.n = (A.b.q_start ? min(max(A.b.q_start[s1], R.q0), A.b.n_tokens) : s1) - R.q0;
+    R.first = shared_pages(A.G, A.b, g);
+    R.rows = R.first > 0 ? R.n : 0;
+    return R;
+}
+__device__ __forceinline__ Tile tile_of(const AttendPrefix& A, const KvRows& R, int t) {
+    Tile x;
+    x.R = R;
+    x.i0 = t * A.TQ;
+    x.n = min(R.rows - x.i0, A.TQ);
+    x.pg0 = 0;
+    x.pages = x.n > 0 ? R.first : 0;
+    return x;
+}
+__device__ __forceinline__ const int32_t* table_of(const AttendPrefix& A, int g) {
+    return A.b.block_table + (size_t)min(group_at(A.G, g), A.G.n_seq - 1) * A.b.max_pages;
+}
+__device__ __forceinline__ int ctx_of(const AttendPrefix&, const Tile&) { return 0; }   // any slot may hold no token
+__device__ __forceinline__ constexpr bool masked(const AttendPrefix&) { return false; }
+__device__ __forceinline__ float* out_row(const AttendPrefix& A, const Seg& S, int r) {
+    const RowHead h = row_head(A, S, r);
+    return h.row < 0 ? nullptr : A.G.row_part + row_part_at(A, A.G, h.row, h.head);
+}
+__device__ __forceinline__ void put(const AttendPrefix& A, float* to, int c4, f32x4_t o, const Part& a, float) {
+    *reinterpret_cast<f32x4_t*>(to + c4) = o;
+    if (c4 == 0) *reinterpret_cast<float4*>(to + A.c.head_pad) = packed(a);
+}
+
+// ---- launch 2
+struct RestRows : KvRows {
+    int skip;
+};
+struct RestOut {
+    uint16_t* to = nullptr;
+    const float* part = nullptr;
+    __device__ __forceinline__ explicit operator bool() const { return to != nullptr; }
+};
+struct AttendRest : Attend {
+    typedef RestRows Row;
+    typedef RestOut Out;
+    GroupArgs G;
+};
+__device__ __forceinline__ RestRows no_rows(const AttendRest&) { return RestRows{{0, 0, 0, 0}, 0}; }
+__device__ __forceinline__ RestRows shuffled(const RestRows& R, int i) {
+    return RestRows{shuffled(static_cast<const KvRows&>(R), i), __shfl(R.skip, i)};
+}
+__device__ __forceinline__ RestRows of_lane(const RestRows& R, int on) {
+    return RestRows{of_lane(static_cast<const KvRows&>(R), on), __builtin_amdgcn_readlane(R.skip, on)};
+}
+__device__ __forceinline__ RestRows rows_of(const AttendRest& A, int s) {
+    return RestRows{rows_of(static_cast<const Attend&>(A), s), A.G.skip[s]};
+}
+__device__ __forceinline__ TileOf<RestRows> tile_of(const AttendRest& A, const RestRows& R, int t) {
+    TileOf<RestRows> x;
+    x.R = R;
+    x.i0 = t * A.TQ;
+    x.n = min(R.rows - x.i0, A.TQ);
+    const int cap = A.b.max_pages * kKvPage;
+    const int p1 = R.first + x.i0 + x.n, hi = min(p1, cap), lo = R.skip * kKvPage;   // positions lo .. hi - 1
+    const bool some = hi > 0 && lo < hi;
+    x.pg0 = some ? R.skip : 0;
+    x.pages = x.n <= 0 ? 0 : some ? (hi - 1) / kKvPage + 1 - x.pg0 : 1;
+    return x;
+}
+__device__ __forceinline__ int ctx_of(const AttendRest&, const TileOf<RestRows>& T) { return T.R.first + T.R.n; }
+__device__ __forceinline__ RestOut out_row(const AttendRest& A, const Seg& S, int r) {
+    const RowHead h = row_head(A, S, r);
+    RestOut x;
+    if (h.row < 0) return x;
+    x.to = A.out + (int64_t)h.row * A.os + (int64_t)h.head * A.c.head_dim;
+    if (A.G.joins[h.row]) x.part = A.G.row_part + row_part_at(A, A.G, h.row, h.head);
+    return x;
+}
+__device__ __forceinline__ void put(const AttendRest& A, const RestOut& x, int c4, f32x4_t o, const Part& a, float) {
+    if (c4 >= A.c.head_dim) return;
+    Part all = a;
+    if (x.part)
+        join(all, o, unpacked(*reinterpret_cast<const float4*>(x.part + A.c.head_pad)), *reinterpret_cast<const f32x4_t*>(x.part + c4));
+    *reinterpret_cast<uint2*>(x.to + c4) = bf16x4(result(o, inverse(all.sum), all.e));
+}
+
+// Splits of the two launches, and the workspace (host).
+struct SharedPlan {
+    prox_kv_batch groups;      // the batch that launch 1 sees
+    Split prefix;
+    Launches rest;
+    bool fits;
+    size_t row_part, skip, joins, bytes;
+    SharedPlan(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int n_groups)
+        : groups(b), prefix(), rest(c, b, n_heads) {
+        groups.n_seq = n_groups;
+        groups.max_q = b.n_tokens;
+        prefix = split_of(c, groups, n_heads, b.n_tokens, b.n_tokens);
+        fits = prefix.fits && rest.fit();
+        row_part = align_up(std::max(prefix.bytes, std::max(rest.split[0].bytes, rest.split[1].bytes)), 256);
+        skip = row_part + align_up((size_t)b.n_tokens * n_heads * (c.head_pad + 4) * sizeof(float), 256);
+        joins = skip + align_up((size_t)b.n_seq * sizeof(int32_t), 256);
+        bytes = joins + align_up((size_t)b.n_tokens * sizeof(int32_t), 256);
+    }
+};
+
+template <typename AT>
+hipError_t launch(AT& A, const Split& p, void* workspace, hipStream_t s) {
+    A.arrived = static_cast<unsigned long long*>(workspace);
+    A.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_at);
+    set_split(A, p);
+    return A.c.kind == PROX_KV_INT8 ? attend_kind<PROX_KV_INT8>(A, p, s) : attend_kind<PROX_KV_FP8>(A, p, s);
+}
+
+}  // namespace
+
+size_t kv_shared_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int n_groups) {
+    if (b.n_tokens <= 0 || b.max_q <= 0) return 256;
+    const SharedPlan P(c, bounded(b), n_heads, n_groups);
+    return P.fits ? P.bytes : 0;
+}
+
+hipError_t launch_kv_shared(const prox_kv_cache& c, const prox_kv_batch& batch, const int32_t* group_start, int n_groups,
+                            const int32_t* shared, const uint16_t* q, int64_t q_stride, int n_heads, float scale,
+                            uint16_t* out, int64_t out_stride, void* workspace, hipStream_t s) {
+    const prox_kv_batch b = bounded(batch);
+    const SharedPlan P(c, b, n_heads, n_groups);
+    if (!P.fits) return hipErrorInvalidConfiguration;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const GroupArgs G{group_start, shared, n_groups, b.n_seq, n_heads, reinterpret_cast<float*>(ws + P.row_part),
+                      reinterpret_cast<int32_t*>(ws + P.skip), reinterpret_cast<int32_t*>(ws + P.joins)};
+    AttendPrefix A{};
+    set_call(A, c, P.groups, q, q_stride, n_heads, scale, 0, out, out_stride);
+    A.G = G;
+    hipError_t e = launch(A, P.prefix, workspace, s);
+    if (e != hipSuccess) return e;
+    AttendRest B{};
+    set_call(B, c, b, q, q_stride, n_heads, scale, 0, out, out_stride);
+    B.G = G;
+    for (int k = P.rest.few > 0 ? 0 : 1; k < 2; ++k) {
+        B.rows_lo = k == 0 ? 1 : P.rest.few + 1;
+        B.rows_hi = k == 0 ? P.rest.few : b.max_q;
+        e = launch(B, P.rest.split[k], workspace, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace prox

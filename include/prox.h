@@ -508,6 +508,30 @@ prox_status prox_kv_attention_selected(const prox_kv_cache* c, const prox_kv_bat
                                        int32_t n_heads, const int32_t* pages, int32_t n_keep, float scale, void* out,
                                        int64_t out_stride, void* workspace, size_t ws_bytes, void* stream);
 
+/* Workspace bytes of prox_kv_attention_shared for this cache, batch (n_seq,
+ * n_tokens, max_q and max_pages count), query heads and number of groups; 0 if the
+ * arguments are invalid or the batch's bounds too large for one call. */
+size_t prox_kv_shared_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, int32_t n_heads, int32_t n_groups);
+
+/* prox_kv_attention, without a window, for sequences that share their first pages:
+ * the keys and values of a shared prefix are read once for all rows of a group.
+ * Group g is the sequences group_start[g] .. group_start[g + 1] - 1 (rising; a
+ * sequence outside every group shares nothing); their first shared[g] pages are
+ * those of the group's first sequence (the others' table entries for them are not
+ * read).  A sequence that holds no more than those pages before the call's rows
+ * (first position below 64 * shared[g]) counts as sharing none, and its own table
+ * names all of its pages.
+ *   group_start  device int32 [n_groups + 1], or null: one group of all sequences
+ *   shared       device int32 [n_groups], 0 <= shared[g] <= max_pages (clamped)
+ *   n_groups     1 <= n_groups <= n_seq
+ * The other arguments as prox_kv_attention's; the workspace is
+ * prox_kv_shared_workspace_bytes(), among it a result in fp32 for every row and
+ * query head. */
+prox_status prox_kv_attention_shared(const prox_kv_cache* c, const prox_kv_batch* b, const int32_t* group_start,
+                                     int32_t n_groups, const int32_t* shared, const void* q, int64_t q_stride,
+                                     int32_t n_heads, float scale, void* out, int64_t out_stride, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
 /* ---- Measurement helper (not part of the forward) ---------------------------
  * Read-stream probe: reads the first bytes / 16 * 16 bytes of the device
  * buffer `buf` (16-byte aligned) with `blocks` blocks of 512 threads, each

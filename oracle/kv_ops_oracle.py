@@ -154,3 +154,19 @@ def attention_selected(cache, table, ctx, q_start, max_q, q, pages, scale):
             o, e = KO.attention(_Part(cache, g), t, np.array([n]), np.array([0, 1]), 1, q[row:row + 1, heads], scale)
             out[row, heads], tol[row, heads] = o[0], e[0]
     return out, tol
+
+
+def attention_shared(cache, table, ctx, q_start, max_q, q, shared, group_start, scale):
+    """(out, tol) as kv_oracle.attention, with the first pages of a group's sequences taken
+    from its first one."""
+    table = table.copy()
+    n, width = table.shape
+    q0 = np.arange(n + 1) if q_start is None else np.asarray(q_start)
+    gs = [0, n] if group_start is None else [int(x) for x in group_start]
+    own = table.copy()
+    for g, (a, b) in enumerate(zip(gs, gs[1:])):
+        pages = min(max(int(shared[g]), 0), width)
+        for s in range(a, b):
+            if int(ctx[s]) - int(q0[s + 1] - q0[s]) >= PAGE * pages:
+                table[s, :pages] = own[a, :pages]
+    return KO.attention(cache, table, ctx, q_start, max_q, q, scale)

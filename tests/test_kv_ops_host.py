@@ -39,6 +39,11 @@ def selected(c=None, b=None, q=FAKE, qs=512, H=4, lst=FAKE, keep=4, scale=0.1, o
                                            scale, out, os, ws, n, None)
 
 
+def shared(c=None, b=None, gs=FAKE, n=2, sh=FAKE, q=FAKE, qs=512, H=4, scale=0.1, out=2 * FAKE, os=512, ws=FAKE, bytes=1 << 40):
+    return _lib.prox_kv_attention_shared(ctypes.byref(c or cache()), ctypes.byref(b or batch()), gs, n, sh, q, qs, H, scale,
+                                         out, os, ws, bytes, None)
+
+
 def test_pool_refusals():
     for over, want in ((dict(n_pages=0), INVALID), (dict(n_seq=0), INVALID), (dict(max_pages=0), INVALID),
                        (dict(n_pages=(1 << 24) + 1), UNSUPPORTED), (dict(n_seq=(1 << 24) + 1), UNSUPPORTED),
@@ -53,7 +58,7 @@ def test_pool_refusals():
     assert need > 0 and pages(n=need - 1) == WORKSPACE
 
 
-@pytest.mark.parametrize("call", [bounds, select, selected])
+@pytest.mark.parametrize("call", [bounds, select, selected, shared])
 def test_cache_and_batch_refusals(call):
     for over, want in ((dict(kind=0), INVALID), (dict(n_pages=0), INVALID), (dict(n_kv=1025), UNSUPPORTED),
                        (dict(head_dim=132), INVALID), (dict(head_pad=64), MISMATCH), (dict(k=0), INVALID)):
@@ -92,6 +97,24 @@ def test_selected_refusals():
     c = cache(n_kv=64)
     assert _lib.prox_kv_selected_workspace_bytes(ctypes.byref(c), ctypes.byref(big), 64, 4) == 0
     assert selected(c=c, b=big, H=64, qs=64 * 128, os=64 * 128) == UNSUPPORTED
+
+
+def test_shared_refusals():
+    assert shared(q=0) == INVALID and shared(out=0) == INVALID and shared(out=FAKE) == INVALID
+    assert shared(H=5) == INVALID and shared(H=1026) == UNSUPPORTED
+    assert shared(qs=511) == INVALID and shared(os=500) == INVALID
+    assert shared(n=0) == INVALID and shared(n=4) == INVALID and shared(gs=0) == INVALID
+    assert shared(sh=0) == INVALID and shared(sh=FAKE + 2) == INVALID and shared(gs=FAKE + 1) == INVALID
+    assert shared(scale=float("inf")) == INVALID and shared(scale=float("nan")) == INVALID
+    assert shared(ws=0) == INVALID and shared(ws=FAKE + 16) == INVALID
+    need = _lib.prox_kv_shared_workspace_bytes(ctypes.byref(cache()), ctypes.byref(batch()), 4, 2)
+    assert need > 0 and shared(bytes=need - 1) == WORKSPACE
+    assert shared(gs=0, n=1, bytes=0) == WORKSPACE
+    for over in (dict(n_seq=1 << 20, n_tokens=1 << 20, max_q=1, max_pages=300),
+                 dict(n_seq=1 << 28, n_tokens=1 << 28, max_q=1 << 28, max_pages=(1 << 25) - 1)):
+        b, c = batch(**over), cache(n_kv=8)
+        assert _lib.prox_kv_shared_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 32, 1) == 0
+        assert shared(c=c, b=b, H=32, qs=32 * 128, os=32 * 128, n=1) == UNSUPPORTED
 
 
 def test_python_handles_refuse_host_tensors_and_shapes():
