@@ -199,7 +199,7 @@ def test_memory_let_go_before_the_stream_runs():
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(50_000_000)
+        torch.cuda._sleep(400_000_000)      # the calls below wait behind this
 
     def calls():
         batch = P.KVBatch(b.ctx_len.clone(), b.block_table.clone(), b.q_start.clone(), n_tokens=3, max_q=2)
@@ -214,6 +214,7 @@ def test_memory_let_go_before_the_stream_runs():
     out, kept, sizes = calls()
     assert not side.query()
     junk = [torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") for n in sizes + [8, 12] for _ in range(2)]
-    assert not kept & {t.data_ptr() for t in junk}
+    again = {t.data_ptr() for t in junk}
+    assert not side.query() and not kept & again
     torch.cuda.synchronize()
     assert torch.equal(out, want)

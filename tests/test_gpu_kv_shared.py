@@ -174,7 +174,7 @@ def test_long_prefix_in_many_pieces(kind):
     w.o.ks[:], w.o.vs[:] = 0.002, 0.01
     w.c.k_scale.fill_(0.002), w.c.v_scale.fill_(0.01)
     attend(w, [1, 1, 1], [254])
-    attend(w, [6, 40, 100], [254])
+    attend(w, [6, 10, 20], [254])
 
 
 def test_same_result_twice_and_workspace_of_any_content():
@@ -245,13 +245,14 @@ def test_memory_let_go_before_the_stream_runs():
     q = w.rows(7, 8, 1.5)
     want = P.kv_attention_shared(q, w.c, b, dev([9]), group_start=dev([0, 3]))
     side = torch.cuda.Stream()
+    sh0, gs0 = dev([9]), dev([0, 3])
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(50_000_000)
+        torch.cuda._sleep(400_000_000)      # the calls below wait behind this
 
     def calls():
         batch = P.KVBatch(b.ctx_len.clone(), b.block_table.clone(), b.q_start.clone(), n_tokens=7, max_q=4)
-        qq, sh, gs = q.clone(), dev([9]), dev([0, 3])
+        qq, sh, gs = q.clone(), sh0.clone(), gs0.clone()
         side.wait_stream(torch.cuda.current_stream())
         out = P.kv_attention_shared(qq, w.c, batch, sh, group_start=gs, stream=side)
         return out, {t.data_ptr() for t in (qq, sh, gs, batch.ctx_len, batch.block_table, batch.q_start)}, \
@@ -259,6 +260,7 @@ def test_memory_let_go_before_the_stream_runs():
     out, kept, sizes = calls()
     assert not side.query()
     junk = [torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") for n in sizes + [8, 12, 16] for _ in range(2)]
-    assert not kept & {t.data_ptr() for t in junk}
+    again = {t.data_ptr() for t in junk}
+    assert not side.query() and not kept & again
     torch.cuda.synchronize()
     assert torch.equal(out, want)
