@@ -189,7 +189,7 @@ extern "C" prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want,
         !aligned(status, 4))
         return fail(PROX_E_INVALID, "misaligned array");
     if (!workspace) return fail(PROX_E_INVALID, "null workspace");
-    if (!aligned(workspace, 4)) return fail(PROX_E_INVALID, "workspace must be 4-byte aligned");
+    if (!aligned(workspace, 8)) return fail(PROX_E_INVALID, "workspace must be 8-byte aligned");
     const size_t need = kv_pages_workspace(*p);
     if (ws_bytes < need) return fail(PROX_E_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     return launched(launch_kv_pages(*p, want, parent, shared, q_start, n_rows, slots, status, workspace, (hipStream_t)stream),

@@ -145,6 +145,7 @@ __device__ __forceinline__ float over_groups_max(float v) {
 struct Attend {
     typedef KvRows Row;
     typedef uint16_t* Out;
+    static constexpr bool kJoinLater = false;   // parts of cut segments are joined by another launch
     prox_kv_cache c;
     prox_kv_batch b;
     const uint16_t* q;
@@ -410,6 +411,9 @@ template <typename Tile>
 __device__ __forceinline__ Seg seg_of(const Place& P, const Tile& T) {
     return Seg{P.begin, P.pages, P.vh, T.R.q0 + T.i0, T.n};
 }
+
+// Where the parts of token i of a segment are, for the launch that joins them.
+__device__ __forceinline__ void later(const Attend&, const Seg&, int, int, int) {}
 
 // r / A.HG for r < 256, HG <= 256: r times the rounding of 2^17 / HG stays below 2^17 / HG
 __device__ __forceinline__ int token_of(const Attend& A, int r) { return (int)((uint32_t)r * A.HG_inv >> 17); }
@@ -1110,6 +1114,15 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(AT A
         }
     }
     if (!sent) return;                            // uniform over the block
+    if constexpr (AT::kJoinLater) {
+        __syncthreads();
+        const Seg S = cut_s[1];                   // the segment that begins here and goes on behind the piece
+        if (S.begin < 0) return;
+        int w0, w1;
+        blocks_of(A, piece, S.begin, S.pages, w0, w1);
+        for (int i = threadIdx.x; i < S.n; i += blockDim.x) later(A, S, i, w0, w1 - w0 + 1);
+        return;
+    }
 
     // Arrivals: of the segment that continues into this piece, and of the one
     // that goes on behind it (the same one if it spans the piece).

@@ -1,15 +1,20 @@
 // Attention over the paged key/value cache for sequences that share a prefix.
 //
 // A softmax over two sets of positions is put together from the two sets' own
-// maxima, sums and results.  So a call is two launches of the attention's kernel:
+// maxima, sums and results.  So a call is two launches of the attention's kernel
+// and one between them:
 //   1  the rows of all sequences of a group, as those of one sequence, over the
 //      group's shared pages, without a mask; what comes out is each row's
 //      maximum, sum, unit and unnormalised result, in fp32, in the workspace;
-//   2  the rows of each sequence over its other pages, causal; a row's part of 1
+//   2  a group has few tiles of rows, each cut among many blocks: the parts of a
+//      row are joined, all rows at once (by the block that arrives last, as the
+//      attention over all pages does it, 64 tokens over 512 shared pages took
+//      148 us instead of 62 + 9: 4 MB of parts for one block);
+//   3  the rows of each sequence over its other pages, causal; a row's part of 1
 //      joins before it is normalised and rounded.
 // A page of a prefix is read once for up to 256 rows (32 of each of 8 waves)
 // instead of once for each sequence.  A sequence whose first row lies inside the
-// prefix takes no part in it: launch 2 goes over all of its pages.
+// prefix takes no part in it: launch 3 goes over all of its pages.
 #include "prox_kv_attn.hpp"
 
 namespace prox {
@@ -20,9 +25,11 @@ struct GroupArgs {
     const int32_t *group_start, *shared;
     int n_groups, n_seq;
     int n_heads;
+    int blocks;                // of launch 1
     float* row_part;           // [n_tokens][n_heads][head_pad + 4]
     int32_t* skip;             // [n_seq]: pages of a sequence that are taken from its group
     int32_t* joins;            // [n_tokens]: whether the row takes its part of the prefix
+    int4* parts;               // [n_tokens][VH of launch 1]: first block, blocks (0: none to join), row of the tile
 };
 
 __device__ __forceinline__ int group_at(const GroupArgs& G, int g) {
@@ -47,12 +54,18 @@ __device__ __forceinline__ RowHead row_head(const Attend& A, const Seg& S, int r
 
 // ---- launch 1: "sequence" s is group s, A.b.n_seq their number; a group's Row has
 // the number of its shared pages as `first`.
+struct PrefixOut {
+    float* to = nullptr;
+    int4* parts = nullptr;
+    __device__ __forceinline__ explicit operator bool() const { return to != nullptr; }
+};
 struct AttendPrefix : Attend {
-    typedef float* Out;
+    typedef PrefixOut Out;
+    static constexpr bool kJoinLater = true;
     GroupArgs G;
 };
 
-// Which sequences and rows take part, for launch 2.
+// Which sequences and rows take part, for the other launches.
 __device__ __forceinline__ void prologue(const AttendPrefix& A, int wv, int l) {
     const GroupArgs& G = A.G;
     for (int s = blockIdx.x * (int)(blockDim.x >> 6) + wv; s < G.n_seq; s += gridDim.x * (int)(blockDim.x >> 6)) {
@@ -70,6 +83,12 @@ __device__ __forceinline__ void prologue(const AttendPrefix& A, int wv, int l) {
         const int cap = A.b.max_pages * kKvPage;
         for (int i = l; i < R.n; i += 64) G.joins[R.q0 + i] = pages > 0 && R.first + i < cap;
     }
+    // rows before the first and behind the last sequence
+    if (!A.b.q_start) return;
+    const int lo = min(max(A.b.q_start[0], 0), A.b.n_tokens), hi = min(max(A.b.q_start[G.n_seq], lo), A.b.n_tokens);
+    const int t = blockIdx.x * (int)blockDim.x + (int)threadIdx.x, all = gridDim.x * (int)blockDim.x;
+    for (int i = t; i < lo; i += all) G.joins[i] = 0;
+    for (int i = hi + t; i < A.b.n_tokens; i += all) G.joins[i] = 0;
 }
 __device__ __forceinline__ KvRows rows_of(const AttendPrefix& A, int g) {
     const int s0 = group_at(A.G, g), s1 = max(group_at(A.G, g + 1), s0);
@@ -94,16 +113,62 @@ __device__ __forceinline__ const int32_t* table_of(const AttendPrefix& A, int g)
 }
 __device__ __forceinline__ int ctx_of(const AttendPrefix&, const Tile&) { return 0; }   // any slot may hold no token
 __device__ __forceinline__ constexpr bool masked(const AttendPrefix&) { return false; }
-__device__ __forceinline__ float* out_row(const AttendPrefix& A, const Seg& S, int r) {
+__device__ __forceinline__ PrefixOut out_row(const AttendPrefix& A, const Seg& S, int r) {
     const RowHead h = row_head(A, S, r);
-    return h.row < 0 ? nullptr : A.G.row_part + row_part_at(A, A.G, h.row, h.head);
+    PrefixOut x;
+    if (h.row < 0) return x;
+    x.to = A.G.row_part + row_part_at(A, A.G, h.row, h.head);
+    x.parts = A.G.parts + (size_t)h.row * A.VH + S.vh;
+    return x;
 }
-__device__ __forceinline__ void put(const AttendPrefix& A, float* to, int c4, f32x4_t o, const Part& a, float) {
+__device__ __forceinline__ void put(const AttendPrefix& A, const PrefixOut& x, int c4, f32x4_t o, const Part& a, float) {
+    *reinterpret_cast<f32x4_t*>(x.to + c4) = o;
+    if (c4 == 0) {
+        *reinterpret_cast<float4*>(x.to + A.c.head_pad) = packed(a);
+        *x.parts = make_int4(0, 0, 0, 0);
+    }
+}
+__device__ __forceinline__ void later(const AttendPrefix& A, const Seg& S, int i, int block, int blocks) {
+    A.G.parts[(size_t)(S.row0 + i) * A.VH + S.vh] = make_int4(block, blocks, i * A.HG, 0);
+}
+
+// ---- launch 2: a thread for each row, query head and four channels.
+template <int NP>
+__global__ void __launch_bounds__(256) k_kv_join(AttendPrefix A, int64_t pairs) {
+    constexpr int RW = 64 * NP + 4, LPR = 16 * NP;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, pair = t / LPR;
+    const int c4 = 4 * (int)(t % LPR);
+    if (pair >= pairs) return;
+    const int row = (int)(pair / A.G.n_heads), hq = (int)(pair % A.G.n_heads);
+    if (!A.G.joins[row]) return;
+    const int groups = A.VH / A.c.n_kv, head = hq / A.rep, in = hq - head * A.rep, grp = in / A.HG;
+    const int4 p = A.G.parts[(size_t)row * A.VH + head * groups + grp];
+    // (a q_start that does not rise leaves rows that nobody wrote this for: their loop ends too)
+    const int parts = min(p.y, A.G.blocks);
+    if (parts <= 0) return;
+    const __amdgpu_buffer_rsrc_t rp = make_rsrc(A.part, A.part_bytes);
+    const uint32_t r = (uint32_t)(p.z + in - grp * A.HG);
+    Part a = no_part();
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int p0 = 0; p0 < parts; p0 += 8) {
+        u32x4_t v[8], ms[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int k = min(p0 + u, parts - 1);
+            const uint32_t at = ((2u * ((uint32_t)p.x + (uint32_t)k) + (k == 0 ? 1u : 0u)) * (uint32_t)A.slot_rows + r) * (uint32_t)(RW * 4);
+            v[u] = __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 4 * c4), 0, 0);
+            ms[u] = __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 256 * NP), 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (p0 + u < parts) join(a, o, unpacked(__builtin_bit_cast(float4, ms[u])), __builtin_bit_cast(f32x4_t, v[u]));
+    }
+    float* to = A.G.row_part + row_part_at(A, A.G, row, hq);
     *reinterpret_cast<f32x4_t*>(to + c4) = o;
     if (c4 == 0) *reinterpret_cast<float4*>(to + A.c.head_pad) = packed(a);
 }
 
-// ---- launch 2
+// ---- launch 3
 struct RestRows : KvRows {
     int skip;
 };
@@ -156,23 +221,24 @@ __device__ __forceinline__ void put(const AttendRest& A, const RestOut& x, int c
     *reinterpret_cast<uint2*>(x.to + c4) = bf16x4(result(o, inverse(all.sum), all.e));
 }
 
-// Splits of the two launches, and the workspace (host).
+// Splits of the launches, and the workspace (host).
 struct SharedPlan {
     prox_kv_batch groups;      // the batch that launch 1 sees
     Split prefix;
     Launches rest;
     bool fits;
-    size_t row_part, skip, joins, bytes;
+    size_t row_part, skip, joins, parts, bytes;
     SharedPlan(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int n_groups)
         : groups(b), prefix(), rest(c, b, n_heads) {
         groups.n_seq = n_groups;
         groups.max_q = b.n_tokens;
         prefix = split_of(c, groups, n_heads, b.n_tokens, b.n_tokens);
-        fits = prefix.fits && rest.fit();
+        fits = prefix.fits && rest.fit() && (int64_t)b.n_tokens * n_heads <= 0x7fffffffll * 4;
         row_part = align_up(std::max(prefix.bytes, std::max(rest.split[0].bytes, rest.split[1].bytes)), 256);
         skip = row_part + align_up((size_t)b.n_tokens * n_heads * (c.head_pad + 4) * sizeof(float), 256);
         joins = skip + align_up((size_t)b.n_seq * sizeof(int32_t), 256);
-        bytes = joins + align_up((size_t)b.n_tokens * sizeof(int32_t), 256);
+        parts = joins + align_up((size_t)b.n_tokens * sizeof(int32_t), 256);
+        bytes = parts + align_up((size_t)b.n_tokens * prefix.VH * sizeof(int4), 256);
     }
 };
 
@@ -199,12 +265,23 @@ hipError_t launch_kv_shared(const prox_kv_cache& c, const prox_kv_batch& batch, 
     const SharedPlan P(c, b, n_heads, n_groups);
     if (!P.fits) return hipErrorInvalidConfiguration;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const GroupArgs G{group_start, shared, n_groups, b.n_seq, n_heads, reinterpret_cast<float*>(ws + P.row_part),
-                      reinterpret_cast<int32_t*>(ws + P.skip), reinterpret_cast<int32_t*>(ws + P.joins)};
+    const GroupArgs G{group_start, shared, n_groups, b.n_seq, n_heads, P.prefix.blocks, reinterpret_cast<float*>(ws + P.row_part),
+                      reinterpret_cast<int32_t*>(ws + P.skip), reinterpret_cast<int32_t*>(ws + P.joins),
+                      reinterpret_cast<int4*>(ws + P.parts)};
     AttendPrefix A{};
     set_call(A, c, P.groups, q, q_stride, n_heads, scale, 0, out, out_stride);
     A.G = G;
     hipError_t e = launch(A, P.prefix, workspace, s);
+    if (e != hipSuccess) return e;
+    const int64_t pairs = (int64_t)b.n_tokens * n_heads, blocks = (pairs * (c.head_pad / 4) + 255) / 256;
+    const dim3 grid((uint32_t)blocks), threads(256);
+    switch (c.head_pad / 64) {
+        case 1: hipLaunchKernelGGL((k_kv_join<1>), grid, threads, 0, s, A, pairs); break;
+        case 2: hipLaunchKernelGGL((k_kv_join<2>), grid, threads, 0, s, A, pairs); break;
+        case 3: hipLaunchKernelGGL((k_kv_join<3>), grid, threads, 0, s, A, pairs); break;
+        default: hipLaunchKernelGGL((k_kv_join<4>), grid, threads, 0, s, A, pairs); break;
+    }
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
     AttendRest B{};
     set_call(B, c, b, q, q_stride, n_heads, scale, 0, out, out_stride);

@@ -452,7 +452,7 @@ size_t prox_kv_pages_workspace_bytes(const prox_kv_pool* p);
  *   slots   [n_rows]     64 * page + slot of each such row, -1 for rows behind the
  *                        last (rows that n_rows leaves no room for are dropped)
  *   status  [2]          sequences refused; free pages left
- * parent and shared [n_seq] are both given or both null.  workspace: device, 4-byte
+ * parent and shared [n_seq] are both given or both null.  workspace: device, 8-byte
  * aligned, scratch.  Calls on one pool must not overlap in time. */
 prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want, const int32_t* parent, const int32_t* shared,
                           int32_t* q_start, int32_t n_rows, int32_t* slots, int32_t* status, void* workspace,

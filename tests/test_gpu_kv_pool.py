@@ -115,8 +115,10 @@ def test_rows_that_do_not_fit():
         w.move([0, 0, 0])
 
 
+# the last ones in several blocks: many pages, many sequences, long tables
 @pytest.mark.parametrize("n_pages,n_seq,max_pages,top", [(1, 1, 1, 70), (3000, 1100, 9, 500), (5000, 70, 200, 9000),
-                                                         (129, 17, 40, 2000)])
+                                                         (129, 17, 40, 2000), (70003, 300, 300, 19000), (2047, 1024, 3, 190),
+                                                         (33000, 5000, 12, 700), (66000, 3, 30000, 1900000)])
 def test_random_steps(n_pages, n_seq, max_pages, top):
     w = Pair(n_pages, n_seq, max_pages)
     r = np.random.default_rng(n_pages)
@@ -127,9 +129,10 @@ def test_random_steps(n_pages, n_seq, max_pages, top):
         w.move(want, parent=par, shared=r.integers(0, 6, n_seq))
 
 
-def test_captured_and_replayed():
+@pytest.mark.parametrize("n_pages,max_pages", [(200, 16), (70000, 16)])
+def test_captured_and_replayed(n_pages, max_pages):
     import free_ffn_activation_prox_amd as P
-    w = Pair(200, 8, 16)
+    w = Pair(n_pages, 8, max_pages)
     want, par, sh = (torch.zeros(8, dtype=torch.int32, device="cuda") for _ in range(3))
     par.fill_(-1)
     r = np.random.default_rng(5)

@@ -191,6 +191,29 @@ def test_same_result_twice_and_workspace_of_any_content():
     assert all(torch.equal(g, got[0]) for g in got)
 
 
+def test_rows_outside_every_sequence_with_any_workspace():
+    """Rows before the first and behind the last sequence, whose places in the workspace nobody writes."""
+    w = World("int8", 4, 2, 64, [700, 500, 449], seed=42)
+    settle(w, [700, 500, 449])
+    share(w, [0, 3], [6])
+    P = w.P
+    b = P.KVBatch(torch.from_numpy(w.ctx.copy()).cuda(), torch.from_numpy(w.table).cuda(), dev([5, 6, 9, 10]), n_tokens=40, max_q=3)
+    q = w.rows(40, 4, 1.5)
+    ws = P.alloc_kv_shared_workspace(w.c, b, 4)
+    got = []
+    for fill in (0, 0x7f, 0xff):
+        ws.fill_(fill)
+        out = torch.full_like(q, 7.0)
+        P.kv_attention_shared(q, w.c, b, dev([6]), out=out, workspace=ws)
+        got.append(out)
+    torch.cuda.synchronize()
+    want, tol = OO.attention_shared(w.o, w.table, w.ctx, [5, 6, 9, 10], 3, f64(q), [6], None, 64 ** -0.5)
+    for out in got:
+        out = f64(out)
+        assert (np.abs(out[5:10] - want[5:10]) <= tol[5:10]).all()
+        assert (out[:5] == 7).all() and (out[10:] == 7).all()
+
+
 def test_two_captured_graphs_share_a_workspace_as_lengths_move():
     w = World("fp8", 8, 2, 64, [900] * 4, seed=40)
     settle(w, [700, 600, 650, 580])

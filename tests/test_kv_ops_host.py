@@ -52,7 +52,7 @@ def test_pool_refusals():
         assert pages(p=pool(**over)) == want, over
         assert _lib.prox_kv_pages_workspace_bytes(ctypes.byref(pool(**over))) == 0
     for over in (dict(want=0), dict(qs=0), dict(status=0), dict(slots=0), dict(ws=0), dict(parent=FAKE), dict(shared=FAKE),
-                 dict(rows=-1), dict(want=FAKE + 2), dict(ws=FAKE + 2), dict(slots=FAKE + 1)):
+                 dict(rows=-1), dict(want=FAKE + 2), dict(ws=FAKE + 4), dict(slots=FAKE + 1)):
         assert pages(**over) == INVALID, over
     need = _lib.prox_kv_pages_workspace_bytes(ctypes.byref(pool()))
     assert need > 0 and pages(n=need - 1) == WORKSPACE
