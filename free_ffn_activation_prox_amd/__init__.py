@@ -121,7 +121,9 @@ def _load() -> ctypes.CDLL:
         "prox_kv_pages_workspace_bytes": (SZ, [ctypes.POINTER(_KVPool)]),
         "prox_kv_pages": (I32, [ctypes.POINTER(_KVPool), P, P, P, P, I32, P, P, P, SZ, P]),
         "prox_kv_page_bounds": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, P]),
-        "prox_kv_select": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, P, I32, I32, I32, P, P]),
+        "prox_kv_select": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, P, I32, I32, I32, P,
+                                 P, SZ, P]),
+        "prox_kv_select_workspace_bytes": (SZ, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), I32]),
         "prox_kv_selected_workspace_bytes": (SZ, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), I32, I32]),
         "prox_kv_attention_selected": (I32, [ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch), P, I64, I32, P, I32,
                                              ctypes.c_float, P, I64, P, SZ, P]),
@@ -777,8 +779,15 @@ def kv_page_bounds(cache: KVCache, batch: KVBatch, bounds, *, stream=None):
     return bounds
 
 
+def alloc_kv_select_workspace(cache: KVCache, batch: KVBatch, n_heads: int):
+    """Workspace of kv_select for batches of this shape (n_seq, n_tokens, max_q, max_pages)."""
+    with torch.cuda.device(cache.device):
+        n = _lib.prox_kv_select_workspace_bytes(cache._ref, batch._ref, n_heads)
+    return _alloc_scratch(cache, n)
+
+
 def kv_select(q, cache: KVCache, batch: KVBatch, bounds, n_keep: int, *, first: int = 1, last: int = 1, pages=None,
-              stream=None):
+              workspace=None, stream=None):
     """For every row of q (as kv_attention takes it) and key head the n_keep pages
     of its sequence whose keys can give the largest scores, by their bounds; the
     first `first` and last `last` pages that the row sees are always among them.
@@ -791,14 +800,18 @@ def kv_select(q, cache: KVCache, batch: KVBatch, bounds, n_keep: int, *, first: 
         raise ValueError("n_keep, first and last must fit 32 bits")
     qs = _kv_rows("q", q, n, None, hd, dev)
     bp = _bounds_ptr(cache, bounds)
-    if pages is None:
-        with _made_on(stream):
+    with _made_on(stream):
+        if pages is None:
             pages = torch.empty(n, cache.n_kv, max(n_keep, 0), dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = alloc_kv_select_workspace(cache, batch, q.shape[1])
     pp = _ints("pages", pages, (n, cache.n_kv, n_keep), dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
     sp, here = _on(stream, dev)
     _kv_call(_lib.prox_kv_select, "prox_kv_select", dev, here, cache._ref, batch._ref, q.data_ptr(), qs, q.shape[1], bp,
-             n_keep, first, last, pp, sp)
-    _held_for(stream, cache, batch, q, bounds, pages)
+             n_keep, first, last, pp, workspace.data_ptr(), workspace.nbytes, sp)
+    _held_for(stream, cache, batch, q, bounds, pages, workspace)
     return pages
 
 
@@ -889,7 +902,7 @@ def kv_attention_shared(q, cache: KVCache, batch: KVBatch, shared, *, group_star
     return out
 
 
-__all__ = ["alloc_kv_shared_workspace", "kv_attention_shared", "alloc_kv_selected_workspace", "kv_attention_selected", "KVPool", "kv_pages", "alloc_kv_bounds", "kv_page_bounds", "kv_select",
+__all__ = ["alloc_kv_shared_workspace", "kv_attention_shared", "alloc_kv_selected_workspace", "kv_attention_selected", "KVPool", "kv_pages", "alloc_kv_bounds", "kv_page_bounds", "alloc_kv_select_workspace", "kv_select",
            "KVCache", "KVBatch", "KV_KINDS", "KV_PAGE", "kv_head_pad", "kv_append", "kv_attention", "kv_read",
            "kv_workspace_bytes", "alloc_kv_workspace",
            "QWeights", "build_qweights", "qweights_bytes", "quality", "timeline_forward", "read_probe", "noalloc_scratch_bytes", "ffn_forward_noalloc", "Weights", "Proxy", "ProxError", "abi_version", "library_sha256", "proxy_bytes", "workspace_bytes",

@@ -174,40 +174,6 @@ __device__ __forceinline__ void dwords_of_tokens(const uint2 w[4], uint32_t d[8]
 // several kilobytes lies in different banks.
 __device__ __forceinline__ int in_image(int at) { return at + (at >> 10) * 16; }
 
-// Codes of x / unit, correctly rounded.  With the rounded reciprocal i of unit,
-// y = x i and its exact remainder x - y unit, y + i (x - y unit) is the rounded
-// quotient (Markstein) unless the mantissa of unit is all ones or a number
-// leaves the normal range; a page with such a scale, or with an infinity or
-// NaN, is not `tame` and takes the division and clamp.  The division alone
-// takes ten instructions a value, all of the rest six.
-template <int KIND>
-struct Quotient {
-    float unit, inv;
-    bool tame, zero;
-    __device__ __forceinline__ Quotient(float scale, bool finite) {
-        zero = !(scale > 0.f);
-        unit = zero ? 1.f : scale;
-        tame = finite && scale > 0x1p-90f && scale < 0x1p90f && (__float_as_uint(unit) & 0x7fffffu) != 0x7fffffu;
-        inv = 1.f / unit;
-    }
-    __device__ __forceinline__ uint32_t tame4(const float* x) const {
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float q = x[e] * inv;
-            y[e] = fmaf(fmaf(-q, unit, x[e]), inv, q);
-        }
-        return kv_codes4_tame<KIND>(y);
-    }
-    __device__ __forceinline__ uint32_t codes4(const float* x) const {
-        if (tame) return tame4(x);
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = zero ? 0.f : x[e] / unit;
-        return kv_codes4<KIND>(y);
-    }
-};
-
 // Eight channels of one row of K (normed and rotated for position pos) or V;
 // a lane that holds none (`off`) takes part with zeros.
 template <int TPT, bool VAL>

@@ -88,6 +88,40 @@ __device__ __forceinline__ uint32_t kv_codes4_tame(const float x[4]) {
     }
 }
 
+// Codes of x / unit, correctly rounded.  With the rounded reciprocal i of unit,
+// y = x i and its exact remainder x - y unit, y + i (x - y unit) is the rounded
+// quotient (Markstein) unless the mantissa of unit is all ones or a number
+// leaves the normal range; a page with such a scale, or with an infinity or
+// NaN, is not `tame` and takes the division and clamp.  The division alone
+// takes ten instructions a value, all of the rest six.
+template <int KIND>
+struct Quotient {
+    float unit, inv;
+    bool tame, zero;
+    __device__ __forceinline__ Quotient(float scale, bool finite) {
+        zero = !(scale > 0.f);
+        unit = zero ? 1.f : scale;
+        tame = finite && scale > 0x1p-90f && scale < 0x1p90f && (__float_as_uint(unit) & 0x7fffffu) != 0x7fffffu;
+        inv = 1.f / unit;
+    }
+    __device__ __forceinline__ uint32_t tame4(const float* x) const {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float q = x[e] * inv;
+            y[e] = fmaf(fmaf(-q, unit, x[e]), inv, q);
+        }
+        return kv_codes4_tame<KIND>(y);
+    }
+    __device__ __forceinline__ uint32_t codes4(const float* x) const {
+        if (tame) return tame4(x);
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = zero ? 0.f : x[e] / unit;
+        return kv_codes4<KIND>(y);
+    }
+};
+
 // The rows of sequence s: rows q0 .. q0 + n - 1 (clamped to the batch), of
 // which the first `rows` are worked on; row i has position first + i.
 struct KvRows {
@@ -184,7 +218,8 @@ hipError_t launch_kv_pages(const prox_kv_pool& p, const int32_t* want, const int
                            int32_t* q_start, int n_rows, int32_t* slots, int32_t* status, void* workspace, hipStream_t s);
 hipError_t launch_kv_bounds(const prox_kv_cache& c, const prox_kv_batch& b, int8_t* bounds, hipStream_t s);
 hipError_t launch_kv_select(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride, int n_heads,
-                            const int8_t* bounds, int keep, int first, int last, int32_t* pages, hipStream_t s);
+                            const int8_t* bounds, int keep, int first, int last, int32_t* pages, void* workspace, hipStream_t s);
+size_t kv_select_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads);
 size_t kv_selected_workspace(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int keep);
 hipError_t launch_kv_selected(const prox_kv_cache& c, const prox_kv_batch& b, const uint16_t* q, int64_t q_stride, int n_heads,
                               const int32_t* pages, int keep, float scale, uint16_t* out, int64_t out_stride,

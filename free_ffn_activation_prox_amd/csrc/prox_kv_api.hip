@@ -212,9 +212,16 @@ extern "C" prox_status prox_kv_page_bounds(const prox_kv_cache* c, const prox_kv
     return launched(launch_kv_bounds(*c, *b, static_cast<int8_t*>(bounds), (hipStream_t)stream), "page bounds");
 }
 
+extern "C" size_t prox_kv_select_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, int32_t n_heads) {
+    clear_error();
+    if (check_cache(c) != PROX_OK || check_batch(b) != PROX_OK || check_heads(c, n_heads) != PROX_OK) return 0;
+    if (b->max_pages > PROX_KV_MAX_SELECT_PAGES) return 0;
+    return kv_select_workspace(*c, *b, n_heads);
+}
+
 extern "C" prox_status prox_kv_select(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
                                       int32_t n_heads, const void* bounds, int32_t n_keep, int32_t first, int32_t last,
-                                      int32_t* pages, void* stream) {
+                                      int32_t* pages, void* workspace, size_t ws_bytes, void* stream) {
     clear_error();
     PROX_CHECK(check_cache(c));
     PROX_CHECK(check_batch(b));
@@ -227,8 +234,13 @@ extern "C" prox_status prox_kv_select(const prox_kv_cache* c, const prox_kv_batc
     if (!bounds || !pages) return fail(PROX_E_INVALID, "null bounds or pages");
     if (!aligned(bounds, 16) || !aligned(pages, 4)) return fail(PROX_E_INVALID, "misaligned bounds or pages");
     PROX_CHECK(check_rows("q", q, q_stride, (int64_t)n_heads * c->head_dim));
+    if (!workspace) return fail(PROX_E_INVALID, "null workspace");
+    if (!aligned(workspace, 256)) return fail(PROX_E_INVALID, "workspace must be 256-byte aligned");
+    const size_t need = kv_select_workspace(*c, *b, n_heads);
+    if (need == 0) return launched(hipErrorInvalidConfiguration, "page selection");
+    if (ws_bytes < need) return fail(PROX_E_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     return launched(launch_kv_select(*c, *b, static_cast<const uint16_t*>(q), q_stride, n_heads,
-                                     static_cast<const int8_t*>(bounds), n_keep, first, last, pages, (hipStream_t)stream),
+                                     static_cast<const int8_t*>(bounds), n_keep, first, last, pages, workspace, (hipStream_t)stream),
                     "page selection");
 }
 

@@ -468,6 +468,11 @@ prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want, const int3
  * bounds: device, 16-byte aligned. */
 prox_status prox_kv_page_bounds(const prox_kv_cache* c, const prox_kv_batch* b, void* bounds, void* stream);
 
+/* Workspace bytes of prox_kv_select for this cache, batch (n_seq, n_tokens, max_q and
+ * max_pages count) and query heads; 0 if the arguments are invalid or the batch's
+ * bounds too large for one call. */
+size_t prox_kv_select_workspace_bytes(const prox_kv_cache* c, const prox_kv_batch* b, int32_t n_heads);
+
 /* For every row of the batch and key head the n_keep pages of its sequence, of
  * those that it sees (0 .. position / 64), whose keys can give the largest score:
  *   unit_h = fl32(max|q_h| / 127) over finite channels, q8 = clamp(round-half-even(
@@ -483,12 +488,14 @@ prox_status prox_kv_page_bounds(const prox_kv_cache* c, const prox_kv_batch* b, 
  *   pages  device int32 [n_tokens][n_kv][n_keep]: numbers within the sequence,
  *          ascending, then -1; all -1 for a row whose position does not exist.
  *          Rows outside every sequence are not touched.
+ *   workspace  device, >= prox_kv_select_workspace_bytes(), 256-byte aligned,
+ *          scratch only.  Calls that share a workspace must not overlap in time.
  * 1 <= n_keep <= 2^20; first + last <= n_keep; max_pages up to
  * PROX_KV_MAX_SELECT_PAGES (PROX_E_UNSUPPORTED above). */
 #define PROX_KV_MAX_SELECT_PAGES 32768
 prox_status prox_kv_select(const prox_kv_cache* c, const prox_kv_batch* b, const void* q, int64_t q_stride,
                            int32_t n_heads, const void* bounds, int32_t n_keep, int32_t first, int32_t last,
-                           int32_t* pages, void* stream);
+                           int32_t* pages, void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of prox_kv_attention_selected for a batch of n_tokens rows; 0 if
  * the arguments are invalid or more than one call can take. */

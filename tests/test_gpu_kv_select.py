@@ -135,6 +135,36 @@ def test_long_context():
     chosen(w, bnd, [3], 1200, first=3, last=7)
 
 
+@pytest.mark.parametrize("pages,H,kinds", [(400, 3, 200), (700, 8, 3), (1500, 20, 200), (2048, 1, 1), (2049, 2, 4)])
+def test_tables_of_any_width(pages, H, kinds):
+    """Rows selected by a wave (of 8 or 32 keys a lane) and by a block, from few and many different keys."""
+    w = World("int8", H, 1, 64, [64 * pages, 64 * 70], seed=pages, extra=0)
+    w.ctx[:] = [64 * pages - 5, 64 * 70 - 1]
+    bnd = torch.from_numpy(w.rng.integers(0, kinds, (w.o.n_pages, 1, 2, 64)).astype(np.int64) - kinds // 2).to(torch.int8).cuda()
+    w.o.ks[:] = w.rng.choice(np.float32([0.5, 1.0]), w.o.ks.shape)
+    w.c.k_scale.copy_(torch.from_numpy(w.o.ks))
+    chosen(w, bnd, [1, 1], 33)
+    chosen(w, bnd, [5, 70], 100, first=2, last=3)
+    chosen(w, bnd, [9, 0], 3 * pages // 4)
+    chosen(w, bnd, [2, 3], 2)
+
+
+def test_workspace_of_any_content_twice():
+    w = World("int8", 8, 2, 64, [64 * 900], seed=19, extra=0)
+    w.ctx[:] = [64 * 900 - 5]
+    bnd = torch.from_numpy(w.rng.integers(-127, 128, (w.o.n_pages, 2, 2, 64)).astype(np.int8)).cuda()
+    P = w.P
+    b, _ = w.batch([2], advance=False)
+    q = w.rows(2, 8)
+    ws = P.alloc_kv_select_workspace(w.c, b, 8)
+    assert ws.numel() > 256                                # several blocks a row
+    got = []
+    for fill in (0, 0xff, 0x5a):
+        ws.fill_(fill)
+        got += [P.kv_select(q, w.c, b, bnd, 40, workspace=ws) for _ in range(3)]
+    assert all(torch.equal(g, got[0]) for g in got)
+
+
 def test_infinities_nan_zeros_and_tiny_values():
     w = World("int8", 4, 2, 64, [900], seed=13)
     settle(w, [900])

@@ -29,9 +29,9 @@ def bounds(c=None, b=None, out=FAKE):
     return _lib.prox_kv_page_bounds(ctypes.byref(c or cache()), ctypes.byref(b or batch()), out, None)
 
 
-def select(c=None, b=None, q=FAKE, qs=512, H=4, bnd=FAKE, keep=4, first=1, last=1, out=FAKE):
+def select(c=None, b=None, q=FAKE, qs=512, H=4, bnd=FAKE, keep=4, first=1, last=1, out=FAKE, ws=FAKE, n=1 << 40):
     return _lib.prox_kv_select(ctypes.byref(c or cache()), ctypes.byref(b or batch()), q, qs, H, bnd, keep, first, last,
-                               out, None)
+                               out, ws, n, None)
 
 
 def selected(c=None, b=None, q=FAKE, qs=512, H=4, lst=FAKE, keep=4, scale=0.1, out=2 * FAKE, os=512, ws=FAKE, n=1 << 40):
@@ -79,6 +79,11 @@ def test_bounds_and_select_refusals():
     assert select(first=-1) == INVALID and select(last=0) == INVALID and select(keep=4, first=3, last=2) == INVALID
     assert select(first=0x7fffffff, last=0x7fffffff) == INVALID
     assert select(b=batch(max_pages=32769)) == UNSUPPORTED
+    assert select(ws=0) == INVALID and select(ws=FAKE + 16) == INVALID
+    for b in (batch(), batch(max_pages=2000), batch(n_seq=1, n_tokens=1, max_q=1, max_pages=32768)):
+        need = _lib.prox_kv_select_workspace_bytes(ctypes.byref(cache()), ctypes.byref(b), 4)
+        assert need > 0 and select(b=b, n=need - 1) == WORKSPACE
+    assert _lib.prox_kv_select_workspace_bytes(ctypes.byref(cache()), ctypes.byref(batch(max_pages=32769)), 4) == 0
 
 
 def test_selected_refusals():
