@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(256) k_kv_bounds(BoundsArgs A, int64_t units) 
 
 constexpr int kSelThreads = 256;
 constexpr int kLeastRun = 128;      // least pages of a block, where a tile has several
-constexpr int kBlocksPerCu = 8;     // blocks that a launch is cut into where it can be
+constexpr int kBlocksPerCu = 1;     // blocks that a launch is cut into where it can be
 constexpr int kSelBins = 2048;      // of the block's selection (LDS words, with some to spare for its counts)
 constexpr int kSelScratch = 64;
 
@@ -217,7 +217,7 @@ template <int NP, int NT>
 __device__ __forceinline__ void page_keys(const SelectArgs& A, uint32_t* keys, uint32_t* q8, float* unit_s, const KvRows& R,
                                           int head, int i0, int rows, const int32_t* table, int from, int most) {
     constexpr int kWaves = NT / kWave, HP = 64 * NP, K = 2 * NP;     // K: products of 64 for a page
-    constexpr int U = NP <= 2 ? 4 : 2;                               // groups of 16 pages whose bounds are on their way together
+    constexpr int U = 2;                               // groups of 16 pages whose bounds are on their way together
     constexpr int kColumns = (16 + kWaves - 1) / kWaves;             // columns whose q a wave turns to codes
     const int l = lane_id(), w = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), n16 = l & 15, g = l >> 4;
     const int hd = A.c.head_dim, RP = A.RP;
