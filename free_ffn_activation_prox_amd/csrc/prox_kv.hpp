@@ -186,6 +186,25 @@ __device__ __forceinline__ bool kv_pair_of(const prox_kv_batch& b, int i, int la
     return false;
 }
 
+// Arrival of `part` of `parts` blocks, by the first wave of each behind a barrier
+// that follows its block's last (coherent, completed) store: whether all have
+// arrived.  Every block sets a flag of its own and then looks at all of them, so
+// the last one sees them all (another that sees them too does the same work over
+// again, with the same result), and whoever does clears them: a call leaves its
+// flags clear, and a replayed graph may go by one tag.  A counter that blocks move
+// by compare-and-swap has them wait for each other: 16 blocks up to 14 us.
+__device__ __forceinline__ bool kv_arrive(unsigned long long* flags, uint32_t tag, int part, int parts, int lane) {
+    const unsigned long long mark = (unsigned long long)tag << 32 | 0x9e3779b9u;
+    if (lane == 0) __hip_atomic_store(flags + part, mark, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    bool all = true;
+    for (int i = lane; i < parts; i += 64)
+        all = all && __hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == mark;
+    all = __ballot(all) == ~0ull;
+    for (int i = lane; all && i < parts; i += 64) __hip_atomic_store(flags + i, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return all;
+}
+
 // Sequence s and page j of it for pair i of the grid (see page_pairs).
 __device__ __forceinline__ bool pair_of(const prox_kv_batch& b, int pp, int i, int lane, int& s, int& j) {
     if (pp == 0) return kv_pair_of(b, i, lane, s, j);

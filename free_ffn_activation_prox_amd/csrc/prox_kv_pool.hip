@@ -29,7 +29,7 @@ struct PoolArgs {
     int n_rows;
     int chunks;                     // of kChunk4 entries in a table row
     uint32_t tag;
-    // workspace: arrivals; what a sequence begins the call with and the first of its new pages in `list`;
+    // workspace: arrivals of blocks; what a sequence begins the call with and the first of its new pages in `list`;
     // a bit for each page, set where it is free; the pages given, in order
     unsigned long long* arrived;
     int32_t *start, *from;
@@ -344,7 +344,10 @@ __global__ void __launch_bounds__(kPoolThreads) k_kv_pages_move(PoolArgs A) {
         take_and_give_back<__HIP_MEMORY_SCOPE_AGENT>(A, s, m, c * kChunk4, l);
     }
     all_done();
-    if (threadIdx.x == 0) last_s = tile_arrive(A.arrived, A.tag, (int)gridDim.x);
+    if (w == 0) {
+        const bool last = kv_arrive(A.arrived, A.tag, blockIdx.x, gridDim.x, l);
+        if (l == 0) last_s = last;
+    }
     __syncthreads();
     if (last_s) number_pages<true>(A);
 }
@@ -360,11 +363,17 @@ __global__ void __launch_bounds__(256) k_kv_pages_fill(PoolArgs A) {
     clear_rows(A, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x, (int64_t)gridDim.x * gridDim.y * 256);
 }
 
+// Most blocks of k_kv_pages_move.
+int pool_blocks(const prox_kv_pool& p) {
+    const int64_t units = (int64_t)p.n_seq * ((p.max_pages + kChunk4 - 1) / kChunk4);
+    return (int)std::min((units + kPoolWaves - 1) / kPoolWaves, (int64_t)2 * device_cus());
+}
+
 // Parts of the workspace, in 32-bit words.
 struct PoolSpace {
     size_t start, from, free, list, words;
     explicit PoolSpace(const prox_kv_pool& p) {
-        start = 2;
+        start = 2 * (size_t)pool_blocks(p);
         from = start + (size_t)p.n_seq;
         free = from + (size_t)p.n_seq;
         list = free + ((size_t)p.n_pages + 31) / 32;
@@ -401,8 +410,7 @@ hipError_t launch_kv_pages(const prox_kv_pool& p, const int32_t* want, const int
         hipLaunchKernelGGL(k_kv_pages_one, dim3(1), dim3(kPoolThreads), 0, s, A);
         return hipGetLastError();
     }
-    const int64_t blocks = std::min((units + kPoolWaves - 1) / kPoolWaves, (int64_t)2 * device_cus());
-    hipLaunchKernelGGL(k_kv_pages_move, dim3((uint32_t)blocks), dim3(kPoolThreads), 0, s, A);
+    hipLaunchKernelGGL(k_kv_pages_move, dim3((uint32_t)pool_blocks(p)), dim3(kPoolThreads), 0, s, A);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // rows of one sequence go to several blocks where there are few sequences

@@ -29,15 +29,17 @@ struct Listed {
     static constexpr int kBytes = kKvPage * 64 * NP;
     const Attend& A;
     const int32_t *list, *table;
+    int first;                     // entry `lane` of the list
     int head, upto, base, at_page, id, ve;
     float ks, vl;
-    __device__ __forceinline__ Listed(const Attend& a, const int32_t* lst, const int32_t* tab, int hd, int from, int up, int l)
-        : A(a), list(lst), table(tab), head(hd), upto(up) {
+    __device__ __forceinline__ Listed(const Attend& a, const int32_t* lst, int first64, const int32_t* tab, int hd, int from, int up, int l)
+        : A(a), list(lst), table(tab), first(first64), head(hd), upto(up) {
         look(from, l);
     }
     __device__ __forceinline__ void look(int e, int l) {
         base = e;
-        at_page = list[min(e + l, upto - 1)];
+        const int i = min(e + l, upto - 1);
+        at_page = upto <= 64 ? __shfl(first, i) : list[i];
         id = table[at_page];
         id = e + l < upto && id >= 0 && id < A.c.n_pages ? id : -1;
         const float k0 = A.c.k_scale[where(id)], v0 = A.c.v_scale[where(id)];
@@ -76,17 +78,20 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_selected(Se
     const int l = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), n = l & 15, g = l >> 4;
     const int unit = (int)(blockIdx.x / (uint32_t)S.parts), part = (int)(blockIdx.x % (uint32_t)S.parts);
     const int row = unit / A.VH, vh = unit - row * A.VH, head = vh / S.groups, h0 = (vh - head * S.groups) * A.HG;
+    // the list is on its way while the row's sequence is found
+    const int32_t* list = S.pages + ((size_t)row * A.c.n_kv + head) * (size_t)S.keep;
+    const int first = list[min(l, S.keep - 1)];
     const int s = kv_seq_of(A.b, row, l), hd = A.c.head_dim;
     const KvRows R = kv_rows(A.b, s);
     if (row < R.q0 || row >= R.q0 + R.rows) return;
     const int pos = R.first + row - R.q0;
     const bool sees = pos >= 0 && pos < A.b.max_pages * kKvPage;
-    const int32_t* list = S.pages + ((size_t)row * A.c.n_kv + head) * (size_t)S.keep;
     // entries that count: up to the first that is not above the one before it, or behind the row's own page
     const int own = pos >> 6;
     int count = 0;
     for (int e = 0; sees && count == e && e < S.keep; e += 64) {
-        const int i = min(e + l, S.keep - 1), page = list[i], before = i > 0 ? list[i - 1] : -1;
+        const int i = min(e + l, S.keep - 1), page = e == 0 ? first : list[i];
+        const int left = __shfl_up(page, 1), before = l > 0 ? left : e > 0 ? list[e - 1] : -1;
         const uint64_t m = ~__ballot(e + l < S.keep && page > before && page <= own);
         count = e + (m ? __builtin_ctzll(m) : 64);
     }
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_selected(Se
     const bool mine = from < upto;
     if (l == 0) some_s[wv] = mine;
     if (mine) {
-        Listed<NP> pages(A, list, A.b.block_table + (size_t)s * A.b.max_pages, head, from, upto, l);
+        Listed<NP> pages(A, list, first, A.b.block_table + (size_t)s * A.b.max_pages, head, from, upto, l);
         Rows<KIND, NP, 1> w;
         w.live[0] = n < A.HG && h0 + n < A.rep;
         w.key_lo[0] = 0;
@@ -149,7 +154,10 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_selected(Se
     if (S.parts == 1) return;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");               // this wave's stores have completed
     __syncthreads();
-    if (threadIdx.x == 0) last_s = tile_arrive(A.arrived + unit, A.tag, S.parts);
+    if (wv == 0) {
+        const bool last = kv_arrive(A.arrived + (size_t)unit * S.parts, A.tag, part, S.parts, l);
+        if (l == 0) last_s = last;
+    }
     __syncthreads();
     if (!last_s) return;
     for (int e = threadIdx.x; e < lanes; e += blockDim.x) {
@@ -171,6 +179,10 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_selected(Se
     }
 }
 
+// Waves of a block where there are blocks for every CU twice: shorter prologues and joins among more pages, and
+// three blocks a CU (64 channels; 1000 rows of 28 / 4 heads and 48 pages 139 us, with 8 waves 185, with 2 140).
+constexpr int kFewWaves = 4;
+
 // How a call is split (host).
 struct SelectedSplit {
     int groups, HG, VH, parts, waves;
@@ -185,23 +197,22 @@ SelectedSplit selected_split(const prox_kv_cache& c, int n_tokens, int n_heads, 
     p.groups = (rep + 15) / 16;
     p.HG = (rep + p.groups - 1) / p.groups;
     p.VH = c.n_kv * p.groups;
-    p.waves = few_waves(NP);
     p.units = (int64_t)n_tokens * p.VH;
+    p.waves = p.units >= 2 * device_cus() ? kFewWaves : few_waves(NP);
     // enough blocks for the chip, as long as each wave has an entry
     const int64_t want = (device_cus() + p.units - 1) / p.units, most = (keep + p.waves - 1) / p.waves;
     p.parts = (int)std::min(want, most);
     const size_t row = (size_t)(c.head_pad + 4) * sizeof(float);
     p.lds = (size_t)p.waves * p.HG * row;
-    p.part_at = align_up((size_t)p.units * sizeof(unsigned long long), 256);
+    p.part_at = align_up((size_t)p.units * p.parts * sizeof(unsigned long long), 256);
     p.part_bytes = p.parts > 1 ? (size_t)p.units * p.parts * p.HG * row : 0;
     p.fits = p.units * p.parts <= 0x7fffffffll;
     p.bytes = align_up(p.parts > 1 ? p.part_at + p.part_bytes : 0, 256) + 256;
     return p;
 }
 
-template <int KIND, int NP>
+template <int KIND, int NP, int kWaves>
 hipError_t selected_launch(const Selected& S, const SelectedSplit& p, hipStream_t s) {
-    constexpr int kWaves = few_waves(NP);
     if (p.lds > 48 * 1024) {
         const hipError_t e = hipFuncSetAttribute((const void*)k_kv_selected<KIND, NP, kWaves>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
@@ -211,13 +222,19 @@ hipError_t selected_launch(const Selected& S, const SelectedSplit& p, hipStream_
     return hipGetLastError();
 }
 
+template <int KIND, int NP>
+hipError_t selected_np(const Selected& S, const SelectedSplit& p, hipStream_t s) {
+    if (p.waves == kFewWaves) return selected_launch<KIND, NP, kFewWaves>(S, p, s);
+    return selected_launch<KIND, NP, few_waves(NP)>(S, p, s);
+}
+
 template <int KIND>
 hipError_t selected_kind(const Selected& S, const SelectedSplit& p, hipStream_t s) {
     switch (S.A.c.head_pad / 64) {
-        case 1: return selected_launch<KIND, 1>(S, p, s);
-        case 2: return selected_launch<KIND, 2>(S, p, s);
-        case 3: return selected_launch<KIND, 3>(S, p, s);
-        default: return selected_launch<KIND, 4>(S, p, s);
+        case 1: return selected_np<KIND, 1>(S, p, s);
+        case 2: return selected_np<KIND, 2>(S, p, s);
+        case 3: return selected_np<KIND, 3>(S, p, s);
+        default: return selected_np<KIND, 4>(S, p, s);
     }
 }
 
