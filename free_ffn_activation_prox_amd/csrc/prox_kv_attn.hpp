@@ -1045,13 +1045,14 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_attend(AT A
                         }
                     } else if (w.live[u]) {
                         const uint32_t at = part_at(blockIdx.x, from == 0, r);
+                        constexpr int kAux = AT::kJoinLater ? 0 : kCoherent;
 #pragma unroll
                         for (int d = 0; d < 4 * NP; ++d)
                             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, w.o[u][d]), rp,
-                                                                   (int)(at + 4 * (16 * d + 4 * g)), 0, kCoherent);
+                                                                   (int)(at + 4 * (16 * d + 4 * g)), 0, kAux);
                         if (g == 0)
                             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, packed(w.part(u))), rp,
-                                                                   (int)(at + 256 * NP), 0, kCoherent);
+                                                                   (int)(at + 256 * NP), 0, kAux);
                     }
                 }
             }
@@ -1236,11 +1237,13 @@ constexpr int kRowWaves = 8;
 // a * b, or anything above 2^62, of numbers up to 2^62
 int64_t times(int64_t a, int64_t b) { return a > 0 && b > (1ll << 62) / a ? (1ll << 62) + 1 : a * b; }
 
-// For n_tokens rows in sequences of up to max_q tokens.
-[[maybe_unused]] Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int64_t n_tokens, int max_q) {
+// For n_tokens rows in sequences of up to max_q tokens; usual: rows that a sequence has in the mean, where max_q is
+// but a bound (0: max_q decides).
+[[maybe_unused]] Split split_of(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads, int64_t n_tokens, int max_q,
+                                int64_t usual = 0) {
     Split p;
     const int rep = n_heads / c.n_kv, NP = c.head_pad / 64;
-    const int64_t most_rows = (int64_t)max_q * rep;
+    const int64_t most_rows = usual > 0 ? usual : (int64_t)max_q * rep;
     // More than 16 rows get tiles with rows for each wave: sequences of up to 6 tokens and 7 query heads a
     // key head take 27 us so, and 41 in tiles of 16 rows, each of which reads the pages again.  (Up to 128 rows
     // leave most of the 8 waves without any: 64 single tokens with 32 query heads on one key head take 47 us.)
