@@ -82,6 +82,9 @@ def main(argv=None):
     ap.add_argument("--context", type=int, default=512, help="--decode: tokens already in the KV cache")
     ap.add_argument("--kv-cache", default="dense", choices=["dense", "int8", "fp8"],
                     help="--decode: the bf16 cache and torch's attention, or the paged 8-bit cache and its kernels")
+    ap.add_argument("--kv-keep", type=int, default=0,
+                    help="--decode with a paged cache: pages of 64 tokens that a step's attention reads, selected by "
+                         "bounds of their keys (0: all)")
     ap.add_argument("--copy-calibration", type=int, default=0, metavar="MIB",
                     help="only run a plain device copy of MIB MiB, --steps times (the reference "
                          "for scaling hardware byte counters)")
@@ -456,6 +459,8 @@ def decode_bench(args):
     # room for the warm-up, the eager steps and (the paged cache, whose captured
     # step goes on by a token) as many replays
     kw = dict(max_ctx=args.context + 2 * args.steps + args.warmup + 2, cache=args.kv_cache)
+    if args.kv_keep:
+        kw["keep_pages"] = args.kv_keep
     if args.kv_cache == "dense":
         kw["max_ctx"] = args.context + args.steps + args.warmup + 1
     variants = {"dense": DecodeHarness(sh, layers, ffn="dense", **kw)}
@@ -506,7 +511,7 @@ def decode_bench(args):
            "higher_is_better": False, "steps": args.steps, "warmup": args.warmup,
            "config": {"workload": f"decode: 32 layers d=4096 d_ff=11008 heads=32 context={args.context} "
                                   f"batch=1; Prox FFN int8 proxy keep=60% sparsity=70% (k_in={k_in} k_ff={k_ff})",
-                      "kv_cache": args.kv_cache},
+                      "kv_cache": args.kv_cache, **({"kv_keep": args.kv_keep} if args.kv_keep else {})},
            "ms_per_step": {k: round(v, 4) for k, v in ms_graph.items()},
            "speedup_vs_dense": {k: round(ms_graph["dense"] / v, 3) for k, v in ms_graph.items() if k != "dense"},
            "speedup_vs_dense_library": {k: round(ms_graph["dense_library"] / v, 3) for k, v in ms_graph.items()

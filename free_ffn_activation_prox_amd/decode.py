@@ -23,6 +23,13 @@ and append in one call, attention over the pages in another, for one or more
 sequences, and prompts (``prefill``) besides single tokens.  The sequences'
 lengths are kept on the device, so a captured step goes on by a token with
 every replay.
+
+With keep_pages a step's attention reads that many pages of each sequence and
+key head, those whose keys can give the largest scores by the bounds that the
+harness keeps of every page (prompts see all pages).  With n_pages the sequences
+take their pages from a pool of that many instead of each having its own share,
+and may begin with a prompt in common (``share_prefix``): its pages are held once
+and read once a step for all of them.
 """
 
 from __future__ import annotations
@@ -34,8 +41,10 @@ from typing import List, Optional
 import numpy as np
 import torch
 
-from . import (KV_PAGE, KVBatch, KVCache, Weights, alloc_kv_workspace, alloc_workspace, build_proxy, build_qweights,
-               ffn_forward, kv_append, kv_attention)
+from . import (KV_PAGE, KVBatch, KVCache, KVPool, Weights, alloc_kv_bounds, alloc_kv_select_workspace,
+               alloc_kv_selected_workspace, alloc_kv_shared_workspace, alloc_kv_workspace, alloc_workspace, build_proxy,
+               build_qweights, ffn_forward, kv_append, kv_attention, kv_attention_selected, kv_attention_shared,
+               kv_page_bounds, kv_pages, kv_select)
 
 EPS = 1e-5
 THETA = 10000.0
@@ -63,11 +72,17 @@ class DecodeHarness:
     (wd row j = W_down[j, :]).  ``ffn``: "dense" | "prox" | "q8" | "exact".
     ``cache``: "dense" (bf16, one sequence) or the paged 8-bit cache, "int8" |
     "fp8", of ``n_seq`` sequences; layers may then have g_q, g_k [hd], the gains
-    of a norm of every head of q and k before the rotation."""
+    of a norm of every head of q and k before the rotation.  ``keep_pages`` and
+    ``n_pages`` (paged cache only): see above."""
 
     def __init__(self, shape: DecoderShape, layers: List[dict], max_ctx: int, ffn: str = "prox",
                  proxy: str = "int8", k_in: Optional[int] = None, k_ff: Optional[int] = None, device="cuda",
-                 cache: str = "dense", n_seq: int = 1):
+                 cache: str = "dense", n_seq: int = 1, keep_pages: Optional[int] = None,
+                 n_pages: Optional[int] = None):
+        if cache == "dense" and (keep_pages is not None or n_pages is not None):
+            raise ValueError("keep_pages and n_pages need the paged cache (cache='int8' or 'fp8')")
+        if keep_pages is not None and keep_pages < 2:
+            raise ValueError("keep_pages must be at least 2: the first page and the last")
         if cache == "dense" and (n_seq != 1 or any("g_q" in L or "g_k" in L for L in layers)):
             raise ValueError("the dense cache holds one sequence and has no norm of q and k: use cache='int8' or 'fp8'")
         self.cache, self.n_seq = cache, n_seq
@@ -80,9 +95,9 @@ class DecodeHarness:
         self.wqkv = [torch.cat([L["wq"], L["wk"], L["wv"]], 0).contiguous() for L in layers]
         # rotary factors e^{i pos theta^(-2i/hd)} per position; the query's
         # carry the attention scale 1/sqrt(hd)
-        n_pages = -(-max_ctx // KV_PAGE)
+        width = -(-max_ctx // KV_PAGE)
         i = torch.arange(hd // 2, dtype=torch.float64)
-        ang = torch.arange(max_ctx if cache == "dense" else n_pages * KV_PAGE, dtype=torch.float64)[:, None] * (THETA ** (-2.0 * i / hd))[None, :]
+        ang = torch.arange(max_ctx if cache == "dense" else width * KV_PAGE, dtype=torch.float64)[:, None] * (THETA ** (-2.0 * i / hd))[None, :]
         rot = torch.polar(torch.ones_like(ang), ang)
         self.rot_k = rot.to(torch.complex64).to(device)
         self.rot_q = (rot / math.sqrt(hd)).to(torch.complex64).to(device)
@@ -94,15 +109,29 @@ class DecodeHarness:
             self.Kt = [torch.zeros(shape.n_kv, hd, max_ctx, dtype=torch.bfloat16, device=device) for _ in layers]
             self.V = [torch.zeros(shape.n_kv, max_ctx, hd, dtype=torch.bfloat16, device=device) for _ in layers]
         else:
-            self.kv = [KVCache.alloc(cache, n_seq * n_pages, shape.n_kv, hd, device) for _ in layers]
+            self.kv = [KVCache.alloc(cache, n_seq * width if n_pages is None else n_pages, shape.n_kv, hd, device) for _ in layers]
             dev = self.kv[0].device
             self.g_q = [L["g_q"].float() if "g_q" in L else None for L in layers]
             self.g_k = [L["g_k"].float() if "g_k" in L else None for L in layers]
-            self.table = torch.arange(n_seq * n_pages, dtype=torch.int32, device=dev).view(n_seq, n_pages)
-            self.ctx = torch.zeros(n_seq, dtype=torch.int32, device=dev)   # tokens of each sequence
+            self.pool = None if n_pages is None else KVPool.alloc(n_pages, n_seq, width, dev)
+            if self.pool is None:
+                self.table = torch.arange(n_seq * width, dtype=torch.int32, device=dev).view(n_seq, width)
+                self.ctx = torch.zeros(n_seq, dtype=torch.int32, device=dev)   # tokens of each sequence
+            else:
+                self.table, self.ctx = self.pool.block_table, self.pool.ctx_len
+                self.want = torch.zeros_like(self.ctx)
+                self.start = torch.zeros(n_seq + 1, dtype=torch.int32, device=dev)
+                self.slots, self.status = torch.zeros_like(self.ctx), torch.zeros(2, dtype=torch.int32, device=dev)
             self.lengths = [0] * n_seq           # the same on the host (a replayed graph does not move it)
+            self.prefix = 0                      # pages that all sequences share
             self.one = KVBatch(self.ctx, self.table)
             self.kv_ws = alloc_kv_workspace(self.kv[0], self.one, shape.n_heads)
+            self.keep_pages = keep_pages
+            if keep_pages is not None:
+                self.bounds = [alloc_kv_bounds(kv) for kv in self.kv]
+                self.picked = torch.empty(n_seq, shape.n_kv, keep_pages, dtype=torch.int32, device=dev)
+                self.pick_ws = alloc_kv_select_workspace(self.kv[0], self.one, shape.n_heads)
+                self.kv_ws = alloc_kv_selected_workspace(self.kv[0], self.one, shape.n_heads, keep_pages)
         self.pos = 0
         if ffn != "dense":
             kind = "exact" if ffn == "exact" else proxy
@@ -122,14 +151,24 @@ class DecodeHarness:
             if n > self.max_ctx:
                 raise ValueError(f"{n} tokens do not fit the cache's {self.max_ctx} positions")
             self.lengths = [0] * self.n_seq
+            if self.prefix:
+                self.prefix = 0
+                if self.keep_pages is None:
+                    self.kv_ws = alloc_kv_workspace(self.kv[0], self.one, self.shape.n_heads)
             self._grow(range(self.n_seq), n)
-            self.ctx.fill_(n)
             T = self.n_seq * n
+            if self.pool is None:
+                self.ctx.fill_(n)
+            else:
+                kv_pages(self.pool, torch.zeros_like(self.ctx), 0)
+                kv_pages(self.pool, torch.full_like(self.ctx, n), T)
             start = torch.arange(0, T + 1, n, dtype=torch.int32, device=self.ctx.device) if n else torch.zeros_like(self.ctx)
             batch = KVBatch(self.ctx, self.table, start, n_tokens=T, max_q=n) if n else None
-            for kv in self.kv if n else ():
+            for li, kv in enumerate(self.kv if n else ()):
                 k, v = (torch.randn(T, kv.n_kv, kv.head_dim, generator=g).to(torch.bfloat16).to(kv.device) for _ in range(2))
                 kv_append(kv, batch, k, v)
+                if self.keep_pages is not None:
+                    kv_page_bounds(kv, batch, self.bounds[li])
             return
         for Kt, V in zip(self.Kt, self.V):
             Kt[:, :, :n] = torch.randn(Kt[:, :, :n].shape, generator=g).to(Kt.dtype).to(Kt.device)
@@ -156,9 +195,52 @@ class DecodeHarness:
         """n more tokens of the sequences `seqs`, on the host's count."""
         if max(self.lengths[s] for s in seqs) + n > self.max_ctx:
             raise ValueError(f"{n} more tokens do not fit the cache's {self.max_ctx} positions")
+        if self.pool is not None:
+            pages = sum(-(-(m + n * (s in seqs)) // KV_PAGE) for s, m in enumerate(self.lengths)) - self.prefix * (self.n_seq - 1)
+            if pages > self.pool.n_pages:
+                raise ValueError(f"{n} more tokens need {pages} pages of a pool of {self.pool.n_pages}")
         for s in seqs:
             self.lengths[s] += n
         self.pos = max(self.lengths)
+
+    def share_prefix(self, x: torch.Tensor) -> torch.Tensor:
+        """A prompt that every sequence begins with, x fp32 [tokens][d]: through
+        the layers once, as that of sequence 0; the others, which must be empty,
+        begin with its whole pages, and a step reads these once for all.  Returns
+        what prefill returns; the prompt's tokens behind its last whole page are
+        sequence 0's alone."""
+        if self.cache == "dense" or self.pool is None:
+            raise ValueError("share_prefix needs a pool of pages (n_pages)")
+        if any(self.lengths):
+            raise ValueError("share_prefix needs empty sequences")
+        y = self.prefill(x, 0)
+        pages = x.shape[0] // KV_PAGE
+        if pages and self.n_seq > 1:
+            dev = self.ctx.device
+            want = torch.full_like(self.ctx, pages * KV_PAGE)
+            want[0] = x.shape[0]
+            parent, shared = torch.zeros_like(want), torch.full_like(want, pages)
+            parent[0] = -1
+            kv_pages(self.pool, want, 0, parent=parent, shared=shared)
+            self.lengths = [x.shape[0]] + [pages * KV_PAGE] * (self.n_seq - 1)
+            self.prefix = pages
+            self.shared = torch.full((1,), pages, dtype=torch.int32, device=dev)
+            if self.keep_pages is None:
+                self.kv_ws = alloc_kv_shared_workspace(self.kv[0], self.one, self.shape.n_heads)
+        return y
+
+    def _attend(self, li: int, q: torch.Tensor, batch: KVBatch, workspace) -> torch.Tensor:
+        kv = self.kv[li]
+        if self.keep_pages is not None:
+            kv_page_bounds(kv, batch, self.bounds[li])
+        if batch is not self.one:
+            return kv_attention(q, kv, batch, workspace=workspace)
+        if self.keep_pages is not None:
+            pages = kv_select(q, kv, batch, self.bounds[li], self.keep_pages, pages=self.picked, workspace=self.pick_ws)
+            return kv_attention_selected(q, kv, batch, pages, workspace=workspace)
+        if self.prefix:
+            return kv_attention_shared(q, kv, batch, self.shared, workspace=workspace)
+        return kv_attention(q, kv, batch, workspace=workspace)
 
     def _paged(self, x: torch.Tensor, batch: KVBatch, workspace) -> torch.Tensor:
         """x fp32 [rows][d], the batch's rows, through every layer over the paged cache."""
@@ -169,7 +251,7 @@ class DecodeHarness:
             qkv = torch.nn.functional.linear(a, self.wqkv[li]).view(T, H + 2 * KV, hd)
             q, k, v = qkv.split([H, KV, KV], 1)
             q = kv_append(self.kv[li], batch, k, v, rot=self.rot_k, q=q, g_q=self.g_q[li], g_k=self.g_k[li], eps=EPS)
-            att = kv_attention(q, self.kv[li], batch, workspace=workspace)
+            att = self._attend(li, q, batch, workspace)
             x = x + torch.nn.functional.linear(att.view(T, d), L["wo"])
             f_in = self._rmsnorm(x, self.g_ffn[li])
             f_out = self._ffn(li, f_in)
@@ -192,9 +274,15 @@ class DecodeHarness:
         out = []
         for p in x.split(MAX_PREFILL) if x.shape[0] else ():
             T = p.shape[0]
-            self.ctx[seq:seq + 1].add_(T)
-            start = torch.tensor([0, T], dtype=torch.int32, device=self.ctx.device)
-            batch = KVBatch(self.ctx[seq:seq + 1], self.table[seq:seq + 1], start, n_tokens=T, max_q=T)
+            if self.pool is None:
+                self.ctx[seq:seq + 1].add_(T)
+                start = torch.tensor([0, T], dtype=torch.int32, device=self.ctx.device)
+                batch = KVBatch(self.ctx[seq:seq + 1], self.table[seq:seq + 1], start, n_tokens=T, max_q=T)
+            else:
+                want = self.ctx.clone()
+                want[seq:seq + 1].add_(T)
+                start, _, _ = kv_pages(self.pool, want, T)
+                batch = KVBatch(self.ctx, self.table, start, n_tokens=T, max_q=T)
             out.append(self._paged(p, batch, alloc_kv_workspace(self.kv[0], batch, self.shape.n_heads)))
         return torch.cat(out) if out else x
 
@@ -204,7 +292,11 @@ class DecodeHarness:
             if x.shape != (self.n_seq, self.shape.d):
                 raise ValueError("x must be [n_seq][d]")
             self._grow(range(self.n_seq), 1)
-            self.ctx.add_(1)
+            if self.pool is None:
+                self.ctx.add_(1)
+            else:
+                torch.add(self.ctx, 1, out=self.want)
+                kv_pages(self.pool, self.want, self.n_seq, q_start=self.start, slots=self.slots, status=self.status)
             return self._paged(x, self.one, self.kv_ws)
         sh, pos = self.shape, self.pos
         H, KV, hd = sh.n_heads, sh.n_kv, sh.hd
