@@ -706,7 +706,8 @@ class KVPool:
         self._c = _KVPool(self.n_pages, self.n_seq, self.max_pages, refs.data_ptr(), ctx_len.data_ptr(),
                           block_table.data_ptr())
         self._ref = ctypes.byref(self._c)
-        n = _lib.prox_kv_pages_workspace_bytes(self._ref)
+        with torch.cuda.device(self.device):
+            n = _lib.prox_kv_pages_workspace_bytes(self._ref)
         if n == 0:
             raise ValueError(f"invalid pool: {_lib.prox_last_error().decode()}")
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)

@@ -156,6 +156,21 @@ __device__ __forceinline__ int kv_seq_of(const prox_kv_batch& b, int row, int la
     return s;
 }
 
+// The same where q_start rises (else any sequence), in two looks for up to 4096
+// sequences, where the search above takes one for each 64.
+__device__ __forceinline__ int kv_seq_find(const prox_kv_batch& b, int row, int lane) {
+    if (!b.q_start) return row;
+    int s = 0, n = b.n_seq;
+    while (n > 1) {
+        const int step = (n + 63) / 64, i = lane * step;
+        const uint64_t m = __ballot(i < n && b.q_start[s + min(i, n - 1)] <= row);
+        const int on = max(__builtin_popcountll(m) - 1, 0) * step;
+        s += on;
+        n = min(step, n - on);
+    }
+    return s;
+}
+
 // Sequence and page (counted from the first that the sequence's tokens touch)
 // of the i-th such pair of the batch, found by a whole wave at once; false
 // behind the last pair.  A sequence with rows has one pair at least.

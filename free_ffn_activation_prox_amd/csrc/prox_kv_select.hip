@@ -12,6 +12,14 @@
 // are kept does not depend on how a kernel orders its sums.  The key of a page
 // for the query heads h of a key head is
 //   fl32(max_h fl32(dot_h unit_h) page_scale).
+//
+// What bounds it (kernel times): bounds of 32768 tokens and 8 heads of 128 channels
+// 9.3 us (34.6 MB, 3.7 TB/s: memory).  Selection is a chain of loads (row, table,
+// bounds) and of steps of one wave: 32 of up to 512 pages for 64 ragged sequences
+// 14.8 us (7.3 MB), for one token 64 of 2048 pages 7.8 + 9.2 us (4.3 MB; in one
+// launch of 8 blocks 31, of which a CU's 30 GB/s take 15), 48 of 250 pages for 1000
+// rows of 28 / 4 heads 24.3 us.  Within a block (stamps of a 64-row case): rows 1.0,
+// table and bounds 2.4, q's codes beside them, product and keys 1.9, selection 1.5.
 #include "prox_kv.hpp"
 
 namespace prox {
@@ -157,11 +165,6 @@ struct SelectArgs {
 // The tile-th group of TQ rows of the batch's sequences: sequence and first row
 // in it, found by a whole wave at once; false behind the last one.
 __device__ __forceinline__ bool tile_at(const prox_kv_batch& b, int TQ, int tile, int lane, int& s, int& i0) {
-    if (!b.q_start) {
-        s = tile;
-        i0 = 0;
-        return tile < b.n_seq;
-    }
     for (int base = 0; base < b.n_seq; base += 64) {
         int upto = base + lane < b.n_seq ? (max(kv_rows(b, base + lane).rows, 0) + TQ - 1) / TQ : 0;
         const int n = upto;
@@ -243,8 +246,6 @@ __device__ __forceinline__ void page_keys(const SelectArgs& A, uint32_t* keys, u
     };
     const int p_first = from + 16 * U * w;
     for (int h0 = 0; h0 < A.rep; h0 += 16) {
-        if (p_first < most) load(p_first);
-        __syncthreads();
         uint2 x2[kColumns];
 #pragma unroll
         for (int k = 0; k < kColumns; ++k) {
@@ -252,6 +253,10 @@ __device__ __forceinline__ void page_keys(const SelectArgs& A, uint32_t* keys, u
             const uint16_t* src = A.q + (int64_t)(R.q0 + i0 + min(c / RP, rows - 1)) * A.qs + (int64_t)(head * A.rep + h) * hd;
             x2[k] = 4 * l < hd ? *reinterpret_cast<const uint2*>(src + 4 * l) : make_uint2(0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);                           // q first: it is turned to codes while the bounds come
+        if (p_first < most) load(p_first);
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < kColumns; ++k) {
             const int c = w + k * kWaves;
@@ -547,9 +552,17 @@ struct SelectTile {
     const int32_t* table;
     __device__ __forceinline__ SelectTile(const SelectArgs& A, int unit, int l) : head(unit % A.c.n_kv), i0(0), rows(0), most(0), table(nullptr) {
         int s;
-        if (!tile_at(A.b, A.TQ, unit / A.c.n_kv, l, s, i0)) return;
-        R = kv_rows(A.b, s);
-        rows = min(R.rows - i0, A.TQ);
+        const int tile = unit / A.c.n_kv;
+        if (A.TQ == 1) {                                             // tiles are rows
+            s = kv_seq_find(A.b, tile, l);
+            R = kv_rows(A.b, s);
+            i0 = tile - R.q0;
+            rows = i0 >= 0 && i0 < R.rows ? 1 : 0;
+        } else {
+            if (!tile_at(A.b, A.TQ, tile, l, s, i0)) return;
+            R = kv_rows(A.b, s);
+            rows = min(R.rows - i0, A.TQ);
+        }
         table = A.b.block_table + (size_t)s * A.b.max_pages;
         for (int i = 0; i < rows; ++i) most = max(most, sees(A, i));
     }
@@ -716,8 +729,7 @@ struct SelectSplit {
         const int max_q = std::max(std::min(b.q_start ? b.max_q : 1, b.n_tokens), 1);
         TQ = row_pages > 2048 ? 1 : std::min(16 / RP, pow2_up(max_q));
         while (TQ > 1 && TQ * row_pages > 8192) TQ /= 2;
-        const int64_t tiles = b.q_start ? std::min((int64_t)b.n_seq * ((max_q - 1) / TQ + 1), (int64_t)b.n_tokens / TQ + b.n_seq)
-                                        : b.n_seq;
+        const int64_t tiles = TQ == 1 ? b.n_tokens : std::min((int64_t)b.n_seq * ((max_q - 1) / TQ + 1), (int64_t)b.n_tokens / TQ + b.n_seq);
         units = tiles * c.n_kv;
         const int64_t want = kBlocksPerCu * device_cus() / units, most = (row_pages + kLeastRun - 1) / kLeastRun;
         parts = (int)std::max<int64_t>(std::min(want, most), 1);

@@ -9,6 +9,12 @@
 // blocks.  The waves of a block meet in LDS; parts of several blocks meet in the
 // workspace, where the block that arrives last joins them in order, so results
 // do not depend on timing.
+//
+// What bounds it (kernel times): one token, 64 / 8 heads x 128, 64 pages 11.2 us
+// (8.4 MB: latency); 64 ragged sequences, 32 / 8 heads x 128, e4m3, 32 pages 25.6 us
+// (105 MB at 4.1 TB/s: memory); 1000 rows, 28 / 4 heads x 64, 48 pages 133 us: some
+// 300 vector instructions for each page and wave, codes to fp16 and weights, of
+// whose 16 columns 7 are in use.
 #include "prox_kv_attn.hpp"
 
 namespace prox {
@@ -81,7 +87,7 @@ __global__ void __launch_bounds__(64 * kWaves, NP <= 2 ? 2 : 1) k_kv_selected(Se
     // the list is on its way while the row's sequence is found
     const int32_t* list = S.pages + ((size_t)row * A.c.n_kv + head) * (size_t)S.keep;
     const int first = list[min(l, S.keep - 1)];
-    const int s = kv_seq_of(A.b, row, l), hd = A.c.head_dim;
+    const int s = kv_seq_find(A.b, row, l), hd = A.c.head_dim;
     const KvRows R = kv_rows(A.b, s);
     if (row < R.q0 || row >= R.q0 + R.rows) return;
     const int pos = R.first + row - R.q0;

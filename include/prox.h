@@ -465,7 +465,8 @@ prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want, const int3
  * those of every page that the batch's tokens lie in, from all tokens of the page
  * up to the sequence's last one; it is called behind prox_kv_append (which may
  * round a page's codes again) with the same batch, or once over whole sequences.
- * bounds: device, 16-byte aligned. */
+ * A page that several of the batch's sequences hold is taken to be full in all of
+ * them.  bounds: device, 16-byte aligned. */
 prox_status prox_kv_page_bounds(const prox_kv_cache* c, const prox_kv_batch* b, void* bounds, void* stream);
 
 /* Workspace bytes of prox_kv_select for this cache, batch (n_seq, n_tokens, max_q and

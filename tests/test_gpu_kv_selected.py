@@ -68,6 +68,25 @@ def test_against_oracle(kind, H, KV, hd):
     attend(w, [1, 1, 0, 0], keep=3, scale=0.0)
 
 
+def test_many_sequences_with_empty_ones_between():
+    """Selection and attention where a row's sequence is one of hundreds, of which many have no rows."""
+    n = 333
+    w = World("int8", 4, 2, 64, [200] * n, seed=27)
+    settle(w, [int(x) for x in w.rng.integers(1, 200, n)])
+    full, _ = w.batch([int(c) for c in w.ctx], advance=False)
+    bnd = w.P.kv_page_bounds(w.c, full, w.P.alloc_kv_bounds(w.c))
+    for most in (1, 3):
+        new = [int(min(c, x)) for c, x in zip(w.ctx, w.rng.integers(-1, most + 1, n).clip(0))]
+        b, start = w.batch(new, advance=False, pad=5)
+        q = w.rows(b.n_tokens, 4, 1.5)
+        pages = torch.full((b.n_tokens, 2, 2), -7, dtype=torch.int32, device="cuda")
+        w.P.kv_select(q, w.c, b, bnd, 2, first=0, pages=pages)
+        exp = np.full((b.n_tokens, 2, 2), -7, np.int32)
+        OO.select(w.o, w.table, w.ctx, start, b.max_q, f64(q), bnd.cpu().numpy(), 2, 0, 1, exp)
+        assert np.array_equal(pages.cpu().numpy(), exp)
+        attend(w, new, pages=exp, q=q, pad=5)
+
+
 def test_without_q_start_and_more_entries_than_pages():
     w = World("int8", 8, 2, 128, [900, 100, 500], seed=8)
     settle(w, [900, 100, 500])
