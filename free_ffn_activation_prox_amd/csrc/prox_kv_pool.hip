@@ -410,9 +410,11 @@ hipError_t launch_kv_pages(const prox_kv_pool& p, const int32_t* want, const int
     A.from = ws + w.from;
     A.free = reinterpret_cast<uint32_t*>(ws + w.free);
     A.list = ws + w.list;
-    const int64_t units = (int64_t)p.n_seq * A.chunks;
-    // one block up to about what it does in 20 us: a launch more costs 5
-    if (units <= 1024 && p.n_pages <= 65536 && n_rows <= 4096) {
+    // One block for a step of a token or two each, where the sequences' lanes do it all (calls back to back): 64
+    // sequences 9.5 us, in two launches 13.3; 256 sequences and 65000 pages 10.2 and 14.5; 1024 sequences 11.6 and
+    // 15.5.  Two launches where sequences begin or take pages over, which are a wave's work each: 16 sequences that
+    // end or begin with 200 to 500 tokens 13.3 us, in one block 22.4; 64 with 16 shared pages 15.6 and 72.6.
+    if (!parent && n_rows <= 2 * (int64_t)p.n_seq && p.n_seq <= 4096) {
         hipLaunchKernelGGL(k_kv_pages_one, dim3(1), dim3(kPoolThreads), 0, s, A);
         return hipGetLastError();
     }

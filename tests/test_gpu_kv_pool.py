@@ -127,6 +127,10 @@ def test_random_steps(n_pages, n_seq, max_pages, top):
         want = np.where(r.random(n_seq) < 0.3, r.integers(0, top, n_seq), want)
         par = r.integers(-1, n_seq, n_seq)
         w.move(want, parent=par, shared=r.integers(0, 6, n_seq))
+        # steps of a token or two, and back, in one block; more rows than that call says, too
+        for _ in range(3):
+            w.move(w.o.ctx + r.integers(-2, 3, n_seq), n_rows=2 * n_seq)
+        w.move(np.where(r.random(n_seq) < 0.4, 0, w.o.ctx + r.integers(0, 90, n_seq)), n_rows=n_seq)
 
 
 @pytest.mark.parametrize("n_pages,max_pages", [(200, 16), (70000, 16)])
