@@ -162,6 +162,15 @@ def test_captured_and_replayed(n_pages, max_pages):
         torch.ones(1000, device="cuda").sum().item()               # eager work between the replays
 
 
+def test_arrays_at_any_four_bytes():
+    import free_ffn_activation_prox_amd as P
+    w = Pair(301, 5, 9)
+    odd = lambda n, v: torch.full((n + 3,), v, dtype=torch.int32, device="cuda")[3:]  # noqa: E731
+    w.p = P.KVPool(odd(301, 0), odd(5, 0), odd(45, -1).view(5, 9))
+    w.move([70, 500, 0, 64, 1], q_start=odd(6, 9), slots=odd(640, 9), status=odd(2, 9), n_rows=640)
+    w.move([71, 0, 128, 64, 2], n_rows=10)
+
+
 def test_pool_feeds_append_and_attention():
     """A run of calls as a server makes them: the pool's arrays as a batch's."""
     from oracle import kv_oracle as KO
