@@ -782,9 +782,7 @@ def kv_page_bounds(cache: KVCache, batch: KVBatch, bounds, *, stream=None):
 
 def alloc_kv_select_workspace(cache: KVCache, batch: KVBatch, n_heads: int):
     """Workspace of kv_select for batches of this shape (n_seq, n_tokens, max_q, max_pages)."""
-    with torch.cuda.device(cache.device):
-        n = _lib.prox_kv_select_workspace_bytes(cache._ref, batch._ref, n_heads)
-    return _alloc_scratch(cache, n)
+    return _alloc_scratch(cache, _lib.prox_kv_select_workspace_bytes, cache._ref, batch._ref, n_heads)
 
 
 def kv_select(q, cache: KVCache, batch: KVBatch, bounds, n_keep: int, *, first: int = 1, last: int = 1, pages=None,
@@ -816,10 +814,18 @@ def kv_select(q, cache: KVCache, batch: KVBatch, bounds, n_keep: int, *, first: 
     return pages
 
 
-def _alloc_scratch(cache, n):
-    """n bytes of scratch on the cache's device, 256-byte aligned."""
+def _alloc_scratch(cache, size, *args):
+    """Scratch of size(*args) bytes on the cache's device, 256-byte aligned."""
+    if _current_device() == cache.device.index:
+        n = size(*args)
+    else:
+        with torch.cuda.device(cache.device):
+            n = size(*args)
     if n == 0:
         raise ValueError(f"no workspace for this call: {_lib.prox_last_error().decode() or 'its bounds are too large'}")
+    raw = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    if raw.data_ptr() % 256 == 0:        # as the allocator's blocks are
+        return raw
     raw = torch.empty(n + 256, dtype=torch.uint8, device=cache.device)
     off = (-raw.data_ptr()) % 256
     return raw[off: off + n]
@@ -827,9 +833,7 @@ def _alloc_scratch(cache, n):
 
 def alloc_kv_selected_workspace(cache: KVCache, batch: KVBatch, n_heads: int, n_keep: int):
     """Workspace of kv_attention_selected for batches of n_tokens rows."""
-    with torch.cuda.device(cache.device):
-        n = _lib.prox_kv_selected_workspace_bytes(cache._ref, batch._ref, n_heads, n_keep)
-    return _alloc_scratch(cache, n)
+    return _alloc_scratch(cache, _lib.prox_kv_selected_workspace_bytes, cache._ref, batch._ref, n_heads, n_keep)
 
 
 def kv_attention_selected(q, cache: KVCache, batch: KVBatch, pages, *, scale: Optional[float] = None, out=None,
@@ -864,9 +868,7 @@ def kv_attention_selected(q, cache: KVCache, batch: KVBatch, pages, *, scale: Op
 
 def alloc_kv_shared_workspace(cache: KVCache, batch: KVBatch, n_heads: int, n_groups: int = 1):
     """Workspace of kv_attention_shared for batches of this shape (n_seq, n_tokens, max_q, max_pages)."""
-    with torch.cuda.device(cache.device):
-        n = _lib.prox_kv_shared_workspace_bytes(cache._ref, batch._ref, n_heads, n_groups)
-    return _alloc_scratch(cache, n)
+    return _alloc_scratch(cache, _lib.prox_kv_shared_workspace_bytes, cache._ref, batch._ref, n_heads, n_groups)
 
 
 def kv_attention_shared(q, cache: KVCache, batch: KVBatch, shared, *, group_start=None, scale: Optional[float] = None,
