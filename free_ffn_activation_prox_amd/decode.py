@@ -29,7 +29,10 @@ key head, those whose keys can give the largest scores by the bounds that the
 harness keeps of every page (prompts see all pages).  With n_pages the sequences
 take their pages from a pool of that many instead of each having its own share,
 and may begin with a prompt in common (``share_prefix``): its pages are held once
-and read once a step for all of them.
+and read once a step for all of them.  A sequence for which the pool has no page
+left (``status`` [0] of them at the last step) keeps its tokens; its row of the
+step has no position, so it stores nothing and its attention is zeros, as where a
+step goes past max_ctx.
 """
 
 from __future__ import annotations
@@ -122,9 +125,10 @@ class DecodeHarness:
                 self.want = torch.zeros_like(self.ctx)
                 self.start = torch.zeros(n_seq + 1, dtype=torch.int32, device=dev)
                 self.slots, self.status = torch.zeros_like(self.ctx), torch.zeros(2, dtype=torch.int32, device=dev)
+                self.got, self.at = torch.zeros_like(self.ctx, dtype=torch.bool), torch.zeros_like(self.ctx)
             self.lengths = [0] * n_seq           # the same on the host (a replayed graph does not move it)
             self.prefix = 0                      # pages that all sequences share
-            self.one = KVBatch(self.ctx, self.table)
+            self.one = KVBatch(self.ctx if self.pool is None else self.at, self.table)
             self.kv_ws = alloc_kv_workspace(self.kv[0], self.one, shape.n_heads)
             self.keep_pages = keep_pages
             if keep_pages is not None:
@@ -297,6 +301,9 @@ class DecodeHarness:
             else:
                 torch.add(self.ctx, 1, out=self.want)
                 kv_pages(self.pool, self.want, self.n_seq, q_start=self.start, slots=self.slots, status=self.status)
+                # the step's row of a sequence that got no page has position -1, which does not exist
+                torch.eq(self.ctx, self.want, out=self.got)
+                torch.mul(self.ctx, self.got, out=self.at)
             return self._paged(x, self.one, self.kv_ws)
         sh, pos = self.shape, self.pos
         H, KV, hd = sh.n_heads, sh.n_kv, sh.hd

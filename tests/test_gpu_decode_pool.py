@@ -1,0 +1,81 @@
+"""The decode harness over a pool of pages where the pool ends: replayed steps that
+the host does not count, refusals, and captured steps that outlive a shared prefix.
+
+What must not change is compared code by code; outputs go by the 2e-2 bound of the
+dense harness's test, as two harnesses may cut a sequence's pages in other places."""
+
+import pytest
+import torch
+
+from test_gpu_decode_kv import SHAPE, _rel, _x
+from test_gpu_decode_ops import BOUND, _build
+
+pytestmark = pytest.mark.gpu
+D = SHAPE["d"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _capture(h, rows):
+    """A captured step of rows that the caller sets in the returned buffer; it does not run here."""
+    buf = torch.zeros(rows, D, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = h.step(buf)
+    return g, buf, out
+
+
+def _replay(g, buf, out, x):
+    buf.copy_(x)
+    g.replay()
+    torch.cuda.synchronize()
+    return out.clone()
+
+
+def _codes(h, pages=slice(None)):
+    return [t[pages].clone() for kv in h.kv for t in (kv.k, kv.v, kv.k_scale, kv.v_scale)]
+
+
+def _same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(keep_pages=3)])
+def test_replays_past_the_pool_leave_refused_sequences_as_they_are(kw):
+    h, twin = (_build(n_seq=2, n_pages=n, **kw) for n in (4, 30))
+    for g in (h, twin):
+        g.prefill(_x(62, D, 1), 0)
+        g.prefill(_x(126, D, 2), 1)
+    run = _capture(h, 2)
+    for i in range(2):                                             # 64 and 128 tokens: three whole pages
+        x = _x(2, D, 3 + i)
+        a, b = _replay(*run, x), twin.step(x)
+        assert _rel(a, b) <= BOUND
+    assert h.ctx.tolist() == [64, 128]
+    own = _codes(h, h.table[1, :2].long())
+    for i in range(3):                                             # sequence 0 takes the fourth page, 1 is refused
+        x = _x(2, D, 6 + i)
+        a, b = _replay(*run, x), twin.step(x)
+        assert _rel(a[0], b[0]) <= BOUND and torch.isfinite(a).all()
+        assert h.ctx.tolist() == [65 + i, 128] and h.status.tolist() == [1, 0]
+        assert _same(_codes(h, h.table[1, :2].long()), own)
+
+
+def test_a_refused_row_is_that_of_no_position():
+    """Both sequences refused: the step is the FFN's alone, as without a pool past max_ctx."""
+    h, past = _build(n_seq=2, n_pages=2), _build(n_seq=2, max_ctx=64)
+    for g in (h, past):
+        g.prefill(_x(63, D, 1), 0)
+        g.prefill(_x(63, D, 2), 1)
+    run, other = _capture(h, 2), _capture(past, 2)
+    x = _x(2, D, 3)
+    assert _rel(_replay(*run, x), _replay(*other, x)) <= BOUND
+    own = _codes(h)
+    for i in range(2):
+        x = _x(2, D, 4 + i)
+        assert torch.equal(_replay(*run, x), _replay(*other, x))
+        assert h.ctx.tolist() == [64, 64] and h.status.tolist() == [2, 0] and _same(_codes(h), own)
