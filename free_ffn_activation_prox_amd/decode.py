@@ -154,6 +154,9 @@ class DecodeHarness:
         if self.cache != "dense":
             if n > self.max_ctx:
                 raise ValueError(f"{n} tokens do not fit the cache's {self.max_ctx} positions")
+            pages = self.n_seq * -(-n // KV_PAGE)
+            if self.pool is not None and pages > self.pool.n_pages:
+                raise ValueError(f"{self.n_seq} times {n} tokens need {pages} pages of a pool of {self.pool.n_pages}")
             self.lengths = [0] * self.n_seq
             if self.prefix:
                 self.prefix = 0

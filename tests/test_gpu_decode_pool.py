@@ -79,3 +79,21 @@ def test_a_refused_row_is_that_of_no_position():
         x = _x(2, D, 4 + i)
         assert torch.equal(_replay(*run, x), _replay(*other, x))
         assert h.ctx.tolist() == [64, 64] and h.status.tolist() == [2, 0] and _same(_codes(h), own)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(keep_pages=3)])
+def test_a_context_that_the_pool_cannot_hold_changes_nothing(kw):
+    h, twin = (_build(n_seq=2, n_pages=5, **kw) for _ in range(2))
+    for g in (h, twin):
+        g.share_prefix(_x(130, D, 1))
+    before, codes, space = (h.lengths[:], h.pos, h.prefix, h.ctx.tolist(), h.pool.refs.tolist()), _codes(h), h.kv_ws
+    with pytest.raises(ValueError):
+        h.fill_cache(200)                                          # 8 pages
+    assert before == (h.lengths[:], h.pos, h.prefix, h.ctx.tolist(), h.pool.refs.tolist())
+    assert _same(_codes(h), codes) and h.kv_ws is space
+    x = _x(2, D, 2)
+    assert torch.equal(h.step(x), twin.step(x))
+    with pytest.raises(ValueError):
+        h.prefill(_x(190, D), 1)                                   # what the host counts is still there
+    h.fill_cache(100)
+    assert h.ctx.tolist() == [100, 100] and h.lengths == [100, 100]
