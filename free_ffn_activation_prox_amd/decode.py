@@ -136,6 +136,11 @@ class DecodeHarness:
                 self.picked = torch.empty(n_seq, shape.n_kv, keep_pages, dtype=torch.int32, device=dev)
                 self.pick_ws = alloc_kv_select_workspace(self.kv[0], self.one, shape.n_heads)
                 self.kv_ws = alloc_kv_selected_workspace(self.kv[0], self.one, shape.n_heads, keep_pages)
+            if self.pool is not None:
+                # these stay where they are: a captured step goes on using them when a prefix begins or ends
+                self.shared = torch.zeros(1, dtype=torch.int32, device=dev)
+                if keep_pages is None:
+                    self.share_ws = alloc_kv_shared_workspace(self.kv[0], self.one, shape.n_heads)
         self.pos = 0
         if ffn != "dense":
             kind = "exact" if ffn == "exact" else proxy
@@ -160,8 +165,7 @@ class DecodeHarness:
             self.lengths = [0] * self.n_seq
             if self.prefix:
                 self.prefix = 0
-                if self.keep_pages is None:
-                    self.kv_ws = alloc_kv_workspace(self.kv[0], self.one, self.shape.n_heads)
+                self.shared.zero_()
             self._grow(range(self.n_seq), n)
             T = self.n_seq * n
             if self.pool is None:
@@ -223,7 +227,6 @@ class DecodeHarness:
         y = self.prefill(x, 0)
         pages = x.shape[0] // KV_PAGE
         if pages and self.n_seq > 1:
-            dev = self.ctx.device
             want = torch.full_like(self.ctx, pages * KV_PAGE)
             want[0] = x.shape[0]
             parent, shared = torch.zeros_like(want), torch.full_like(want, pages)
@@ -231,9 +234,7 @@ class DecodeHarness:
             kv_pages(self.pool, want, 0, parent=parent, shared=shared)
             self.lengths = [x.shape[0]] + [pages * KV_PAGE] * (self.n_seq - 1)
             self.prefix = pages
-            self.shared = torch.full((1,), pages, dtype=torch.int32, device=dev)
-            if self.keep_pages is None:
-                self.kv_ws = alloc_kv_shared_workspace(self.kv[0], self.one, self.shape.n_heads)
+            self.shared.fill_(pages)
         return y
 
     def _attend(self, li: int, q: torch.Tensor, batch: KVBatch, workspace) -> torch.Tensor:
@@ -246,7 +247,7 @@ class DecodeHarness:
             pages = kv_select(q, kv, batch, self.bounds[li], self.keep_pages, pages=self.picked, workspace=self.pick_ws)
             return kv_attention_selected(q, kv, batch, pages, workspace=workspace)
         if self.prefix:
-            return kv_attention_shared(q, kv, batch, self.shared, workspace=workspace)
+            return kv_attention_shared(q, kv, batch, self.shared, workspace=self.share_ws)
         return kv_attention(q, kv, batch, workspace=workspace)
 
     def _paged(self, x: torch.Tensor, batch: KVBatch, workspace) -> torch.Tensor:

@@ -97,3 +97,50 @@ def test_a_context_that_the_pool_cannot_hold_changes_nothing(kw):
         h.prefill(_x(190, D), 1)                                   # what the host counts is still there
     h.fill_cache(100)
     assert h.ctx.tolist() == [100, 100] and h.lengths == [100, 100]
+
+
+def test_a_step_captured_before_a_prefix_goes_on_beside_it():
+    """It reads every sequence's own table; the step that the harness now makes reads the prefix once.
+    Neither uses memory that the harness has let go of."""
+    h, twin = (_build(n_seq=3, n_pages=24) for _ in range(2))
+    run = _capture(h, 3)
+    spaces = [t.data_ptr() for t in (h.kv_ws, h.share_ws, h.shared)]
+    h.fill_cache(0)                                                # the host counts the captured step: begin again
+    for g in (h, twin):
+        g.share_prefix(_x(64 * 3 + 5, D, 1))
+    assert spaces == [t.data_ptr() for t in (h.kv_ws, h.share_ws, h.shared)]
+    for i in range(3):
+        x = _x(3, D, 2 + i)
+        y = twin.step(x)
+        assert _rel(_replay(*run, x), y) <= BOUND
+        junk = torch.full((1 << 20,), float("nan"), device="cuda")  # takes the memory that is free
+        assert h.ctx.tolist() == twin.ctx.tolist()
+        del junk
+
+
+def test_a_step_captured_with_a_prefix_goes_on_without_one():
+    h, twin = (_build(n_seq=3, n_pages=24) for _ in range(2))
+    h.share_prefix(_x(64 * 3 + 5, D, 1))
+    run = _capture(h, 3)
+    spaces = [t.data_ptr() for t in (h.kv_ws, h.share_ws, h.shared)]
+    for g in (h, twin):
+        g.fill_cache(300, seed=4)                                  # each sequence has pages of its own again
+    assert spaces == [t.data_ptr() for t in (h.kv_ws, h.share_ws, h.shared)]
+    for i in range(3):
+        x = _x(3, D, 2 + i)
+        y = twin.step(x)
+        assert _rel(_replay(*run, x), y) <= BOUND
+    assert h.ctx.tolist() == twin.ctx.tolist() == [303] * 3
+
+
+def test_replays_past_the_pool_leave_a_shared_page_as_it_is():
+    """Sequences that end where the prefix does, and one page for three of them."""
+    h = _build(n_seq=3, n_pages=3)
+    run = _capture(h, 3)
+    h.fill_cache(0)
+    h.share_prefix(_x(128, D, 1))
+    prompt = _codes(h, h.table[0, :2].long())
+    for i in range(3):
+        y = _replay(*run, _x(3, D, 2 + i))
+        assert torch.isfinite(y).all() and h.ctx.tolist() == [129 + i, 128, 128] and h.status.tolist() == [2, 0]
+        assert _same(_codes(h, h.table[0, :2].long()), prompt)
