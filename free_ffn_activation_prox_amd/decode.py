@@ -32,7 +32,9 @@ and may begin with a prompt in common (``share_prefix``): its pages are held onc
 and read once a step for all of them.  A sequence for which the pool has no page
 left (``status`` [0] of them at the last step) keeps its tokens; its row of the
 step has no position, so it stores nothing and its attention is zeros, as where a
-step goes past max_ctx.
+step goes past max_ctx.  The host refuses what the pool cannot hold by its own
+count, which replays do not move: a prompt looks at the device's once there is a
+captured call, a step never waits for it.
 """
 
 from __future__ import annotations
@@ -127,6 +129,7 @@ class DecodeHarness:
                 self.slots, self.status = torch.zeros_like(self.ctx), torch.zeros(2, dtype=torch.int32, device=dev)
                 self.got, self.at = torch.zeros_like(self.ctx, dtype=torch.bool), torch.zeros_like(self.ctx)
             self.lengths = [0] * n_seq           # the same on the host (a replayed graph does not move it)
+            self.captured = False                # whether a graph may have moved the pool's
             self.prefix = 0                      # pages that all sequences share
             self.one = KVBatch(self.ctx if self.pool is None else self.at, self.table)
             self.kv_ws = alloc_kv_workspace(self.kv[0], self.one, shape.n_heads)
@@ -202,6 +205,23 @@ class DecodeHarness:
                     workspace=self.ws)
         return self.y
 
+    def _move(self, want: torch.Tensor, n_rows: int, **out):
+        """The pool's sequences to `want` tokens.  at: their tokens, 0 for one that was refused, so that rows of the
+        call have positions below 0, which do not exist."""
+        kv_pages(self.pool, want, n_rows, **out)
+        torch.eq(self.ctx, want, out=self.got)
+        torch.mul(self.ctx, self.got, out=self.at)
+
+    def _recount(self):
+        """The host's lengths after replayed graphs of a harness over a pool: as they are on the device."""
+        if self.pool is None:
+            return
+        if torch.cuda.is_current_stream_capturing():
+            self.captured = True
+        elif self.captured:
+            self.lengths = self.ctx.tolist()
+            self.pos = max(self.lengths)
+
     def _grow(self, seqs, n: int):
         """n more tokens of the sequences `seqs`, on the host's count."""
         if max(self.lengths[s] for s in seqs) + n > self.max_ctx:
@@ -222,6 +242,7 @@ class DecodeHarness:
         sequence 0's alone."""
         if self.cache == "dense" or self.pool is None:
             raise ValueError("share_prefix needs a pool of pages (n_pages)")
+        self._recount()
         if any(self.lengths):
             raise ValueError("share_prefix needs empty sequences")
         y = self.prefill(x, 0)
@@ -278,6 +299,7 @@ class DecodeHarness:
             raise ValueError(f"sequence {seq} of {self.n_seq}")
         if x.dim() != 2 or x.shape[1] != self.shape.d:
             raise ValueError("x must be [tokens][d]")
+        self._recount()
         self._grow([seq], x.shape[0])
         out = []
         for p in x.split(MAX_PREFILL) if x.shape[0] else ():
@@ -289,8 +311,10 @@ class DecodeHarness:
             else:
                 want = self.ctx.clone()
                 want[seq:seq + 1].add_(T)
-                start, _, _ = kv_pages(self.pool, want, T)
-                batch = KVBatch(self.ctx, self.table, start, n_tokens=T, max_q=T)
+                self._move(want, T)
+                start = torch.zeros_like(self.start)
+                start[seq + 1:].fill_(T)
+                batch = KVBatch(self.at, self.table, start, n_tokens=T, max_q=T)
             out.append(self._paged(p, batch, alloc_kv_workspace(self.kv[0], batch, self.shape.n_heads)))
         return torch.cat(out) if out else x
 
@@ -299,15 +323,14 @@ class DecodeHarness:
         if self.cache != "dense":
             if x.shape != (self.n_seq, self.shape.d):
                 raise ValueError("x must be [n_seq][d]")
+            if self.pool is not None and torch.cuda.is_current_stream_capturing():
+                self.captured = True
             self._grow(range(self.n_seq), 1)
             if self.pool is None:
                 self.ctx.add_(1)
             else:
                 torch.add(self.ctx, 1, out=self.want)
-                kv_pages(self.pool, self.want, self.n_seq, q_start=self.start, slots=self.slots, status=self.status)
-                # the step's row of a sequence that got no page has position -1, which does not exist
-                torch.eq(self.ctx, self.want, out=self.got)
-                torch.mul(self.ctx, self.got, out=self.at)
+                self._move(self.want, self.n_seq, q_start=self.start, slots=self.slots, status=self.status)
             return self._paged(x, self.one, self.kv_ws)
         sh, pos = self.shape, self.pos
         H, KV, hd = sh.n_heads, sh.n_kv, sh.hd

@@ -144,3 +144,49 @@ def test_replays_past_the_pool_leave_a_shared_page_as_it_is():
         y = _replay(*run, _x(3, D, 2 + i))
         assert torch.isfinite(y).all() and h.ctx.tolist() == [129 + i, 128, 128] and h.status.tolist() == [2, 0]
         assert _same(_codes(h, h.table[0, :2].long()), prompt)
+
+
+def test_a_prompt_behind_replayed_steps_counts_them():
+    """Replays move the lengths on the device alone: a prompt, a prefix or the pool's end is judged by those."""
+    h = _build(n_seq=2, n_pages=4)
+    h.prefill(_x(62, D, 1), 0)
+    h.prefill(_x(126, D, 2), 1)
+    run = _capture(h, 2)
+    for i in range(4):                                             # 66 tokens in two pages, 128 in two
+        _replay(*run, _x(2, D, 3 + i))
+    assert h.ctx.tolist() == [66, 128]
+    codes = _codes(h)
+    with pytest.raises(ValueError):
+        h.prefill(_x(1, D, 9), 1)                                  # a third page: the host had counted 127 tokens
+    assert h.ctx.tolist() == h.lengths == [66, 128] and h.pos == 128 and _same(_codes(h), codes)
+    assert torch.isfinite(h.prefill(_x(62, D, 9), 0)).all()        # its second page's last tokens
+    with pytest.raises(ValueError):
+        h.prefill(_x(1, D, 9), 0)
+    h.fill_cache(0)
+    _replay(*run, _x(2, D, 8))
+    with pytest.raises(ValueError):
+        h.share_prefix(_x(70, D))                                  # a token each
+    assert h.ctx.tolist() == h.lengths == [1, 1]
+
+
+def test_a_captured_prompt_that_the_pool_refuses():
+    """Its rows have no position, as those of a step; past it, a prompt that fits goes on."""
+    h, twin = (_build(n_seq=2, n_pages=n) for n in (3, 30))
+    buf = torch.zeros(70, D, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        h.prefill(buf, 0)
+    torch.cuda.current_stream().wait_stream(side)
+    h.fill_cache(0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = h.prefill(buf, 1)
+    x = _x(70, D, 1)
+    assert _rel(_replay(g, buf, out, x), twin.prefill(x, 1)) <= BOUND
+    codes = _codes(h)
+    y = _replay(g, buf, out, x)                                    # 140 tokens: a third page, which is there
+    assert _rel(y, twin.prefill(x, 1)) <= BOUND and h.ctx.tolist() == [0, 140]
+    own = _codes(h)
+    y = _replay(g, buf, out, x)
+    assert torch.isfinite(y).all() and h.ctx.tolist() == [0, 140] and _same(_codes(h), own) and not _same(own, codes)
