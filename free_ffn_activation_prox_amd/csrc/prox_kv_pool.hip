@@ -26,6 +26,7 @@ namespace {
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWaves = kPoolThreads / kWave;
 constexpr int kChunk4 = 4 * kWave;      // table entries that a wave takes at once
+constexpr int kFillBlocks = 1 << 20;    // of k_kv_pages_fill in x: 2^24 sequences of 256 threads would be more than a launch has
 
 struct PoolArgs {
     prox_kv_pool p;
@@ -357,14 +358,15 @@ __global__ void __launch_bounds__(kPoolThreads) k_kv_pages_move(PoolArgs A) {
     if (last_s) number_pages<true>(A);
 }
 
-// blockIdx.y: a wave for each of a sequence's runs of 256 rows or entries.
+// blockIdx.x: a sequence (and those kFillBlocks behind it); blockIdx.y: its runs of 256 rows or entries.
 __global__ void __launch_bounds__(256) k_kv_pages_fill(PoolArgs A) {
-    const int s = blockIdx.x;
-    const Fill f = fill_of(A, s);
-    const int rows = max(f.length - f.start, 0), entries = max(pages_of(f.start), pages_of(f.length));
     const int step = gridDim.y * 256, t = blockIdx.y * 256 + threadIdx.x;
-    for (int i = t; i < rows && f.row0 + i < A.n_rows; i += step) fill_row(A, s, f, i);
-    for (int j = min(pages_of(f.start), pages_of(f.length)) + t; j < entries; j += step) fill_entry(A, s, f, j);
+    for (int s = blockIdx.x; s < A.p.n_seq; s += gridDim.x) {
+        const Fill f = fill_of(A, s);
+        const int rows = max(f.length - f.start, 0), entries = max(pages_of(f.start), pages_of(f.length));
+        for (int i = t; i < rows && f.row0 + i < A.n_rows; i += step) fill_row(A, s, f, i);
+        for (int j = min(pages_of(f.start), pages_of(f.length)) + t; j < entries; j += step) fill_entry(A, s, f, j);
+    }
     clear_rows(A, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x, (int64_t)gridDim.x * gridDim.y * 256);
 }
 
@@ -423,7 +425,7 @@ hipError_t launch_kv_pages(const prox_kv_pool& p, const int32_t* want, const int
     if (e != hipSuccess) return e;
     // rows of one sequence go to several blocks where there are few sequences
     const int runs = (int)std::min<int64_t>(std::max<int64_t>(device_cus() * 4 / p.n_seq, 1), ((int64_t)n_rows + 255) / 256 + 1);
-    hipLaunchKernelGGL(k_kv_pages_fill, dim3((uint32_t)p.n_seq, (uint32_t)runs), dim3(256), 0, s, A);
+    hipLaunchKernelGGL(k_kv_pages_fill, dim3((uint32_t)std::min(p.n_seq, kFillBlocks), (uint32_t)runs), dim3(256), 0, s, A);
     return hipGetLastError();
 }
 

@@ -215,3 +215,24 @@ def test_on_a_stream_of_its_own():
     assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, exp))
     w.same()
     del junk
+
+
+def test_as_many_sequences_as_a_pool_may_have():
+    """2^24 sequences (PROX_KV_MAX_POOL), a handful of which have tokens: the first, the last and some between."""
+    import free_ffn_activation_prox_amd as P
+    n = 1 << 24
+    pool = P.KVPool.alloc(40, n, 2)
+    at = torch.tensor([0, 5, 255, 256, 1 << 20, (1 << 20) + 1, n - 257, n - 1], device="cuda")
+    for top, status in ((100, [0, 40 - 16]), (1, [0, 40 - 8]), (0, [0, 40])):
+        want = torch.zeros(n, dtype=torch.int32, device="cuda")
+        want[at] = torch.arange(8, dtype=torch.int32, device="cuda") + top if top else 0
+        had = pool.ctx_len[at].clone()
+        q_start, slots, st = P.kv_pages(pool, want, 900)
+        torch.cuda.synchronize()
+        assert st.tolist() == status and torch.equal(pool.ctx_len, want)
+        pages = -(-want[at] // 64)
+        rows = torch.clamp(want[at] - had, min=0)
+        assert torch.equal(q_start[at + 1] - q_start[at], rows) and int(q_start[-1]) == int(rows.sum())
+        assert torch.equal((pool.block_table[at] >= 0).sum(1), pages.long()) and int((pool.block_table >= 0).sum()) == int(pages.sum())
+        assert int(pool.refs.sum()) == int(pages.sum()) and int(pool.refs.max()) <= 1
+        assert int((slots >= 0).sum()) == int(rows.sum())
