@@ -246,6 +246,9 @@ inline int64_t page_pairs(const prox_kv_batch& b, int& pp) {
     return found;
 }
 
+// Whether blocks of `threads` fit one launch: the number of its threads is held in 32 bits.
+inline bool one_launch(int64_t blocks, int threads) { return blocks <= (int64_t)0xffffffffu / threads; }
+
 // ---- launchers of the operators around the cache; all enqueue on `s`
 size_t kv_pages_workspace(const prox_kv_pool& p);
 hipError_t launch_kv_pages(const prox_kv_pool& p, const int32_t* want, const int32_t* parent, const int32_t* shared,

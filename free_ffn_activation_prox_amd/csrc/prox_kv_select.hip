@@ -678,7 +678,7 @@ int pow2_up(int v) {
 hipError_t launch_kv_bounds(const prox_kv_cache& c, const prox_kv_batch& b, int8_t* bounds, hipStream_t s) {
     BoundsArgs A{c, b, bounds, 0};
     const int64_t units = page_pairs(b, A.pp) * c.n_kv, blocks = (units + 3) / 4;
-    if (blocks > 0x7fffffffll || units / c.n_kv > 0x7fffffffll) return hipErrorInvalidConfiguration;
+    if (!one_launch(blocks, 256) || units / c.n_kv > 0x7fffffffll) return hipErrorInvalidConfiguration;
     if (c.kind == PROX_KV_INT8) hipLaunchKernelGGL((k_kv_bounds<PROX_KV_INT8>), dim3((uint32_t)blocks), dim3(256), 0, s, A, units);
     else hipLaunchKernelGGL((k_kv_bounds<PROX_KV_FP8>), dim3((uint32_t)blocks), dim3(256), 0, s, A, units);
     return hipGetLastError();
@@ -737,7 +737,7 @@ struct SelectSplit {
         units = tiles * c.n_kv;
         const int64_t want = kBlocksPerCu * device_cus() / units, most = (row_pages + kLeastRun - 1) / kLeastRun;
         parts = (int)std::max<int64_t>(std::min(want, most), 1);
-        fits = units * parts <= 0x7fffffffll;
+        fits = one_launch(units * parts, kSelThreads);               // (k_kv_pick has no more)
         bytes = parts > 1 ? align_up((size_t)units * TQ * row_pages * sizeof(uint32_t), 256) : 256;
     }
 };

@@ -212,7 +212,7 @@ SelectedSplit selected_split(const prox_kv_cache& c, int n_tokens, int n_heads, 
     p.lds = (size_t)p.waves * p.HG * row;
     p.part_at = align_up((size_t)p.units * p.parts * sizeof(unsigned long long), 256);
     p.part_bytes = p.parts > 1 ? (size_t)p.units * p.parts * p.HG * row : 0;
-    p.fits = p.units * p.parts <= 0x7fffffffll;
+    p.fits = one_launch(p.units * p.parts, 64 * p.waves);
     p.bytes = align_up(p.parts > 1 ? p.part_at + p.part_bytes : 0, 256) + 256;
     return p;
 }

@@ -134,10 +134,14 @@ __device__ __forceinline__ void later(const AttendPrefix& A, const Seg& S, int i
 
 // ---- launch 2: a thread for each row, query head and four channels.  64 tokens of 32 heads and 32 parts each: 8.7 us
 // (35 MB, 4 TB/s); with the parts of a row split among four threads 9.0.
+constexpr int kJoinThreads = 256;
+int64_t join_blocks(const prox_kv_cache& c, const prox_kv_batch& b, int n_heads) {
+    return ((int64_t)b.n_tokens * n_heads * (c.head_pad / 4) + kJoinThreads - 1) / kJoinThreads;
+}
 template <int NP>
-__global__ void __launch_bounds__(256) k_kv_join(AttendPrefix A, int64_t pairs) {
+__global__ void __launch_bounds__(kJoinThreads) k_kv_join(AttendPrefix A, int64_t pairs) {
     constexpr int RW = 64 * NP + 4, LPR = 16 * NP;
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, pair = t / LPR;
+    const int64_t t = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, pair = t / LPR;
     const int c4 = 4 * (int)(t % LPR);
     if (pair >= pairs) return;
     const int row = (int)(pair / A.G.n_heads), hq = (int)(pair % A.G.n_heads);
@@ -237,7 +241,7 @@ struct SharedPlan {
         // in tiles of twice as many rows 42
         const int64_t usual = (int64_t)((b.n_tokens + n_groups - 1) / n_groups) * (n_heads / c.n_kv);
         prefix = split_of(c, groups, n_heads, b.n_tokens, b.n_tokens, usual);
-        fits = prefix.fits && rest.fit() && (int64_t)b.n_tokens * n_heads <= 0x7fffffffll * 4;
+        fits = prefix.fits && rest.fit() && one_launch(join_blocks(c, b, n_heads), kJoinThreads);
         row_part = align_up(std::max(prefix.bytes, std::max(rest.split[0].bytes, rest.split[1].bytes)), 256);
         skip = row_part + align_up((size_t)b.n_tokens * n_heads * (c.head_pad + 4) * sizeof(float), 256);
         joins = skip + align_up((size_t)b.n_seq * sizeof(int32_t), 256);
@@ -277,8 +281,8 @@ hipError_t launch_kv_shared(const prox_kv_cache& c, const prox_kv_batch& batch, 
     A.G = G;
     hipError_t e = launch(A, P.prefix, workspace, s);
     if (e != hipSuccess) return e;
-    const int64_t pairs = (int64_t)b.n_tokens * n_heads, blocks = (pairs * (c.head_pad / 4) + 255) / 256;
-    const dim3 grid((uint32_t)blocks), threads(256);
+    const int64_t pairs = (int64_t)b.n_tokens * n_heads;
+    const dim3 grid((uint32_t)join_blocks(c, b, n_heads)), threads(kJoinThreads);
     switch (c.head_pad / 64) {
         case 1: hipLaunchKernelGGL((k_kv_join<1>), grid, threads, 0, s, A, pairs); break;
         case 2: hipLaunchKernelGGL((k_kv_join<2>), grid, threads, 0, s, A, pairs); break;

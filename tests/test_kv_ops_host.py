@@ -162,3 +162,29 @@ def test_oracle_bounds_hold_for_every_query():
                 q = r.standard_normal((2, c.hp))
                 top = np.maximum(q * b[pg, :, 0], q * b[pg, :, 1]).sum(-1)
                 assert ((tok[pg, :, :held] * q[:, None]).sum(-1).max(-1) <= top + 1e-9).all()
+
+
+def test_more_threads_than_a_launch_has_are_refused_before_the_first():
+    """2^32 threads: what is one short of them has a workspace, what reaches them has none and is refused."""
+    def both(size, call, c, over, fits):
+        b = batch(**over)
+        assert (size(c, b) > 0) == fits, over
+        if not fits:
+            assert call(c, b) == UNSUPPORTED, over
+
+    one = lambda n: dict(n_seq=n, n_tokens=n, max_q=1, q_start=0)                                     # noqa: E731
+    size = lambda c, b: _lib.prox_kv_select_workspace_bytes(ctypes.byref(c), ctypes.byref(b), c.n_kv)  # noqa: E731
+    call = lambda c, b: select(c=c, b=b, H=c.n_kv, qs=c.n_kv * 128, n=(1 << 62))                       # noqa: E731
+    both(size, call, cache(n_kv=1), one((1 << 24) - 1), True)                                         # a block of 256 a row
+    both(size, call, cache(n_kv=1), one(1 << 24), False)
+    both(size, call, cache(n_kv=8), one(1 << 21), False)
+    size = lambda c, b: _lib.prox_kv_selected_workspace_bytes(ctypes.byref(c), ctypes.byref(b), c.n_kv, 4)  # noqa: E731
+    call = lambda c, b: selected(c=c, b=b, H=c.n_kv, qs=c.n_kv * 128, os=c.n_kv * 128, n=(1 << 62))         # noqa: E731
+    both(size, call, cache(n_kv=1), one((1 << 24) - 1), True)
+    both(size, call, cache(n_kv=1), one(1 << 24), False)
+    both(size, call, cache(n_kv=8), one(1 << 21), False)
+    # the join of a shared prefix: head_pad / 4 threads a row and query head
+    size = lambda c, b: _lib.prox_kv_shared_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 64, 1)        # noqa: E731
+    call = lambda c, b: shared(c=c, b=b, n=1, H=64, qs=64 * 128, os=64 * 128, bytes=1 << 62)                # noqa: E731
+    for n, fits in (((1 << 21) - 4, True), (1 << 21, False), (1 << 24, False)):
+        both(size, call, cache(n_kv=8), dict(n_seq=n // 64, n_tokens=n, max_q=64), fits)
