@@ -74,31 +74,32 @@ __device__ __forceinline__ Move move_of(const PoolArgs& A, int s) {
     return m;
 }
 
-// Entries j0 .. j0 + 255 of a sequence's row, one wave.  Nobody reads a row that
-// this writes: a sequence that takes pages over had none, so it has none to give.
-template <int SCOPE>
-__device__ __forceinline__ void take_and_give_back(const PoolArgs& A, int s, const Move& m, int j0, int l) {
+// Entries j0 .. j0 + 255 of a sequence's row, one wave each.  Nobody reads a row
+// that is written here: a sequence that takes pages over had none.
+__device__ __forceinline__ void take_over(const PoolArgs& A, int s, const Move& m, int j0, int l) {
+    if (m.first <= j0) return;
+    const int32_t* src = row_of(A, m.parent);
     int page[4];
-    if (m.first > j0) {
-        const int32_t* src = row_of(A, m.parent);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) page[i] = src[min(j0 + 64 * i + l, m.first - 1)];
+    for (int i = 0; i < 4; ++i) page[i] = src[min(j0 + 64 * i + l, m.first - 1)];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 64 * i + l;
-            if (j >= m.first) continue;
-            row_of(A, s)[j] = page[i];
-            if (is_page(A, page[i])) __hip_atomic_fetch_add(A.p.refs + page[i], 1, __ATOMIC_RELAXED, SCOPE);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int j = j0 + 64 * i + l;
+        if (j >= m.first) continue;
+        row_of(A, s)[j] = page[i];
+        if (is_page(A, page[i])) __hip_atomic_fetch_add(A.p.refs + page[i], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (m.hi > j0 && m.lo < j0 + kChunk4) {
+}
+template <int SCOPE>
+__device__ __forceinline__ void give_back(const PoolArgs& A, int s, int lo, int hi, int j0, int l) {
+    if (hi <= j0 || lo >= j0 + kChunk4) return;
+    int page[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) page[i] = row_of(A, s)[min(j0 + 64 * i + l, m.hi - 1)];
+    for (int i = 0; i < 4; ++i) page[i] = row_of(A, s)[min(j0 + 64 * i + l, hi - 1)];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 64 * i + l;
-            if (j >= m.lo && j < m.hi && is_page(A, page[i])) __hip_atomic_fetch_add(A.p.refs + page[i], -1, __ATOMIC_RELAXED, SCOPE);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int j = j0 + 64 * i + l;
+        if (j >= lo && j < hi && is_page(A, page[i])) __hip_atomic_fetch_add(A.p.refs + page[i], -1, __ATOMIC_RELAXED, SCOPE);
     }
 }
 
@@ -292,25 +293,24 @@ __device__ __forceinline__ void all_done() {
     __syncthreads();
 }
 
-// The whole call in one block: a lane for each sequence, a wave for those with
-// more to do.  Counts move by atomics of the block's own scope, in the L2 cache
+// A call without parents in one block: a lane for each sequence, a wave for those
+// with more to do.  Counts move by atomics of the block's own scope, in the L2 cache
 // that its loads read, and are loaded only after the last of them.
 __global__ void __launch_bounds__(kPoolThreads) k_kv_pages_one(PoolArgs A) {
     constexpr int kFew = 2;                                        // entries and rows that a lane takes by itself
     const int l = lane_id(), w = threadIdx.x / kWave;
     for (int s0 = w * kWave; s0 < A.p.n_seq; s0 += kPoolThreads) {
-        Move m{-1, 0, 0, 0, 0};
+        int lo = 0, hi = 0;
         if (s0 + l < A.p.n_seq) {
-            m = move_of(A, s0 + l);
-            A.start[s0 + l] = m.start;
+            const int had = tokens_of(A, s0 + l);
+            A.start[s0 + l] = had;
+            lo = pages_of(max(A.want[s0 + l], 0));
+            hi = pages_of(had);
         }
-        for (uint64_t some = __ballot(m.first > 0 || m.hi > m.lo); some; some &= some - 1) {
-            const int i = __builtin_ctzll(some);
-            const Move x{__builtin_amdgcn_readlane(m.parent, i), __builtin_amdgcn_readlane(m.first, i),
-                         __builtin_amdgcn_readlane(m.start, i), __builtin_amdgcn_readlane(m.lo, i),
-                         __builtin_amdgcn_readlane(m.hi, i)};
-            for (int j = x.first > 0 ? 0 : x.lo / kChunk4 * kChunk4; j < max(x.first, x.hi); j += kChunk4)
-                take_and_give_back<__HIP_MEMORY_SCOPE_WORKGROUP>(A, s0 + i, x, j, l);
+        for (uint64_t some = __ballot(hi > lo); some; some &= some - 1) {
+            const int i = __builtin_ctzll(some), from = __builtin_amdgcn_readlane(lo, i), upto = __builtin_amdgcn_readlane(hi, i);
+            for (int j = from / kChunk4 * kChunk4; j < upto; j += kChunk4)
+                give_back<__HIP_MEMORY_SCOPE_WORKGROUP>(A, s0 + i, from, upto, j, l);
         }
     }
     all_done();
@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kPoolThreads) k_kv_pages_move(PoolArgs A) {
         const int s = (int)(u / A.chunks), c = (int)(u % A.chunks);
         const Move m = move_of(A, s);
         if (c == 0 && l == 0) __hip_atomic_store(A.start + s, m.start, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        take_and_give_back<__HIP_MEMORY_SCOPE_AGENT>(A, s, m, c * kChunk4, l);
+        take_over(A, s, m, c * kChunk4, l);
+        give_back<__HIP_MEMORY_SCOPE_AGENT>(A, s, m.lo, m.hi, c * kChunk4, l);
     }
     all_done();
     if (w == 0) {
