@@ -769,7 +769,9 @@ def _bounds_ptr(cache, bounds):
 def kv_page_bounds(cache: KVCache, batch: KVBatch, bounds, *, stream=None):
     """Set the bounds (least and largest code of every channel) of the pages that
     the batch's tokens lie in, behind kv_append with the same batch or over whole
-    sequences.  Returns bounds."""
+    sequences.  A page that other sequences hold too has to be full in those that
+    the batch names tokens of: leave out one that kv_pages cut back into such a
+    page.  Returns bounds."""
     dev = cache.device
     if batch.device != dev:
         raise ValueError("cache and batch are on different devices")

@@ -465,8 +465,12 @@ prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want, const int3
  * those of every page that the batch's tokens lie in, from all tokens of the page
  * up to the sequence's last one; it is called behind prox_kv_append (which may
  * round a page's codes again) with the same batch, or once over whole sequences.
- * A page that several of the batch's sequences hold is taken to be full in all of
- * them.  bounds: device, 16-byte aligned. */
+ * A page that other sequences hold too, of the batch or not, has to be full in
+ * every sequence whose tokens the batch names: bounds from a part of it would not
+ * hold for the others.  One that prox_kv_pages cut back into such a page has no
+ * rows in that call's q_start (it cannot go on there) and stays out of batches of
+ * whole sequences until the others have let the page go.
+ * bounds: device, 16-byte aligned. */
 prox_status prox_kv_page_bounds(const prox_kv_cache* c, const prox_kv_batch* b, void* bounds, void* stream);
 
 /* Workspace bytes of prox_kv_select for this cache, batch (n_seq, n_tokens, max_q and

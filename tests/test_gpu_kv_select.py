@@ -239,3 +239,43 @@ def test_captured_and_replayed_with_moving_lengths():
             exp = np.zeros((2, 2, 5), np.int32)
             OO.select(w.o, w.table, w.ctx, None, 1, f64(q), bnd.cpu().numpy(), 5, 1, 1, exp)
             assert np.array_equal(ph.cpu().numpy(), exp), i
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_bounds_of_a_page_that_one_of_its_sequences_is_cut_back_into(kind):
+    """The calls that the header allows keep the bounds of all that a holder of the page has in it: the rows of
+    kv_pages name no token of the sequence that was cut back, until it holds the page alone."""
+    w = World(kind, 2, 1, 64, [200, 200], seed=21, extra=4)
+    P = w.P
+    pool = P.KVPool.alloc(w.o.n_pages, 2, w.table.shape[1])
+    bnd = P.alloc_kv_bounds(w.c)
+    dev = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def call(*want, parent=None, shared=None, refused=0):
+        start, _, status = P.kv_pages(pool, dev(*want), 400, parent=parent, shared=shared)
+        assert status.tolist()[0] == refused
+        b = P.KVBatch(pool.ctx_len, pool.block_table, start, n_tokens=400, max_q=400)
+        k = w.rows(400, 1)
+        P.kv_append(w.c, b, k, w.rows(400, 1))
+        P.kv_page_bounds(w.c, b, bnd)
+        torch.cuda.synchronize()
+
+    def holds(seq, tokens):
+        """Bounds of the sequence's pages are the oracle's over its tokens."""
+        w.o.k, w.o.ks = w.c.k.cpu().numpy().reshape(w.o.k.shape), w.c.k_scale.cpu().numpy()
+        table, got = pool.block_table.cpu().numpy()[seq:seq + 1], bnd.cpu().numpy()
+        exp = got.copy()
+        OO.bounds(w.o, table, np.array([tokens]), np.array([0, tokens]), tokens, tokens, exp)
+        for page in table[0, :-(-tokens // 64)]:
+            assert np.array_equal(got[page], exp[page])
+
+    call(128, 0)
+    call(130, 128, parent=dev(-1, 0), shared=dev(0, 2))
+    holds(0, 130)
+    call(131, 100)                                                 # cut back into a page that sequence 0 has in full
+    call(132, 101, refused=1)
+    assert pool.ctx_len.tolist() == [132, 100]
+    holds(0, 132)
+    call(0, 100)                                                   # sequence 1 has the page alone: it goes on there
+    call(0, 103)
+    holds(1, 103)
