@@ -111,7 +111,8 @@ __device__ __forceinline__ Tile tile_of(const AttendPrefix& A, const KvRows& R, 
 __device__ __forceinline__ const int32_t* table_of(const AttendPrefix& A, int g) {
     return A.b.block_table + (size_t)min(group_at(A.G, g), A.G.n_seq - 1) * A.b.max_pages;
 }
-__device__ __forceinline__ int ctx_of(const AttendPrefix&, const Tile&) { return 0; }   // any slot may hold no token
+// all slots hold tokens: rows of a sequence that has not filled these pages are worked on here, but never joined
+__device__ __forceinline__ int ctx_of(const AttendPrefix&, const Tile&) { return 0x7fffffff; }
 __device__ __forceinline__ constexpr bool masked(const AttendPrefix&) { return false; }
 __device__ __forceinline__ PrefixOut out_row(const AttendPrefix& A, const Seg& S, int r) {
     const RowHead h = row_head(A, S, r);

@@ -287,3 +287,23 @@ def test_memory_let_go_before_the_stream_runs():
     assert not side.query() and not kept & again
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_nan_codes_that_a_shared_page_holds():
+    """Every slot of a shared page holds a token, so a NaN among its values is one, as in the attention over all
+    pages; one in the slots behind a sequence's last token is not."""
+    w = World("fp8", 4, 2, 64, [300, 300, 290, 200], seed=41)
+    settle(w, [300, 300, 290, 200])
+    share(w, [0, 3, 4], [3, 1])
+    q = [w.rows(n, 4, 1.5) for n in (4, 67)]
+    new = ([1, 1, 1, 1], [5, 60, 1, 1])
+    good = [attend(w, n, [3, 1], [0, 3, 4], q=x.clone()) for n, x in zip(new, q)]
+    codes = w.c.v.view(w.o.n_pages, 2, -1)
+    for s, pg, slot, head, ch in ((0, 1, 9, 1, 5), (0, 2, 63, 0, 60), (3, 0, 0, 0, 17), (3, 2, 4, 0, 3), (3, 3, 30, 1, 9), (1, 4, 50, 0, 8)):
+        codes[int(w.table[s, pg]), head, ((ch // 16 * 4 + slot // 4 % 4) * 16 + ch % 16) * 16 + slot // 16 * 4 + slot % 4] = 0x7f
+    for n, x, a in zip(new, q, good):
+        b, start = w.batch(n, advance=False)
+        out = w.P.kv_attention_shared(x, w.c, b, dev([3, 1]), group_start=dev([0, 3, 4]))
+        nan = torch.zeros(x.shape, dtype=torch.bool)               # query heads 0, 1 read key head 0, heads 2, 3 the other
+        nan[:start[3], 2:, 5] = nan[:start[3], :2, 60] = nan[start[3]:, :2, 17] = nan[start[3]:, :2, 3] = True
+        assert torch.equal(out.isnan().cpu(), nan) and torch.equal(out.cpu()[~nan], a.cpu()[~nan])
