@@ -30,9 +30,9 @@ harness keeps of every page (prompts see all pages).  With n_pages the sequences
 take their pages from a pool of that many instead of each having its own share,
 and may begin with a prompt in common (``share_prefix``): its pages are held once
 and read once a step for all of them.  A sequence for which the pool has no page
-left (``status`` [0] of them at the last step) keeps its tokens; its row of the
-step has no position, so it stores nothing and its attention is zeros, as where a
-step goes past max_ctx.  The host refuses what the pool cannot hold by its own
+left (``status`` [0] of them at the last step) keeps its tokens: the step's row is
+behind them, where the table names no page, so it sees them and stores nothing
+(past max_ctx it sees nothing either).  The host refuses what the pool cannot hold by its own
 count, which replays do not move: a prompt looks at the device's once there is a
 captured call, a step never waits for it.
 """
@@ -127,11 +127,12 @@ class DecodeHarness:
                 self.want = torch.zeros_like(self.ctx)
                 self.start = torch.zeros(n_seq + 1, dtype=torch.int32, device=dev)
                 self.slots, self.status = torch.zeros_like(self.ctx), torch.zeros(2, dtype=torch.int32, device=dev)
-                self.got, self.at = torch.zeros_like(self.ctx, dtype=torch.bool), torch.zeros_like(self.ctx)
             self.lengths = [0] * n_seq           # the same on the host (a replayed graph does not move it)
             self.captured = False                # whether a graph may have moved the pool's
             self.prefix = 0                      # pages that all sequences share
-            self.one = KVBatch(self.ctx if self.pool is None else self.at, self.table)
+            # over a pool, rows of the tokens wanted: the lengths of all but the sequences that kv_pages refuses, whose
+            # row is the first of a page that they do not have (by their lengths it would be their last token's again)
+            self.one = KVBatch(self.ctx if self.pool is None else self.want, self.table)
             self.kv_ws = alloc_kv_workspace(self.kv[0], self.one, shape.n_heads)
             self.keep_pages = keep_pages
             if keep_pages is not None:
@@ -204,13 +205,6 @@ class DecodeHarness:
         ffn_forward(f_in, self.s2[li], self.px[li], self.k_in, self.k_ff, y=self.y, mask=self.mask, idx=self.idx,
                     workspace=self.ws)
         return self.y
-
-    def _move(self, want: torch.Tensor, n_rows: int, **out):
-        """The pool's sequences to `want` tokens.  at: their tokens, 0 for one that was refused, so that rows of the
-        call have positions below 0, which do not exist."""
-        kv_pages(self.pool, want, n_rows, **out)
-        torch.eq(self.ctx, want, out=self.got)
-        torch.mul(self.ctx, self.got, out=self.at)
 
     def _recount(self):
         """The host's lengths after replayed graphs of a harness over a pool: as they are on the device."""
@@ -311,10 +305,12 @@ class DecodeHarness:
             else:
                 want = self.ctx.clone()
                 want[seq:seq + 1].add_(T)
-                self._move(want, T)
+                kv_pages(self.pool, want, T)
+                # a prompt that was refused (only a captured one can be) has rows below position 0, which do not exist
+                at = self.ctx * (self.ctx == want)
                 start = torch.zeros_like(self.start)
                 start[seq + 1:].fill_(T)
-                batch = KVBatch(self.at, self.table, start, n_tokens=T, max_q=T)
+                batch = KVBatch(at, self.table, start, n_tokens=T, max_q=T)
             out.append(self._paged(p, batch, alloc_kv_workspace(self.kv[0], batch, self.shape.n_heads)))
         return torch.cat(out) if out else x
 
@@ -330,7 +326,7 @@ class DecodeHarness:
                 self.ctx.add_(1)
             else:
                 torch.add(self.ctx, 1, out=self.want)
-                self._move(self.want, self.n_seq, q_start=self.start, slots=self.slots, status=self.status)
+                kv_pages(self.pool, self.want, self.n_seq, q_start=self.start, slots=self.slots, status=self.status)
             return self._paged(x, self.one, self.kv_ws)
         sh, pos = self.shape, self.pos
         H, KV, hd = sh.n_heads, sh.n_kv, sh.hd

@@ -65,20 +65,24 @@ def test_replays_past_the_pool_leave_refused_sequences_as_they_are(kw):
         assert _same(_codes(h, h.table[1, :2].long()), own)
 
 
-def test_a_refused_row_is_that_of_no_position():
-    """Both sequences refused: the step is the FFN's alone, as without a pool past max_ctx."""
-    h, past = _build(n_seq=2, n_pages=2), _build(n_seq=2, max_ctx=64)
-    for g in (h, past):
+@pytest.mark.parametrize("n_pages,max_ctx", [(2, 128), (9, 64)])
+def test_a_refused_row_stores_nothing(n_pages, max_ctx):
+    """Both sequences refused, for want of pages or of entries in the table: the step without a pool over a table
+    that names no page there, or past max_ctx."""
+    h, other = _build(n_seq=2, n_pages=n_pages, max_ctx=max_ctx), _build(n_seq=2, max_ctx=max_ctx)
+    for g in (h, other):
         g.prefill(_x(63, D, 1), 0)
         g.prefill(_x(63, D, 2), 1)
-    run, other = _capture(h, 2), _capture(past, 2)
+    other.table[:, 1:] = -1
+    a, b = _capture(h, 2), _capture(other, 2)
     x = _x(2, D, 3)
-    assert _rel(_replay(*run, x), _replay(*other, x)) <= BOUND
+    assert torch.equal(_replay(*a, x), _replay(*b, x))
     own = _codes(h)
     for i in range(2):
         x = _x(2, D, 4 + i)
-        assert torch.equal(_replay(*run, x), _replay(*other, x))
-        assert h.ctx.tolist() == [64, 64] and h.status.tolist() == [2, 0] and _same(_codes(h), own)
+        other.ctx.fill_(64)                                        # without a pool a step goes on
+        assert torch.equal(_replay(*a, x), _replay(*b, x))
+        assert h.ctx.tolist() == [64, 64] and h.status.tolist() == [2, n_pages - 2] and _same(_codes(h), own)
 
 
 @pytest.mark.parametrize("kw", [dict(), dict(keep_pages=3)])
