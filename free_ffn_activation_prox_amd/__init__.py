@@ -732,7 +732,8 @@ def kv_pages(pool: KVPool, want, n_rows: int, *, parent=None, shared=None, q_sta
     pages, which both then hold.  Returns (q_start [n_seq + 1], slots [n_rows],
     status [2]), int32: the new tokens' rows for a KVBatch of n_rows tokens, each
     row's place 64 * page + slot (-1 behind the last), and how many sequences were
-    refused (they keep their tokens) and how many pages are free."""
+    refused (they keep their tokens and have no rows: a KVBatch without q_start
+    would have one of their last token) and how many pages are free."""
     dev, n = pool.device, (pool.n_seq,)
     if not 0 <= n_rows < 1 << 31:
         raise ValueError("n_rows must be at least 0 and below 2^31")

@@ -13,10 +13,11 @@
 // are whole numbers, and places come from prefix sums.  A page is free where its
 // count is 0, so there is no list to keep in order.
 //
-// What bounds it: latency.  A step of 64 sequences 7.2 us in one block (8.7 with a
+// What bounds it: latency.  A step of 64 sequences 6.9 us in one block (8.7 with a
 // wave for each sequence).  256 sequences of 290 pages in a pool of 131072, half of
-// them ending and half beginning with 256 shared pages: 237 us in one block, in many
-// 30.3 + 4.8 (the last block's numbering about half of it).
+// them ending and half beginning with 256 shared pages, in two launches: 30.6 + 4.9
+// (the last block's numbering about half of it; a form that did it all in one block
+// took 237).
 #include "prox_kv.hpp"
 
 namespace prox {
@@ -416,7 +417,9 @@ hipError_t launch_kv_pages(const prox_kv_pool& p, const int32_t* want, const int
     // One block for a step of a token or two each, where the sequences' lanes do it all (calls back to back): 64
     // sequences 9.5 us, in two launches 13.3; 256 sequences and 65000 pages 10.2 and 14.5; 1024 sequences 11.6 and
     // 15.5.  Two launches where sequences begin or take pages over, which are a wave's work each: 16 sequences that
-    // end or begin with 200 to 500 tokens 13.3 us, in one block 22.4; 64 with 16 shared pages 15.6 and 72.6.
+    // end or begin with 200 to 500 tokens 13.3 us, in one block 22.4; 64 with 16 shared pages 15.6 and 72.6.  The
+    // rule sees neither what is given back nor how long the tables are: 256 sequences of 290 pages that end in a
+    // call of no rows take 179 us in one block, where two launches would take 17.
     if (!parent && n_rows <= 2 * (int64_t)p.n_seq && p.n_seq <= 4096) {
         hipLaunchKernelGGL(k_kv_pages_one, dim3(1), dim3(kPoolThreads), 0, s, A);
         return hipGetLastError();

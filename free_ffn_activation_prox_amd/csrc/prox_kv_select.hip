@@ -14,12 +14,15 @@
 //   fl32(max_h fl32(dot_h unit_h) page_scale).
 //
 // What bounds it (kernel times): bounds of 32768 tokens and 8 heads of 128 channels
-// 9.3 us (34.6 MB, 3.7 TB/s: memory).  Selection is a chain of loads (row, table,
-// bounds) and of steps of one wave: 32 of up to 512 pages for 64 ragged sequences
-// 14.8 us (7.3 MB), for one token 64 of 2048 pages 7.8 + 9.2 us (4.3 MB; in one
-// launch of 8 blocks 31, of which a CU's 30 GB/s take 15), 48 of 250 pages for 1000
-// rows of 28 / 4 heads 24.3 us.  Within a block (stamps of a 64-row case): rows 1.0,
-// table and bounds 2.4, q's codes beside them, product and keys 1.9, selection 1.5.
+// 9.0 us (34.6 MB, 3.8 TB/s: a wave's loads of 4 KB wait for the reduction of the 4 KB
+// before them).  Selection is a chain of loads (row, table, bounds) and of steps of
+// one wave.  32 of up to 512 pages for 64 ragged sequences 14.5 us (7.3 MB): those of
+// the longest rows, which have one block each (stamps: rows and table 0.6, keys of 33
+// to 128 pages 4.1, of 129 to 320 7.6, of more 10.2, none where all pages are kept,
+// selection 1.2 to 1.8).  48 of 250 pages for 1000 rows of 28 / 4 heads 24.0 us, two
+// rounds of blocks of 10.7 (rows 1.7, keys 7.9, selection 1.6).  For one token 64 of
+// 2048 pages 7.9 + 9.3 us (4.3 MB; in one launch of 8 blocks 31, of which a CU's
+// 30 GB/s take 15).
 #include "prox_kv.hpp"
 
 namespace prox {
@@ -714,7 +717,8 @@ hipError_t select_launch(const SelectArgs& A, int64_t units, hipStream_t s) {
 
 template <int NP>
 hipError_t select_np(const SelectArgs& A, int64_t units, hipStream_t s) {
-    // a wave's selection of 2048 keys takes 9.2 us, a block's 10.4
+    // by the table's width: what the rows' lengths are, the host does not see.  A wave's selection of 2048 keys
+    // takes 9.3 us, a block's 10.4
     if (A.row_pages > 2048) return select_launch<NP, 0>(A, units, s);
     if (A.row_pages > 512) return select_launch<NP, 32>(A, units, s);
     return A.row_pages > 256 ? select_launch<NP, 8>(A, units, s) : select_launch<NP, 4>(A, units, s);

@@ -11,8 +11,10 @@
 // do not depend on timing.
 //
 // What bounds it (kernel times): one token, 64 / 8 heads x 128, 64 pages 11.2 us
-// (8.4 MB: latency); 64 ragged sequences, 32 / 8 heads x 128, e4m3, 32 pages 25.6 us
-// (105 MB at 4.1 TB/s: memory); 1000 rows, 28 / 4 heads x 64, 48 pages 133 us: some
+// (8.4 MB: latency); 64 ragged sequences, 32 / 8 heads x 128, e4m3, 32 pages 25.5 us
+// (105 MB; lists of 12.4 pages in the mean and one block each: those of a page or two
+// end after 5.7 us, full ones after 16.7, the last after 24.4, so most CUs are idle in
+// the last third); 1000 rows, 28 / 4 heads x 64, 48 pages 133 us: some
 // 300 vector instructions for each page and wave, codes to fp16 and weights, of
 // whose 16 columns 7 are in use.
 #include "prox_kv_attn.hpp"

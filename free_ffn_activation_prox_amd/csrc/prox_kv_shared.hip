@@ -12,9 +12,14 @@
 //      148 us instead of 60 + 9: 4 MB of parts for one block);
 //   3  the rows of each sequence over its other pages, causal; a row's part of 1
 //      joins before it is normalised and rounded.
-// A page of a prefix is read once for up to 256 rows (32 of each of 8 waves)
-// instead of once for each sequence.  A sequence whose first row lies inside the
-// prefix takes no part in it: launch 3 goes over all of its pages.
+// A page of a prefix is read once for a tile of rows instead of once for each
+// sequence: 256 (32 of each of 8 waves) where the groups have more than 128 rows of
+// a key head in the mean, 128 up to there and for heads wider than 128, 16 where
+// they have no more than 16.  Unlike groups lose by the mean: 63 sequences of 32 / 32
+// heads x 128 over 512 shared pages take 111 us in a call of their own, 7 groups of
+// one such sequence 342, the eight groups in one call 483.
+// A sequence whose first row lies inside the prefix takes no part in it: launch 3
+// goes over all of its pages.
 #include "prox_kv_attn.hpp"
 
 namespace prox {

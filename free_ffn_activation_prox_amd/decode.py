@@ -29,7 +29,7 @@ key head, those whose keys can give the largest scores by the bounds that the
 harness keeps of every page (prompts see all pages).  With n_pages the sequences
 take their pages from a pool of that many instead of each having its own share,
 and may begin with a prompt in common (``share_prefix``): its pages are held once
-and read once a step for all of them.  A sequence for which the pool has no page
+and, where a step sees all pages, read once for all of them.  A sequence for which the pool has no page
 left (``status`` [0] of them at the last step) keeps its tokens: the step's row is
 behind them, where the table names no page, so it sees them and stores nothing
 (past max_ctx it sees nothing either).  The host refuses what the pool cannot hold by its own
@@ -231,7 +231,8 @@ class DecodeHarness:
     def share_prefix(self, x: torch.Tensor) -> torch.Tensor:
         """A prompt that every sequence begins with, x fp32 [tokens][d]: through
         the layers once, as that of sequence 0; the others, which must be empty,
-        begin with its whole pages, and a step reads these once for all.  Returns
+        begin with its whole pages, and a step reads these once for all (with
+        keep_pages, those selected of them for each).  Returns
         what prefill returns; the prompt's tokens behind its last whole page are
         sequence 0's alone."""
         if self.cache == "dense" or self.pool is None:

@@ -452,6 +452,10 @@ size_t prox_kv_pages_workspace_bytes(const prox_kv_pool* p);
  *   slots   [n_rows]     64 * page + slot of each such row, -1 for rows behind the
  *                        last (rows that n_rows leaves no room for are dropped)
  *   status  [2]          sequences refused; free pages left
+ * A refused sequence has no rows in q_start.  In a batch of one token a sequence
+ * (q_start null) it has one all the same: its last token's, which append would
+ * write over, unless the batch's lengths are those wanted (then the row lies in a
+ * page that the table does not name, where it was refused for want of one).
  * parent and shared [n_seq] are both given or both null.  workspace: device, 8-byte
  * aligned, scratch.  Calls on one pool must not overlap in time. */
 prox_status prox_kv_pages(const prox_kv_pool* p, const int32_t* want, const int32_t* parent, const int32_t* shared,
